@@ -26,7 +26,14 @@ EXPORTS = ("bl_tile_stats_elems", "bl_lists_elems", "bl_bwd_workspace_bytes", "b
            "bl_attn_fwd_varlen", "bl_mask_from_stats_varlen", "bl_fwd_workspace_bytes_varlen",
            "bl_attn_fwd_tile_weights_varlen", "bl_mask_from_tile_weights_varlen",
            "bl_attn_bwd_varlen",
-           "bl_varlen_bwd_check_status", "bl_set_wait_limit")
+           "bl_varlen_bwd_check_status", "bl_set_wait_limit",
+           "bl_act_save", "bl_act_load", "bl_rms_norm_fwd", "bl_rms_norm_bwd_workspace_bytes",
+           "bl_rms_norm_bwd", "bl_rope", "bl_attn_bwd_act8_workspace_bytes", "bl_attn_bwd_act8")
+
+# bl_dtype, bl_format8
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+FORMATS8 = {torch.int8: 1, torch.float8_e4m3fn: 2}
+NORM_MAX_COLS = 16384
 
 
 class Shape(ctypes.Structure):
@@ -47,6 +54,24 @@ class Lists(ctypes.Structure):
     _fields_ = [("mask", ctypes.c_void_p), ("kv_idx", ctypes.c_void_p),
                 ("kv_cnt", ctypes.c_void_p), ("q_idx", ctypes.c_void_p),
                 ("q_cnt", ctypes.c_void_p), ("nan_count", ctypes.c_void_p)]
+
+
+class Act8Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("format", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("n", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
+                ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+                ("q_out_strides", ctypes.c_int64 * 3), ("k_out_strides", ctypes.c_int64 * 3),
+                ("positions", ctypes.c_void_p), ("positions_batch_stride", ctypes.c_int64),
+                ("freqs", ctypes.c_void_p)]
 
 
 class VarlenStruct(ctypes.Structure):
@@ -132,6 +157,18 @@ def load():
     lib.bl_varlen_bwd_check_status.restype = ctypes.c_int
     lib.bl_set_wait_limit.argtypes = [D]
     lib.bl_set_wait_limit.restype = D
+    I, L, A = ctypes.c_int, ctypes.c_int64, ctypes.POINTER(Act8Struct)
+    lib.bl_act_save.argtypes = [L, L, I, P, L, A, P]
+    lib.bl_act_load.argtypes = [L, L, I, A, P, P]
+    lib.bl_rms_norm_fwd.argtypes = [L, L, I, P, L, P, L, P, I, F, P, P, P, A, P]
+    lib.bl_rms_norm_bwd_workspace_bytes.argtypes = [L, L]
+    lib.bl_rms_norm_bwd_workspace_bytes.restype = Z
+    lib.bl_rms_norm_bwd.argtypes = [L, L, I, P, P, A, P, P, I, P, P, P, P, Z, P]
+    lib.bl_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+    lib.bl_attn_bwd_act8_workspace_bytes.argtypes = [S]
+    lib.bl_attn_bwd_act8_workspace_bytes.restype = Z
+    lib.bl_attn_bwd_act8.argtypes = [S, A, A, A, P, A, P, P, F, ctypes.POINTER(Lists), P, P, P, P,
+                                     Z, P]
     lib.bl_status_string.argtypes = [ctypes.c_int]
     lib.bl_status_string.restype = ctypes.c_char_p
     _lib = lib

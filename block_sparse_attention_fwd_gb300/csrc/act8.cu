@@ -1,0 +1,211 @@
+// Activations held in 8 bits between the forward and the backward: saving
+// (one scale a group of 32, 64 or 128 elements of a row, or one a row),
+// loading, and the expansion of an attention's q, k and v into its backward's
+// workspace.  The format is in rows.cuh.  All passes are bound by HBM: x once
+// in, one byte an element and the scales out, or the other way round.
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace bl {
+
+namespace {
+
+// Quotient and remainder by a divisor that does not change over a launch, in
+// 32 bits wherever the dividend allows.
+__device__ __forceinline__ void div_mod(int64_t x, int64_t d, int64_t& q, int64_t& r) {
+  if ((uint64_t)x >> 32) {
+    q = x / d;
+    r = x - q * d;
+  } else {
+    const uint32_t qq = (uint32_t)x / (uint32_t)d;
+    q = qq;
+    r = (uint32_t)x - qq * (uint32_t)d;
+  }
+}
+
+// Groups of `a.group` elements: a.group / 8 neighbouring lanes hold one, each
+// lane one chunk.  A row takes a whole number of groups (the last may be cut).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
+  const int lanes = a.group / 8;                    // 4, 8 or 16
+  const int64_t per_row = a.groups * lanes;         // chunks of a row, padded
+  const int64_t total = a.rows * per_row;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t x0 = (int64_t)blockIdx.x * blockDim.x; x0 < total; x0 += stride) {
+    const int64_t x = x0 + threadIdx.x;
+    const bool in = x < total;
+    int64_t row, j;
+    div_mod(in ? x : 0, per_row, row, j);
+    const int64_t col = j * 8;
+    const int64_t left = in ? a.cols - col : 0;
+    const int valid = (int)(left < 8 ? left : 8);
+    const Chunk<T> c = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col, valid);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
+    const float scale = scale_of(lanes_max(amax_bits8(f), lanes), a.fmt);
+    store_codes<VEC>(a.codes + row * a.cols + col, encode8(a.fmt, f, scale), valid);
+    if (in && j % lanes == 0) a.scales[row * a.groups + j / lanes] = scale;
+  }
+}
+
+// One scale a row: a warp (BLOCK: a block) goes over its row twice, for the
+// maximum and for the codes; the second reading comes from the caches.
+template <typename T, bool VEC, bool BLOCK>
+__global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
+  __shared__ uint32_t buf[2][32];
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  const int step = BLOCK ? 256 : 32;
+  const int rows_here = BLOCK ? 1 : 8;
+  int slot = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * rows_here) {
+    const int64_t row = row0 + (BLOCK ? 0 : threadIdx.x >> 5);
+    const int64_t cols = row < a.rows ? a.cols : 0;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    uint32_t m = 0;
+    for (int64_t col = t * 8; col < cols; col += step * 8) {
+      const int valid = (int)min((int64_t)8, cols - col);
+      const Chunk<T> c = load8<T, VEC>(x + col, valid);
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
+      m = max(m, amax_bits8(f));
+    }
+    if constexpr (BLOCK) {
+      m = block_max(m, buf, slot);
+      slot ^= 1;
+    } else {
+      __syncwarp();
+      m = lanes_max(m, 32);
+    }
+    const float scale = scale_of(m, a.fmt);
+    for (int64_t col = t * 8; col < cols; col += step * 8) {
+      const int valid = (int)min((int64_t)8, cols - col);
+      const Chunk<T> c = load8<T, VEC>(x + col, valid);
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
+      store_codes<VEC>(a.codes + row * a.cols + col, encode8(a.fmt, f, scale), valid);
+    }
+    if (t == 0 && row < a.rows) a.scales[row] = scale;
+  }
+}
+
+template <typename T, bool VEC, int FMT>
+__global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
+  const int64_t per_row = (a.cols + 7) / 8;
+  const int64_t total = a.rows * per_row;
+  const int shift = a.group ? __ffs(a.group) - 1 : 62;
+  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < total;
+       x += (int64_t)gridDim.x * blockDim.x) {
+    int64_t row, j;
+    div_mod(x, per_row, row, j);
+    const int64_t col = j * 8;
+    const int valid = (int)min((int64_t)8, a.cols - col);
+    const Codes c = load_codes<VEC>(a.codes + row * a.cols + col, valid);
+    const float scale = a.scales[row * a.groups + (col >> shift)];
+    float f[8];
+    decode8<FMT>(c, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= scale;
+    store8<T, VEC>(static_cast<T*>(a.x) + row * a.cols + col, f, valid);
+  }
+}
+
+// q, k and v of an attention, [tokens, heads, D] codes with one scale a
+// (token, head), to bf16.  16 codes a thread; the blocks of the three tensors
+// follow one another.
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) expand_kernel(Expand a) {
+  int s = 0;
+  int64_t blk = blockIdx.x;
+  while (s < 2 && blk >= a.blocks[s]) blk -= a.blocks[s++];
+  const int64_t x = blk * 256 + threadIdx.x;          // 16 elements
+  constexpr int PER_ROW = D / 16;
+  if (x >= a.rows[s] * PER_ROW) return;
+  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(a.codes[s]) + x);
+  const float scale = __ldg(a.scales[s] + x / PER_ROW);
+  const Codes c[2] = {{{raw.x, raw.y}}, {{raw.z, raw.w}}};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    float f[8];
+    decode8<FMT>(c[u], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= scale;
+    store8<__nv_bfloat16, true>(static_cast<__nv_bfloat16*>(a.out[s]) + x * 16 + u * 8, f, 8);
+  }
+}
+
+constexpr int64_t kMaxBlocks = 152 * 64;
+
+unsigned blocks_for(int64_t units) {
+  return (unsigned)(units < kMaxBlocks ? units : kMaxBlocks);
+}
+
+}  // namespace
+
+cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
+  ActSave a = in;
+  if (a.rows == 0) return cudaSuccess;
+  // one scale a row of 32, 64 or 128 elements is one scale a group
+  if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
+                     aligned_to(a.codes, 8);
+    if (a.group) {
+      const int64_t units = (a.rows * a.groups * (a.group / 8) + 255) / 256;
+      if (vec)
+        act_save_groups_kernel<T, true><<<blocks_for(units), 256, 0, st>>>(a);
+      else
+        act_save_groups_kernel<T, false><<<blocks_for(units), 256, 0, st>>>(a);
+    } else if (a.cols <= 1024) {
+      if (vec)
+        act_save_rows_kernel<T, true, false><<<blocks_for((a.rows + 7) / 8), 256, 0, st>>>(a);
+      else
+        act_save_rows_kernel<T, false, false><<<blocks_for((a.rows + 7) / 8), 256, 0, st>>>(a);
+    } else {
+      if (vec)
+        act_save_rows_kernel<T, true, true><<<blocks_for(a.rows), 256, 0, st>>>(a);
+      else
+        act_save_rows_kernel<T, false, true><<<blocks_for(a.rows), 256, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_act_load(int dtype, const ActLoad& a, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.codes, 8);
+    const unsigned g = blocks_for((a.rows * ((a.cols + 7) / 8) + 255) / 256);
+    if (a.fmt == kFmtInt8)
+      vec ? act_load_kernel<T, true, kFmtInt8><<<g, 256, 0, st>>>(a)
+          : act_load_kernel<T, false, kFmtInt8><<<g, 256, 0, st>>>(a);
+    else
+      vec ? act_load_kernel<T, true, kFmtE4m3><<<g, 256, 0, st>>>(a)
+          : act_load_kernel<T, false, kFmtE4m3><<<g, 256, 0, st>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_expand(int d, int fmt, const Expand& in, cudaStream_t st) {
+  Expand a = in;
+  int64_t blocks = 0;
+  for (int s = 0; s < 3; ++s) {
+    a.blocks[s] = (a.rows[s] * (d / 16) + 255) / 256;
+    blocks += a.blocks[s];
+  }
+  const unsigned g = (unsigned)blocks;
+  if (d == 64)
+    fmt == kFmtInt8 ? expand_kernel<64, kFmtInt8><<<g, 256, 0, st>>>(a)
+                    : expand_kernel<64, kFmtE4m3><<<g, 256, 0, st>>>(a);
+  else
+    fmt == kFmtInt8 ? expand_kernel<128, kFmtInt8><<<g, 256, 0, st>>>(a)
+                    : expand_kernel<128, kFmtE4m3><<<g, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace bl

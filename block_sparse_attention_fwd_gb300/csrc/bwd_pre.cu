@@ -11,6 +11,7 @@
 // rounds to bf16.
 #include "common.cuh"
 #include "kernels.h"
+#include "rows.cuh"
 
 namespace bl {
 
@@ -24,12 +25,16 @@ namespace {
 // values with one coalesced store.  The warp also zeroes its rows of the fp32
 // dQ accumulator, and block 0 the status word and the word after it (the
 // tcgen05 backward's work-item counter), so no separate memset pass is needed.
-template <int D>
+// FMT != 0: O comes as 8-bit codes ([B,n,H,D], one scale a row) and is never
+// expanded; the row's scale multiplies the finished sum of products.
+template <int D, int FMT>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __restrict__ o,
                                                       const __nv_bfloat16* __restrict__ g_o,
                                                       float* __restrict__ Dv,
                                                       float* __restrict__ dq_acc,
-                                                      int32_t* __restrict__ status, Shape sh) {
+                                                      int32_t* __restrict__ status, Shape sh,
+                                                      const uint8_t* __restrict__ o_codes,
+                                                      const float* __restrict__ o_scales) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPS = 32 / LPR;     // rows per step
   constexpr int STEPS = 32 / RPS;
@@ -58,7 +63,13 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
       gv[u] = ov[u];
       if (r < sh.n) {
         const int64_t off = bshd(sh.os, b, r, h) + c8;
-        ov[u] = *reinterpret_cast<const uint4*>(o + off);
+        if constexpr (FMT == 0) {
+          ov[u] = *reinterpret_cast<const uint4*>(o + off);
+        } else {
+          const int64_t orow = ((int64_t)b * sh.n + r) * sh.H + h;
+          const uint2 c = *reinterpret_cast<const uint2*>(o_codes + orow * D + c8);
+          ov[u] = make_uint4(c.x, c.y, __float_as_uint(o_scales[orow]), 0u);
+        }
         gv[u] = *reinterpret_cast<const uint4*>(g_o + off);
       }
     }
@@ -67,13 +78,20 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
       const uint32_t* a = reinterpret_cast<const uint32_t*>(&ov[u]);
       const uint32_t* c = reinterpret_cast<const uint32_t*>(&gv[u]);
       float acc = 0.f;
+      float oc[8];
+      if constexpr (FMT != 0) decode8<FMT>(Codes{{ov[u].x, ov[u].y}}, oc);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a[e]));
+        float2 x;
+        if constexpr (FMT == 0)
+          x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&a[e]));
+        else
+          x = make_float2(oc[2 * e], oc[2 * e + 1]);
         const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&c[e]));
         acc = fmaf(x.x, y.x, acc);
         acc = fmaf(x.y, y.y, acc);
       }
+      if constexpr (FMT != 0) acc *= __uint_as_float(ov[u].z);
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
       // row (s0 + u) * RPS + i sits in lanes i * LPR ...; lane l takes row l
@@ -118,22 +136,43 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float4* __restric
 
 }  // namespace
 
+namespace {
+
+template <int D, int FMT>
+void launch_pre(const Shape& sh, const void* o, const uint8_t* o_codes, const float* o_scales,
+                const void* g_o, float* ws_D, float* ws_dq, int32_t* ws_status, cudaStream_t st) {
+  const int64_t warps = (int64_t)sh.B * ((sh.n + 31) / 32) * sh.H;
+  bwd_pre_kernel<D, FMT><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(
+      (const __nv_bfloat16*)o, (const __nv_bfloat16*)g_o, ws_D, ws_dq, ws_status, sh, o_codes,
+      o_scales);
+}
+
+}  // namespace
+
 cudaError_t launch_bwd(const Shape& sh, const void* q, const void* k, const void* v,
                        const void* o, const void* g_o, const float* lse, float scale,
                        const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
                        void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
                        int32_t* ws_status, cudaStream_t st) {
+  return launch_bwd_act8(sh, q, k, v, o, nullptr, nullptr, 0, g_o, lse, scale, q_idx, q_cnt, g_q,
+                         g_k, g_v, ws_D, ws_dq, ws_sub, ws_status, st);
+}
+
+cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const void* v,
+                            const void* o, const uint8_t* o_codes, const float* o_scales,
+                            int o_fmt, const void* g_o, const float* lse, float scale,
+                            const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
+                            void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
+                            int32_t* ws_status, cudaStream_t st) {
   const int64_t rows = (int64_t)sh.B * sh.n * sh.H;
-  const int64_t pre_warps = (int64_t)sh.B * ((sh.n + 31) / 32) * sh.H;
-  unsigned pre_blocks = (unsigned)((pre_warps + 7) / 8);
-  if (sh.d == 64)
-    bwd_pre_kernel<64><<<pre_blocks, 256, 0, st>>>((const __nv_bfloat16*)o,
-                                                   (const __nv_bfloat16*)g_o, ws_D, ws_dq,
-                                                   ws_status, sh);
-  else
-    bwd_pre_kernel<128><<<pre_blocks, 256, 0, st>>>((const __nv_bfloat16*)o,
-                                                    (const __nv_bfloat16*)g_o, ws_D, ws_dq,
-                                                    ws_status, sh);
+  const int fmt = o_codes ? o_fmt : 0;
+  auto pre = sh.d == 64 ? (fmt == 0          ? launch_pre<64, 0>
+                           : fmt == kFmtInt8 ? launch_pre<64, kFmtInt8>
+                                             : launch_pre<64, kFmtE4m3>)
+                        : (fmt == 0          ? launch_pre<128, 0>
+                           : fmt == kFmtInt8 ? launch_pre<128, kFmtInt8>
+                                             : launch_pre<128, kFmtE4m3>);
+  pre(sh, o, o_codes, o_scales, g_o, ws_D, ws_dq, ws_status, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_bwd_tc(sh, q, k, v, g_o, lse, ws_D, q_idx, q_cnt, g_k, g_v, ws_dq, ws_sub, ws_status,

@@ -67,6 +67,86 @@ cudaError_t launch_grad_error(const void* a, const void* b, int64_t n, double* o
 cudaError_t launch_combine(int parts, int B, int n, int H, int d, const void* o_parts,
                            const float* lse_parts, void* o, float* lse, cudaStream_t st);
 
+// Rows of a root-mean-square norm (norm.cu).  Strides in elements; y, h, g_y,
+// g_x, g_h and codes are contiguous [rows, cols].
+struct NormFwd {
+  int64_t rows, cols, x_stride, r_stride, groups;
+  const void *x, *r, *w;          // r: residual or null; w: weight or null (ones)
+  void *y, *h;                    // y or codes may be null; h only with r
+  float* rstd;
+  uint8_t* codes;                 // 8-bit output, with scales [rows, groups]
+  float* scales;
+  float eps;
+  int group, fmt;
+  bool w_f32;                     // the weight is fp32, whatever x is
+};
+struct NormBwd {
+  int64_t rows, cols, groups;
+  const void *g_y, *h, *w, *g_h;  // h null: codes and scales
+  const uint8_t* codes;
+  const float *scales, *rstd;
+  void* g_x;
+  float* partial;                 // [norm_bwd_parts, cols], or null without g_w
+  int group, fmt;
+  bool w_f32;
+};
+cudaError_t launch_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st);
+// Partial rows of g_w that the backward writes.
+int norm_bwd_parts(int64_t rows, int64_t cols);
+cudaError_t launch_norm_bwd(int dtype, const NormBwd& a, void* g_w, cudaStream_t st);
+
+// 8-bit activations (act8.cu).
+struct ActSave {
+  int64_t rows, cols, x_stride, groups;
+  const void* x;
+  uint8_t* codes;
+  float* scales;
+  int group, fmt;
+};
+struct ActLoad {
+  int64_t rows, cols, groups;
+  const uint8_t* codes;
+  const float* scales;
+  void* x;
+  int group, fmt;
+};
+cudaError_t launch_act_save(int dtype, const ActSave& a, cudaStream_t st);
+cudaError_t launch_act_load(int dtype, const ActLoad& a, cudaStream_t st);
+// Codes of up to three tensors [rows, d] with one scale a row, to bf16.
+struct Expand {
+  const uint8_t* codes[3];
+  const float* scales[3];
+  void* out[3];
+  int64_t rows[3], blocks[3];
+};
+cudaError_t launch_expand(int d, int fmt, const Expand& a, cudaStream_t st);
+
+// The backward whose q, k and v have been expanded into bf16 and whose o is
+// either bf16 (o_codes null) or codes with one scale a (token, head).
+cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const void* v,
+                            const void* o, const uint8_t* o_codes, const float* o_scales,
+                            int o_fmt, const void* g_o, const float* lse, float scale,
+                            const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
+                            void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
+                            int32_t* ws_status, cudaStream_t st);
+
+// Rotary positions (rope.cu).  Strides {batch, token, head} in elements.
+struct Rope {
+  int B, n, H, Hk, d, pairs, axes;
+  int ends[3];                    // first pair of axes 1, 2, 3 (pairs where there is none)
+  bool half, inverse, copy;       // copy: the dims behind 2 * pairs too
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t qs[3], ks[3], qos[3], kos[3];
+  const int32_t* pos;             // [B or 1, n, axes]
+  int64_t pos_batch;              // 0: shared by the batches
+  const uint64_t* freqs;          // [pairs], turns in 64-bit fixed point
+  int lanes;                      // set by the launch
+  uint32_t q_units, k_units;
+  int64_t units;
+};
+cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st);
+
 // 4-D TMA map of a BSHD bf16 tensor [B][n][heads][d] with element strides
 // st = {batch, seq, head} (d contiguous): box of 64 elements of d x 1 head x
 // `rows` tokens x 1 batch, 128-byte swizzle, out-of-range reads 0.

@@ -1,0 +1,254 @@
+// Rows of a matrix in chunks of 8 consecutive elements, the unit that the row
+// kernels (norm.cu, act8.cu) load, keep in registers and store: 16 bytes of
+// a 16-bit type, 32 of fp32, 8 of codes.  With VEC a chunk is whole and
+// aligned and moves in one or two vector instructions; otherwise element by
+// element under a count of valid elements (odd widths, views whose rows start
+// anywhere).
+//
+// Also the 8-bit format: a group of consecutive elements of a row shares one
+// fp32 scale,
+//   scale = max(amax / qmax, 2^-126),   qmax = 127 (int8) or 448 (e4m3),
+//   code  = round to nearest even of fl32(x * fl32(1 / scale)),
+//   value = code * scale.
+// The lower bound keeps 1 / scale finite, so an all-zero group needs no case
+// of its own.  A NaN or an infinity in the group makes the scale NaN (codes
+// 0): the whole group loads as NaN instead of as a wrong number.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace bl {
+
+constexpr int kFmtInt8 = 1, kFmtE4m3 = 2;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+template <typename T>
+struct alignas(16) Chunk {
+  T e[8];
+};
+struct alignas(8) Codes {
+  uint32_t w[2];
+};
+
+// 8 elements at p, of which `valid` exist (the others read as zero).
+template <typename T, bool VEC>
+__device__ __forceinline__ Chunk<T> load8(const T* __restrict__ p, int valid) {
+  Chunk<T> c;
+  constexpr int NW = sizeof(Chunk<T>) / 16;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      reinterpret_cast<uint4*>(&c)[i] =
+          valid > 0 ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c.e[i] = i < valid ? p[i] : from_f32<T>(0.f);
+  }
+  return c;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], int valid) {
+  Chunk<T> c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c.e[i] = from_f32<T>(f[i]);
+  constexpr int NW = sizeof(Chunk<T>) / 16;
+  if constexpr (VEC) {
+    if (valid > 0) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i)
+        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&c)[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = c.e[i];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ Codes load_codes(const uint8_t* __restrict__ p, int valid) {
+  Codes c{{0u, 0u}};
+  if constexpr (VEC) {
+    if (valid > 0) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      c.w[0] = v.x;
+      c.w[1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) c.w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+  }
+  return c;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, Codes c, int valid) {
+  if constexpr (VEC) {
+    if (valid > 0) *reinterpret_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = (uint8_t)(c.w[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+// Codes as floats (without the scale).  int8: the byte with its sign bit
+// flipped is placed in the low mantissa bits of 2^23, so one add takes off
+// 2^23 + 128 and leaves the exact integer; that is full-rate arithmetic where
+// an integer-to-float conversion is not.
+template <int FMT>
+__device__ __forceinline__ void decode8(const Codes& c, float (&f)[8]) {
+  if constexpr (FMT == kFmtInt8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t flipped = c.w[i / 4] ^ 0x80808080u;
+      const uint32_t bits = __byte_perm(flipped, 0x4b000000u, 0x7650 + (i % 4));
+      f[i] = __uint_as_float(bits) - 8388736.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t two = (uint16_t)(c.w[i / 2] >> (16 * (i % 2)));
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+}
+
+// Largest magnitude of 8 values as bits: of non-negative floats the integer
+// order is the numeric one, with infinity and then every NaN on top, so a
+// maximum of bits lets no NaN slip through.
+__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  return m;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t amax_bits, int fmt) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
+  const float s = __fdiv_rn(__uint_as_float(amax_bits), fmt == kFmtInt8 ? 127.f : 448.f);
+  return fmaxf(s, 1.17549435e-38f);
+}
+
+// The codes of 8 values of a group with this scale.  |x / scale| stays below
+// qmax (1 + 2^-22), which rounds to qmax, so nothing is clamped.  int8: adding
+// 1.5 * 2^23 rounds to an integer (ties to even) and leaves its two's
+// complement in the low mantissa byte.
+template <int FMT>
+__device__ __forceinline__ Codes encode8(const float (&f)[8], float scale) {
+  Codes c{{0u, 0u}};
+  if (isnan(scale)) return c;
+  const float inv = __frcp_rn(scale);
+  if constexpr (FMT == kFmtInt8) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      b[i] = __float_as_uint(__fadd_rn(__fmul_rn(f[i], inv), 12582912.f));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      c.w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                           __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv));
+      c.w[i / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)
+                    << (16 * (i % 2));
+    }
+  }
+  return c;
+}
+
+__device__ __forceinline__ Codes encode8(int fmt, const float (&f)[8], float scale) {
+  return fmt == kFmtInt8 ? encode8<kFmtInt8>(f, scale) : encode8<kFmtE4m3>(f, scale);
+}
+__device__ __forceinline__ void decode8(int fmt, const Codes& c, float (&f)[8]) {
+  if (fmt == kFmtInt8)
+    decode8<kFmtInt8>(c, f);
+  else
+    decode8<kFmtE4m3>(c, f);
+}
+
+// Maximum over `width` neighbouring lanes (a power of two up to 32).
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum (maximum) over the block: warp partials through one of two slots of
+// `buf` (uint32 [2][32]), which the caller alternates, so that one barrier a
+// reduction is enough: a slot is written again only after the barrier of the
+// reduction in between.  Every thread gets the result, added in the same order.
+__device__ __forceinline__ float block_sum(float v, uint32_t (*buf)[32], int slot) {
+  v = lanes_sum(v, 32);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) buf[slot][warp] = __float_as_uint(v);
+  __syncthreads();
+  return lanes_sum(lane < warps ? __uint_as_float(buf[slot][lane]) : 0.f, 32);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t (*buf)[32], int slot) {
+  v = lanes_max(v, 32);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) buf[slot][warp] = v;
+  __syncthreads();
+  return lanes_max(lane < warps ? buf[slot][lane] : 0u, 32);
+}
+
+// A weight row of type T or fp32 (or none: ones).
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_weight8(const void* w, bool f32, int64_t col, int valid,
+                                             float (&f)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  } else if (f32) {
+    const Chunk<float> c = load8<float, VEC>(static_cast<const float*>(w) + col, valid);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c.e[i];
+  } else {
+    const Chunk<T> c = load8<T, VEC>(static_cast<const T*>(w) + col, valid);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
+  }
+}
+
+inline bool aligned_to(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Calls f with a null pointer of the element type that `dtype` (BL_BF16,
+// BL_FP16, BL_FP32) names.
+template <typename F>
+cudaError_t with_type(int dtype, F&& f) {
+  if (dtype == 0) return f((__nv_bfloat16*)nullptr);
+  if (dtype == 1) return f((__half*)nullptr);
+  return f((float*)nullptr);
+}
+
+inline int64_t groups_of(int64_t cols, int group) {
+  return group ? (cols + group - 1) / group : 1;
+}
+
+}  // namespace bl

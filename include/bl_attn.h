@@ -287,6 +287,134 @@ bl_status bl_attn_bwd_noalloc(const bl_shape* shape, const void* q, const void* 
 bl_status bl_bwd_noalloc_check_status(const bl_shape* shape, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Around the attention: rotary positions, the root-mean-square norm with the
+ * residual's addition, and activations held in 8 bits until the backward.
+ * (The BackLite pages have no counterpart: these are the steps a training
+ * block runs directly before the attention, and what it keeps meanwhile.)
+ *
+ * Rows.  The norm and the 8-bit calls see a tensor as [rows, cols] with a
+ * contiguous last dim; a row stride (in elements, >= cols) is taken where an
+ * argument gives one, every other tensor is contiguous.  rows = 0 is allowed
+ * and reads and writes no row.  Pointers need the alignment of their element
+ * only; 16-byte aligned rows of a multiple of 8 elements run on vector loads.
+ * Outputs must not overlap inputs unless a call says so.
+ * ------------------------------------------------------------------------- */
+typedef enum { BL_BF16 = 0, BL_FP16 = 1, BL_FP32 = 2 } bl_dtype;
+typedef enum { BL_INT8 = 1, BL_E4M3 = 2 } bl_format8;
+
+/* A [rows, cols] tensor in 8 bits: one fp32 scale for every `group`
+ * consecutive elements of a row (32, 64 or 128; the last group of a row may
+ * be cut), or one a row (group = 0).
+ *   scale = max(amax / qmax, 2^-126), qmax = 127 (int8) or 448 (e4m3)
+ *   code  = round to nearest even of fl32(x * fl32(1 / scale))
+ *   value = code * scale
+ * A group that holds a NaN or an infinity gets the scale NaN and loads as NaN.
+ *   codes  [rows, cols]  int8 or e4m3, contiguous
+ *   scales [rows, ceil(cols / group)] fp32 ([rows] with group = 0) */
+typedef struct {
+  void* codes;
+  float* scales;
+  int format;               /* bl_format8 */
+  int group;
+} bl_act8;
+
+/* x [rows, cols] (dtype, row stride x_stride) into codes and scales.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
+bl_status bl_act_save(int64_t rows, int64_t cols, int dtype, const void* x, int64_t x_stride,
+                      const bl_act8* out, void* stream);
+
+/* The values of codes and scales, rounded to dtype, into x [rows, cols]
+ * (contiguous).  Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
+bl_status bl_act_load(int64_t rows, int64_t cols, int dtype, const bl_act8* in, void* x,
+                      void* stream);
+
+/* Largest number of columns of the norm. */
+#define BL_NORM_MAX_COLS 16384
+
+/* h = x + residual (h = x without one), rstd = 1 / sqrt(mean(h^2) + eps),
+ * y = h * rstd * weight, row by row.
+ *   x, residual   [rows, cols] of dtype, row strides x_stride, residual_stride;
+ *                 residual may be NULL.
+ *   weight        [cols] of weight_dtype (dtype or BL_FP32), or NULL: ones.
+ *   y             [rows, cols] of dtype, or NULL when y8 is given.
+ *   h             [rows, cols] of dtype, h rounded: the residual stream behind
+ *                 the addition.  May be NULL; NULL without a residual.
+ *   rstd          [rows] fp32, for the backward; may be NULL.
+ *   y8            y in 8 bits (from y before its rounding to dtype), beside y
+ *                 or in its place; may be NULL.
+ * y and y8 come from the unrounded h.  eps >= 0, cols <= BL_NORM_MAX_COLS.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED (cols), BL_ERR_CUDA. */
+bl_status bl_rms_norm_fwd(int64_t rows, int64_t cols, int dtype, const void* x, int64_t x_stride,
+                          const void* residual, int64_t residual_stride, const void* weight,
+                          int weight_dtype, float eps, void* y, void* h, float* rstd,
+                          const bl_act8* y8, void* stream);
+
+/* Bytes of device workspace bl_rms_norm_bwd needs when it forms g_w (16-byte
+ * aligned base; the call initialises it). */
+size_t bl_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Gradients of bl_rms_norm_fwd.  With u = h rstd and c = mean(weight g_y u):
+ *   g_x = rstd (weight g_y - u c) + g_h     (of x and of the residual alike)
+ *   g_w = sum over the rows of g_y u        (in a fixed order: reproducible)
+ *   g_y, g_h, g_x [rows, cols] of dtype; g_h, the gradient that reaches h along
+ *                 the residual stream, may be NULL.
+ *   h, h8         h as the forward wrote it (x without a residual), or its
+ *                 8-bit checkpoint, which is read as it is: exactly one of both.
+ *   rstd          [rows] fp32 from the forward.
+ *   g_w           [cols] of weight_dtype, or NULL; then no workspace is needed.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED, BL_ERR_WORKSPACE, BL_ERR_CUDA. */
+bl_status bl_rms_norm_bwd(int64_t rows, int64_t cols, int dtype, const void* g_y, const void* h,
+                          const bl_act8* h8, const float* rstd, const void* weight,
+                          int weight_dtype, const void* g_h, void* g_x, void* g_w,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions with up to four axes (one: the ordinary rotation; three:
+ * time, height and width of a video grid), on q and k in one launch.
+ * The first 2 * pairs dimensions of every head turn in pairs, the others pass
+ * through.  The pairs are dealt to the axes in consecutive sections
+ * (sections[0..axes) >= 1, their sum is `pairs`); pair p of axis a turns by
+ * positions[token][a] * f_p:
+ *   (u, v) -> (u cos - v sin, u sin + v cos),
+ *   (u, v) = (x[2p], x[2p+1]) with interleaved = 1, (x[p], x[p+pairs]) with 0.
+ * inverse = 1 turns back: applied to the gradients of the outputs it gives
+ * those of the inputs.
+ *   q, q_out  [B, n, H, d] of dtype, k, k_out [B, n, Hk, d]; Hk = 0: no k.
+ *             Element strides {batch, token, head}, the dim stride is 1.
+ *             q_out may be q itself (with the same strides), likewise k_out.
+ *   positions [B, n, axes] int32, contiguous; the batches are
+ *             positions_batch_stride elements apart (0: all share the first).
+ *   freqs     [pairs] uint64 on the device: round(f_p / (2 pi) * 2^64) modulo
+ *             2^64, f_p in radians a position.
+ * 1 <= pairs <= d / 2.  Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
+typedef struct {
+  int B, n, H, Hk, d, pairs, axes;
+  int sections[4];
+  int interleaved, inverse, dtype;
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+  const int32_t* positions;
+  int64_t positions_batch_stride;
+  const uint64_t* freqs;
+} bl_rope_args;
+bl_status bl_rope(const bl_rope_args* args, void* stream);
+
+/* bl_attn_bwd from an 8-bit checkpoint: q, k and v come as codes with one
+ * scale a (token, head) (group 0 over rows of d: q8->codes [B,n,H,d],
+ * q8->scales [B,n,H]) and stand for their values rounded to bf16; o comes
+ * either in bf16 (o) or as codes (o8), exactly one of both.  All codes have
+ * the same format.  Contiguous tensors only (zero strides in the shape).
+ * The workspace begins with bl_attn_bwd's, so bl_bwd_check_status reads it. */
+size_t bl_attn_bwd_act8_workspace_bytes(const bl_shape* shape);
+bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_act8* k8,
+                           const bl_act8* v8, const void* o, const bl_act8* o8, const void* g_o,
+                           const float* lse, float scale, const bl_lists* lists, void* g_q,
+                           void* g_k, void* g_v, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
  * Packed variable-length batches.
  *
  * nseq sequences of lengths n_s = cu_seqlens[s+1] - cu_seqlens[s] are packed
