@@ -8,7 +8,9 @@ to such a target as training goes.  ``calibrate_negl_prob`` does that for one
 batch: it runs the forward with tile statistics and the dense backward once,
 then mask + sparse backward for every candidate negl_prob, measures the three
 gradients against the dense ones (``bl_grad_error``), and returns the largest
-candidate whose worst gradient meets the target.
+candidate whose worst gradient meets the target.  With ``checkpoint`` the
+candidates' backward reads q, k and v (and o) from 8 bits, as
+``BLAttention(checkpoint=...)`` does, so the errors hold both roundings.
 
 Every step runs in libbl_attn.so; this module orders the calls and applies
 the selection rule (``select_negl``), which is plain host logic.
@@ -19,7 +21,7 @@ import dataclasses
 
 import torch
 
-from . import _lib
+from . import _lib, ops
 
 
 @dataclasses.dataclass
@@ -49,7 +51,8 @@ def select_negl(trials, max_rel_l2: float = 0.1, min_cos: float = 0.99):
 
 def calibrate_negl_prob(q, k, v, g_o, *, candidates=(0.005, 0.01, 0.02, 0.05, 0.1, 0.2),
                         max_rel_l2: float = 0.1, min_cos: float = 0.99, scale=None,
-                        block: int = 128, causal: bool = False, window: int = 0):
+                        block: int = 128, causal: bool = False, window: int = 0,
+                        checkpoint: str | None = None, checkpoint_out: bool = False):
     """Returns (negl_prob, trials) for bf16 device tensors q, g_o [B,n,H,d] and
     k, v [B,n,Hk,d]."""
     B, n, H, d = q.shape
@@ -74,9 +77,15 @@ def calibrate_negl_prob(q, k, v, g_o, *, candidates=(0.005, 0.01, 0.02, 0.05, 0.
     nonempty = float(dense_lists["mask"].sum())
     out = torch.empty(4, dtype=torch.float64, device=dev)
     trials = []
+    if checkpoint is not None:
+        q8, k8, v8 = (ops.act_save(t, checkpoint) for t in (q, k, v))
+        o8 = ops.act_save(o, checkpoint) if checkpoint_out else o
     for negl in sorted(candidates):
         _lib.mask_from_stats(shape, stats, lse, float(negl), lists)
-        _lib.attn_bwd(shape, q, k, v, o, g_o, lse, scale, lists, *got, ws)
+        if checkpoint is not None:
+            got = ops.attn_bwd_act8(shape, q8, k8, v8, o8, g_o, lse, scale, lists)
+        else:
+            _lib.attn_bwd(shape, q, k, v, o, g_o, lse, scale, lists, *got, ws)
         rel, cos = {}, {}
         for name, a, b in zip(("G_Q", "G_K", "G_V"), got, ref):
             rel[name], cos[name] = _lib.grad_error(a, b, out)

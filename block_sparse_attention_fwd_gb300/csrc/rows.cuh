@@ -11,7 +11,8 @@
 //   code  = round to nearest even of fl32(x * fl32(1 / scale)),
 //   value = code * scale.
 // The lower bound keeps 1 / scale finite, so an all-zero group needs no case
-// of its own.  A NaN or an infinity in the group makes the scale NaN (codes
+// of its own; where scale * qmax would round past the largest fp32 number the
+// scale is one step lower.  A NaN or an infinity in the group makes the scale NaN (codes
 // 0): the whole group loads as NaN instead of as a wrong number.
 #pragma once
 
@@ -144,8 +145,10 @@ __device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8]) {
 
 __device__ __forceinline__ float scale_of(uint32_t amax_bits, int fmt) {
   if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
-  const float s = __fdiv_rn(__uint_as_float(amax_bits), fmt == kFmtInt8 ? 127.f : 448.f);
-  return fmaxf(s, 1.17549435e-38f);
+  const float qmax = fmt == kFmtInt8 ? 127.f : 448.f;
+  float s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits), qmax), 1.17549435e-38f);
+  if (isinf(__fmul_rn(s, qmax))) s = __uint_as_float(__float_as_uint(s) - 1u);
+  return s;
 }
 
 // The codes of 8 values of a group with this scale.  |x / scale| stays below

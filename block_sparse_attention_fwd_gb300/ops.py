@@ -45,33 +45,40 @@ def _tensor(t, name, device=None, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t, name):
-    """(rows, cols, row stride) of a tensor whose leading dims make one run of
-    equally spaced rows with a contiguous last dim."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _lib.DTYPES:
-        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name} needs a last dim of at least one element")
+def row_stride(t):
+    """Stride of the rows of the last dim, if they are equally spaced and each
+    is contiguous; None where the tensor is no such run of rows."""
     cols = t.shape[-1]
-    rows = t.numel() // cols
     if t.is_contiguous():
-        return rows, cols, cols
-    stride = None
-    run = 1                     # rows covered by the dims behind
+        return cols
+    if cols > 1 and t.stride(-1) != 1:
+        return None
+    stride, run = None, 1                   # run: rows covered by the dims behind
     for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if stride is None:
             stride = st
         elif st != stride * run:
-            stride = -1
+            return None
         run *= size
-    if (cols > 1 and t.stride(-1) != 1) or (stride is not None and stride < cols):
-        raise ValueError(f"{name} with strides {t.stride()} is not a run of rows: "
-                         "pass name.contiguous()".replace("name", name))
-    return rows, cols, cols if stride is None else stride
+    if stride is None:
+        return cols
+    return stride if stride >= cols else None
+
+
+def _rows(t, name):
+    """(rows, cols, row stride) of a tensor argument."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _lib.DTYPES:
+        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} needs a last dim of at least one element")
+    stride = row_stride(t)
+    if stride is None:
+        raise ValueError(f"{name} with strides {tuple(t.stride())} is not a run of rows")
+    return t.numel() // t.shape[-1], t.shape[-1], stride
 
 
 # --- activations in 8 bits -----------------------------------------------------

@@ -7,5 +7,6 @@ code with the CUDA path.
 * ``attention``  -- exact forward, per-tile LSE statistics, masked backward.
 * ``mask_spec``  -- the canonical tile-selection rule (mask_from_stats).
 * ``varlen``     -- the three steps over packed variable-length batches.
+* ``block``      -- rotary positions, the residual norm and 8-bit activations.
 """
-from . import attention, mask_spec, varlen  # noqa: F401
+from . import attention, block, mask_spec, varlen  # noqa: F401

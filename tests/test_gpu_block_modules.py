@@ -1,0 +1,377 @@
+"""The modules around the attention: gradients against the formula and against
+differences, a block of them together, other streams, CUDA graphs."""
+import numpy as np
+import pytest
+import torch
+
+from tests import parity_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__ as g
+    g.build()
+
+
+@pytest.fixture(scope="module")
+def bl():
+    import block_sparse_attention_fwd_gb300 as bl
+    return bl
+
+
+def _randn(*shape, dtype=torch.float32, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+# --- plain fp64 forms ----------------------------------------------------------------
+
+def _norm64(x, w, eps=1e-6):
+    return x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w
+
+
+def _rope64(x, pos, plan):
+    axis = torch.repeat_interleave(torch.arange(len(plan.sections)), torch.tensor(plan.sections)).cuda()
+    angle = pos.double()[..., axis] * torch.tensor(plan.freqs, dtype=torch.float64, device="cuda")
+    c, s = torch.cos(angle)[..., None, :], torch.sin(angle)[..., None, :]
+    P = plan.pairs
+    if plan.layout == "interleaved":
+        u, v = x[..., 0:2 * P:2], x[..., 1:2 * P:2]
+        turned = torch.stack((u * c - v * s, u * s + v * c), -1).flatten(-2)
+    else:
+        u, v = x[..., :P], x[..., P:2 * P]
+        turned = torch.cat((u * c - v * s, u * s + v * c), -1)
+    return torch.cat((turned, x[..., 2 * P:]), -1)
+
+
+def _attn64(q, k, v, causal):
+    G = q.shape[2] // k.shape[2]
+    q, k, v = q.transpose(1, 2), k.transpose(1, 2), v.transpose(1, 2)
+    k, v = k.repeat_interleave(G, 1), v.repeat_interleave(G, 1)
+    s = q @ k.transpose(2, 3) * q.shape[-1] ** -0.5
+    if causal:
+        n = s.shape[-1]
+        s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=s.device).triu(1), -float("inf"))
+    return (torch.softmax(s, -1) @ v).transpose(1, 2)
+
+
+def _rel(a, b):
+    return float((a.double() - b.double()).norm() / b.double().norm())
+
+
+# --- single modules --------------------------------------------------------------------
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_module_gradients(bl, residual):
+    """fp32: against fp64 autograd (64 roundings of 2^-24, see the operators' tests, are
+    4e-6) and against central differences of the module itself along a direction."""
+    norm = bl.BLRMSNorm(96, eps=1e-5, device="cuda")
+    with torch.no_grad():
+        norm.weight.copy_(1 + 0.3 * _randn(96, seed=1))
+    x, r = (_randn(2, 5, 96, seed=s).requires_grad_() for s in (2, 3))
+    gy, gh = _randn(2, 5, 96, seed=4), _randn(2, 5, 96, seed=5)
+
+    def loss(x, r):
+        if not residual:
+            return (norm(x).double() * gy).sum()
+        y, h = norm(x, r)
+        return (y.double() * gy).sum() + (h.double() * gh).sum()
+
+    leaves = [x, norm.weight] + ([r] if residual else [])
+    got = torch.autograd.grad(loss(x, r), leaves)
+    a, w, b = (t.detach().double().requires_grad_() for t in (x, norm.weight, r))
+    h = a + b if residual else a
+    ref_loss = (_norm64(h, w, 1e-5) * gy).sum() + ((h * gh).sum() if residual else 0)
+    ref = torch.autograd.grad(ref_loss, [a, w] + ([b] if residual else []))
+    for g, f in zip(got, ref):
+        assert _rel(g, f) <= 4e-6
+    # differences: the fp32 forward's rounding, about 1e-7 of terms of size 30, over 2 e
+    d, e = _randn(2, 5, 96, seed=6), 1e-2
+    with torch.no_grad():
+        slope = float(loss(x + e * d, r) - loss(x - e * d, r)) / (2 * e)
+    assert abs(slope - float((got[0].double() * d).sum())) <= 1e-3 * float(got[0].norm() * d.norm())
+
+
+def test_norm_module_unused_outputs_and_broadcast_gradients(bl):
+    """Only h used; only y used; a gradient that is one number expanded; one tensor as x and
+    residual."""
+    norm = bl.BLRMSNorm(64, device="cuda", dtype=torch.bfloat16)
+    x = _randn(3, 64, dtype=torch.bfloat16, seed=7).requires_grad_()
+    r = _randn(3, 64, dtype=torch.bfloat16, seed=8).requires_grad_()
+    _, h = norm(x, r)
+    gx, gr, gw = torch.autograd.grad(h.float().sum(), [x, r, norm.weight], allow_unused=True)
+    assert (gx == 1).all() and (gr == 1).all() and (gw is None or (gw == 0).all())
+    y, _ = norm(x, r)
+    gx, gr = torch.autograd.grad(y.sum(), [x, r])
+    a = (x.detach().double() + r.detach().double()).requires_grad_()
+    ref, = torch.autograd.grad(_norm64(a, 1.0).sum(), a)
+    assert torch.equal(gx, gr) and _rel(gx, ref) <= 1e-2       # h is saved in bf16
+    y, h = norm(x, x)
+    g, = torch.autograd.grad(h.sum(), x)
+    assert (g == 2).all()
+    frozen = bl.BLRMSNorm(64, device="cuda").requires_grad_(False)
+    frozen(x).float().sum().backward()
+    assert x.grad is not None and frozen.weight.grad is None
+
+
+@pytest.mark.parametrize("fmt,tol", [("int8", 0.02), ("e4m3", 0.06)])
+def test_norm_module_with_a_checkpoint(bl, fmt, tol):
+    """h in 8 bits: half a step is amax / 254 (int8: about 1% of an element of normal size,
+    uniformly distributed) or 2^-4 (e4m3: 3.6% root mean square at most) of u, which enters
+    g_w once and g_x's second, smaller, term."""
+    x = _randn(200, 640, dtype=torch.bfloat16, seed=9).requires_grad_()
+    gy = _randn(200, 640, dtype=torch.bfloat16, seed=10)
+    got = {}
+    for c in (None, fmt):
+        norm = bl.BLRMSNorm(640, checkpoint=c, device="cuda")
+        y = norm(x)
+        got[c] = (y, *torch.autograd.grad(y, [x, norm.weight], gy))
+    assert torch.equal(got[None][0], got[fmt][0])
+    assert _rel(got[fmt][1], got[None][1]) <= tol and _rel(got[fmt][2], got[None][2]) <= tol
+    # the bytes between forward and backward
+    held = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: held.append(t) or t, lambda t: t):
+        bl.BLRMSNorm(640, checkpoint=fmt, device="cuda")(x)
+    assert sum(t.numel() * t.element_size() for t in held) <= 200 * 640 * (1 + 4 / 128) + 200 * 4 + 640 * 4
+
+
+def test_rotary_module_gradients(bl):
+    rot = bl.Rotary(64, (10, 12, 10), layout="interleaved")
+    pos = bl.grid_positions(3, 4, 5)
+    assert pos.shape == (60, 3) and pos[-1].tolist() == [2, 3, 4] and pos[5].tolist() == [0, 1, 0]
+    q, k = _randn(2, 60, 4, 64, seed=11).requires_grad_(), _randn(2, 60, 2, 64, seed=12).requires_grad_()
+    gq, gk = _randn(2, 60, 4, 64, seed=13), _randn(2, 60, 2, 64, seed=14)
+    a, b = rot(q, k, pos)
+    got = torch.autograd.grad([a, b], [q, k], [gq, gk])
+    q64, k64 = q.detach().double().requires_grad_(), k.detach().double().requires_grad_()
+    ra, rb = _rope64(q64, pos, rot.plan), _rope64(k64, pos, rot.plan)
+    ref = torch.autograd.grad([ra, rb], [q64, k64], [gq.double(), gk.double()])
+    for x, y in zip((a, b, *got), (ra, rb, *ref)):
+        assert _rel(x, y) <= 2e-6
+    only, = torch.autograd.grad(rot(q, k, pos)[0].sum(), [q])       # k unused, an expanded gradient
+    assert _rel(only, torch.autograd.grad(_rope64(q64, pos, rot.plan).sum(), q64)[0]) <= 2e-6
+
+
+# --- a block of them --------------------------------------------------------------------
+
+def _block(bl, causal, checkpoint, d=128, H=4, Hk=2, seed=15):
+    """The modules of a block's attention half, and its fp64 form over the same weights."""
+    cols = H * d
+    entry = bl.BLRMSNorm(cols, device="cuda", dtype=torch.bfloat16, checkpoint=checkpoint)
+    q_norm = bl.BLRMSNorm(d, device="cuda", checkpoint=checkpoint, group=0)
+    k_norm = bl.BLRMSNorm(Hk * d, device="cuda")
+    rot = bl.Rotary(d, (22, 21, 21), layout="interleaved")
+    attn = bl.BLAttention(0.0, causal=causal, q_norm=q_norm, k_norm=k_norm, rotary=rot,
+                          checkpoint=checkpoint, checkpoint_out=checkpoint is not None)
+    with torch.no_grad():
+        for i, m in enumerate((entry, q_norm, k_norm)):
+            m.weight.add_(0.2 * _randn(m.cols, seed=seed + i).to(m.weight.dtype))
+    ws = [(_randn(cols, h * d, seed=seed + 5 + i) * cols ** -0.5).to(torch.bfloat16).requires_grad_()
+          for i, h in enumerate((H, Hk, Hk))]
+
+    def run(x, r, pos, cu=None):
+        y, h = entry(x, r)
+        q, k, v = (torch.matmul(y, w).unflatten(-1, (-1, d)) for w in ws)
+        if cu is not None:
+            o = attn.varlen(q, k, v, cu, positions=pos)
+        else:
+            o = attn(q, k, v, positions=pos)
+        return o.flatten(-2) + h, h
+
+    params = [entry.weight, q_norm.weight, k_norm.weight, *ws]
+
+    def plain(x, r, pos, p):
+        e, qn, kn, wq, wk, wv = p
+        h = x + r
+        y = _norm64(h, e)
+        q, k, v = ((y @ w).unflatten(-1, (-1, d)) for w in (wq, wk, wv))
+        q = _norm64(q, qn)
+        k = _norm64(k.flatten(-2), kn).unflatten(-1, (-1, d))
+        o = _attn64(_rope64(q, pos, rot.plan), _rope64(k, pos, rot.plan), v, causal)
+        return o.flatten(-2) + h, h
+
+    return run, plain, params
+
+
+# bf16: some ten roundings of 2^-9 root mean square on the way forward and back, and the
+# attention backward's own bar of 1e-2: 3e-2.  int8 adds errors of about 1% of u, q, k, v
+# and o each (a step of amax / 127, uniform), which enter the scores and their gradient a
+# few times: 8e-2; e4m3 has 2.7% (2^-4 / sqrt 3 at most) in their place: 2e-1.
+@pytest.mark.parametrize("checkpoint,tol", [(None, 3e-2), ("int8", 8e-2), ("e4m3", 2e-1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_block_together(bl, causal, checkpoint, tol):
+    run, plain, params = _block(bl, causal, checkpoint)
+    pos = bl.grid_positions(5, 6, 11)
+    n, cols = 330, 512
+    x = _randn(1, n, cols, dtype=torch.bfloat16, seed=30).requires_grad_()
+    r = _randn(1, n, cols, dtype=torch.bfloat16, seed=31).requires_grad_()
+    g, gh = _randn(1, n, cols, dtype=torch.bfloat16, seed=32), _randn(1, n, cols, dtype=torch.bfloat16,
+                                                                    seed=33)
+    out, h = run(x, r, pos)
+    got = torch.autograd.grad([out, h], [x, r, *params], [g, gh])
+    leaves = [t.detach().double().requires_grad_() for t in (x, r, *params)]
+    ref_out, ref_h = plain(leaves[0], leaves[1], pos, leaves[2:])
+    ref = torch.autograd.grad([ref_out, ref_h], leaves, [g.double(), gh.double()])
+    assert _rel(out, ref_out) <= 2e-2 and _rel(h, ref_h) <= 4e-3
+    for name, a, b in zip(("x", "r", "entry", "q_norm", "k_norm", "wq", "wk", "wv"), got, ref):
+        assert _rel(a, b) <= tol, name
+
+
+def test_block_packed(bl):
+    """A packed batch is its sequences one by one, positions and 8-bit checkpoints included."""
+    run, _, params = _block(bl, True, "int8")
+    lens = [130, 1, 257]
+    cu = [0, 130, 131, 388]
+    x = _randn(388, 512, dtype=torch.bfloat16, seed=34).requires_grad_()
+    r = _randn(388, 512, dtype=torch.bfloat16, seed=35)
+    pos = torch.cat([bl.grid_positions(1, 1, n) for n in lens])
+    g = _randn(388, 512, dtype=torch.bfloat16, seed=36)
+    out, _ = run(x, r, pos, cu)
+    got = torch.autograd.grad(out, [x], g)[0]
+    for a, b in zip(cu[:-1], cu[1:]):
+        xs = x.detach()[a:b][None].requires_grad_()
+        o, _ = run(xs, r[a:b][None], pos[a:b].contiguous())
+        gs = torch.autograd.grad(o, [xs], g[a:b][None])[0]
+        # the matrix products of other shapes may round differently
+        assert _rel(out[a:b], o[0]) <= 1e-2 and _rel(got[a:b], gs[0]) <= 2e-2
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_attention_checkpoint_holds_half_the_bytes(bl, fmt):
+    q, k, v = (_randn(1, 512, h, 128, dtype=torch.bfloat16, seed=s).requires_grad_()
+               for h, s in ((4, 40), (2, 41), (2, 42)))
+    held = {}
+    for c, out in ((None, False), (fmt, False), (fmt, True)):
+        attn = bl.BLAttention(0.05, checkpoint=c, checkpoint_out=out)
+        kept = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t) or t, lambda t: t):
+            o = attn(q, k, v)
+        held[out if c else None] = sum(t.numel() * t.element_size() for t in kept)
+        assert all(torch.isfinite(g).all() for g in torch.autograd.grad(o.float().sum(), [q, k, v]))
+    qkv, o, rows = 512 * 8 * 128, 512 * 4 * 128, 512 * 8 * 4
+    assert held[None] - held[False] == qkv - rows
+    assert held[False] - held[True] == o - 512 * 4 * 4
+
+
+def test_calibration_counts_the_checkpoint(bl):
+    from block_sparse_attention_fwd_gb300 import inputs
+    from block_sparse_attention_fwd_gb300.calibrate import calibrate_negl_prob
+    w = inputs.custom("calib8", B=1, n=1024, H=2, Hk=1, d=128, run=64, clusters=8, alpha=1.0)
+    q, k, v, go = (x.cuda() for x in inputs.generate(w, seed=6))
+    worst = {}
+    for c, out in ((None, False), ("int8", False), ("int8", True), ("e4m3", True)):
+        _, trials = calibrate_negl_prob(q, k, v, go, candidates=(1e-4,), checkpoint=c, checkpoint_out=out)
+        worst[c, out] = trials[0].worst_rel_l2
+    assert worst[None, False] < worst["int8", False] < worst["int8", True] * 1.05
+    assert worst["int8", True] < worst["e4m3", True]
+
+
+# --- streams and graphs ------------------------------------------------------------------
+
+def test_another_stream(bl):
+    """Work on a side stream is ordered there: inputs made on it, outputs read on it."""
+    side = torch.cuda.Stream()
+    w = 1 + 0.1 * _randn(5120, seed=50)
+    base = _randn(2000, 5120, dtype=torch.bfloat16, seed=51)
+    plan = bl.RopePlan(128, (64,))
+    pos = torch.arange(2000, dtype=torch.int32, device="cuda")[:, None]
+    torch.cuda.synchronize()
+
+    def chain(x):
+        y, h, rstd = bl.rms_norm_fwd(x, w, residual=x)
+        a = bl.act_save(y, "int8", 128)
+        g_x, g_w = bl.rms_norm_bwd(y, bl.act_save(h), rstd, w)
+        r, _ = bl.rope(y.view(1, 2000, 40, 128), None, pos, plan)
+        return bl.act_load(a), g_x, g_w, r
+
+    want = chain(base * 2)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x = base.clone()
+        for _ in range(20):
+            x.mul_(1.0)
+        x.mul_(2)
+        got = chain(x)
+        same = [torch.equal(a, b) for a, b in zip(got, want)]
+    assert all(same)
+
+
+def test_operators_replay_from_a_graph(bl):
+    """Captured once and replayed on new contents of the same tensors; two graphs that run in
+    turn do not share scratch."""
+    plan = bl.RopePlan(64, (20, 12))
+    w = 1 + 0.1 * _randn(512, seed=60)
+    pos = torch.randint(0, 100, (130, 2), dtype=torch.int32, device="cuda")
+
+    def chain(x, g):
+        y, h, rstd = bl.rms_norm_fwd(x, w, residual=g)
+        y8, _, _ = bl.rms_norm_fwd_8bit(x, w, residual=g, fmt="int8")
+        h8 = bl.act_save(h, "e4m3", 32)
+        g_x, g_w = bl.rms_norm_bwd(g, h8, rstd, w)
+        q = y.view(1, 130, 8, 64)
+        q, k = bl.rope(q, q[:, :, :4], pos, plan)
+        v = bl.act_load(y8).view(1, 130, 8, 64)[:, :, :4].contiguous()
+        shape = bl.make_shape(1, 130, 8, 4, 64, 128, 128, 1)
+        o = torch.empty_like(q)
+        lse = torch.empty((1, 8, 130), dtype=torch.float32, device="cuda")
+        bl.attn_fwd(shape, q, k, v, 0.125, o, lse)
+        back = bl.attn_bwd_act8(shape, bl.act_save(q), bl.act_save(k), bl.act_save(v), bl.act_save(o),
+                                g.view(1, 130, 8, 64), lse, 0.125)
+        return [g_x, g_w, q, k, o, *back]
+
+    data = [[_randn(130, 512, dtype=torch.bfloat16, seed=s + i) for i in range(2)] for s in (61, 63, 65)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        want = [chain(*d) for d in data]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        x, g = torch.empty_like(data[0][0]), torch.empty_like(data[0][1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = chain(x, g)
+        graphs.append((graph, x, g, out))
+    for turn in range(3):
+        for j, (graph, x, g, out) in enumerate(graphs):
+            d = (turn + j) % 3
+            x.copy_(data[d][0])
+            g.copy_(data[d][1])
+            graph.replay()
+        torch.cuda.synchronize()
+        for j, (_, _, _, out) in enumerate(graphs):
+            for i, (a, b) in enumerate(zip(out, want[(turn + j) % 3])):
+                if i == 5:                     # G_Q: the order of its reduce-adds varies
+                    assert U.rel_l2(U.cpu(a), U.cpu(b)) <= 1e-3
+                else:
+                    assert torch.equal(a, b), i
+
+
+def test_a_training_step_replays_from_a_graph(bl):
+    """Forward and backward of the block captured together."""
+    run, _, params = _block(bl, False, "int8", seed=70)
+    pos = bl.grid_positions(2, 5, 13)
+    x = _randn(1, 130, 512, dtype=torch.bfloat16, seed=71).requires_grad_()
+    r = _randn(1, 130, 512, dtype=torch.bfloat16, seed=72)
+    g = _randn(1, 130, 512, dtype=torch.bfloat16, seed=73)
+
+    def step():
+        out, _ = run(x, r, pos)
+        return torch.autograd.grad(out, [x, *params], g)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            want = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert _rel(a, b) <= 2e-3
