@@ -23,8 +23,45 @@ __device__ __forceinline__ void div_mod(int64_t x, int64_t d, int64_t& q, int64_
   }
 }
 
-// Groups of `a.group` elements: a.group / 8 neighbouring lanes hold one, each
-// lane one chunk.  A row takes a whole number of groups (the last may be cut).
+// Groups back to back in memory (every row a whole number of them): no rows,
+// no division.  A lane holds 16 elements, so group / 16 = 2, 4 or 8
+// neighbouring lanes hold a group; a thread takes U such pieces, 256 apart, and
+// loads all of them before it works on any, which keeps U * 32 bytes of a
+// 16-bit type in flight for each thread.
+template <typename T, int FMT, int U>
+__global__ void __launch_bounds__(256) act_save_flat_kernel(const T* __restrict__ x,
+                                                            uint8_t* __restrict__ codes,
+                                                            float* __restrict__ scales,
+                                                            int64_t pieces, int shift) {
+  const int lanes = 1 << shift;
+  const int64_t p0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+  Chunk<T> c[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) c[u][v] = load8<T, true>(x + p * 16 + v * 8, p < pieces ? 8 : 0);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+    float f[2][8];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[v][i] = to_f32(c[u][v].e[i]);
+    const float scale = scale_of(lanes_amax(amax2(amax8(f[0]), amax8(f[1])), lanes), FMT);
+    const Codes lo = encode8<FMT>(f[0], scale), hi = encode8<FMT>(f[1], scale);
+    if (p < pieces) {
+      reinterpret_cast<uint4*>(codes)[p] = make_uint4(lo.w[0], lo.w[1], hi.w[0], hi.w[1]);
+      if ((p & (lanes - 1)) == 0) scales[p >> shift] = scale;
+    }
+  }
+}
+
+// Groups of `a.group` elements of rows of any width and stride: a.group / 8
+// neighbouring lanes hold one, each lane one chunk.  A row takes a whole number
+// of groups (the last may be cut).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
   const int lanes = a.group / 8;                    // 4, 8 or 16
@@ -43,9 +80,9 @@ __global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
     float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
-    const float scale = scale_of(lanes_max(amax_bits8(f), lanes), a.fmt);
+    const float scale = scale_of(lanes_amax(amax8(f), lanes), a.fmt);
     store_codes<VEC>(a.codes + row * a.cols + col, encode8(a.fmt, f, scale), valid);
-    if (in && j % lanes == 0) a.scales[row * a.groups + j / lanes] = scale;
+    if (in && (j & (lanes - 1)) == 0) a.scales[row * a.groups + j / lanes] = scale;
   }
 }
 
@@ -53,7 +90,7 @@ __global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
 // maximum and for the codes; the second reading comes from the caches.
 template <typename T, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
-  __shared__ uint32_t buf[2][32];
+  __shared__ float buf[2][32];
   const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
   const int step = BLOCK ? 256 : 32;
   const int rows_here = BLOCK ? 1 : 8;
@@ -63,23 +100,25 @@ __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
     const int64_t row = row0 + (BLOCK ? 0 : threadIdx.x >> 5);
     const int64_t cols = row < a.rows ? a.cols : 0;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    uint32_t m = 0;
+    float m = 0.f;
+#pragma unroll 4
     for (int64_t col = t * 8; col < cols; col += step * 8) {
       const int valid = (int)min((int64_t)8, cols - col);
       const Chunk<T> c = load8<T, VEC>(x + col, valid);
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
-      m = max(m, amax_bits8(f));
+      m = amax2(m, amax8(f));
     }
     if constexpr (BLOCK) {
-      m = block_max(m, buf, slot);
+      m = block_amax(m, buf, slot);
       slot ^= 1;
     } else {
       __syncwarp();
-      m = lanes_max(m, 32);
+      m = lanes_amax(m, 32);
     }
     const float scale = scale_of(m, a.fmt);
+#pragma unroll 4
     for (int64_t col = t * 8; col < cols; col += step * 8) {
       const int valid = (int)min((int64_t)8, cols - col);
       const Chunk<T> c = load8<T, VEC>(x + col, valid);
@@ -89,6 +128,40 @@ __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
       store_codes<VEC>(a.codes + row * a.cols + col, encode8(a.fmt, f, scale), valid);
     }
     if (t == 0 && row < a.rows) a.scales[row] = scale;
+  }
+}
+
+// Rows of whole groups back to back in memory, as in the flat saving kernel.
+template <typename T, int FMT, int U>
+__global__ void __launch_bounds__(256) act_load_flat_kernel(const uint8_t* __restrict__ codes,
+                                                            const float* __restrict__ scales,
+                                                            T* __restrict__ x, int64_t pieces,
+                                                            int shift) {
+  const int64_t p0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+  uint4 raw[U];
+  float scale[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+    scale[u] = 0.f;
+    if (p < pieces) {
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(codes) + p);
+      scale[u] = __ldg(scales + (p >> shift));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+    const Codes c[2] = {{{raw[u].x, raw[u].y}}, {{raw[u].z, raw[u].w}}};
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float f[8];
+      decode8<FMT>(c[v], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= scale[u];
+      store8<T, true>(x + p * 16 + v * 8, f, p < pieces ? 8 : 0);
+    }
   }
 }
 
@@ -143,6 +216,16 @@ unsigned blocks_for(int64_t units) {
   return (unsigned)(units < kMaxBlocks ? units : kMaxBlocks);
 }
 
+// Pieces of 16 elements a thread of the flat kernels.
+constexpr int kFlatU = 2;
+
+// Whether the flat kernels take rows of `cols` with this group: then the shift
+// from a piece to its group.
+int flat_shift(int64_t cols, int group) {
+  if (!group || cols % group) return -1;
+  return group_shift(group) - 4;
+}
+
 }  // namespace
 
 cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
@@ -154,7 +237,19 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
                      aligned_to(a.codes, 8);
-    if (a.group) {
+    const int shift = a.x_stride == a.cols && aligned_to(a.x, 16) && aligned_to(a.codes, 16)
+                          ? flat_shift(a.cols, a.group) : -1;
+    if (shift >= 0) {
+      const int64_t pieces = a.rows * (a.cols / 16);
+      const unsigned g = (unsigned)((pieces + 256 * kFlatU - 1) / (256 * kFlatU));
+      auto* x = static_cast<const T*>(a.x);
+      if (a.fmt == kFmtInt8)
+        act_save_flat_kernel<T, kFmtInt8, kFlatU><<<g, 256, 0, st>>>(x, a.codes, a.scales, pieces,
+                                                                     shift);
+      else
+        act_save_flat_kernel<T, kFmtE4m3, kFlatU><<<g, 256, 0, st>>>(x, a.codes, a.scales, pieces,
+                                                                     shift);
+    } else if (a.group) {
       const int64_t units = (a.rows * a.groups * (a.group / 8) + 255) / 256;
       if (vec)
         act_save_groups_kernel<T, true><<<blocks_for(units), 256, 0, st>>>(a);
@@ -175,11 +270,27 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
   });
 }
 
-cudaError_t launch_act_load(int dtype, const ActLoad& a, cudaStream_t st) {
+cudaError_t launch_act_load(int dtype, const ActLoad& in, cudaStream_t st) {
+  ActLoad a = in;
   if (a.rows == 0) return cudaSuccess;
+  if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.codes, 8);
+    const int shift = aligned_to(a.x, 16) && aligned_to(a.codes, 16)
+                          ? flat_shift(a.cols, a.group) : -1;
+    if (shift >= 0) {
+      const int64_t pieces = a.rows * (a.cols / 16);
+      const unsigned g = (unsigned)((pieces + 256 * kFlatU - 1) / (256 * kFlatU));
+      auto* x = static_cast<T*>(a.x);
+      if (a.fmt == kFmtInt8)
+        act_load_flat_kernel<T, kFmtInt8, kFlatU><<<g, 256, 0, st>>>(a.codes, a.scales, x, pieces,
+                                                                     shift);
+      else
+        act_load_flat_kernel<T, kFmtE4m3, kFlatU><<<g, 256, 0, st>>>(a.codes, a.scales, x, pieces,
+                                                                     shift);
+      return cudaGetLastError();
+    }
     const unsigned g = blocks_for((a.rows * ((a.cols + 7) / 8) + 255) / 256);
     if (a.fmt == kFmtInt8)
       vec ? act_load_kernel<T, true, kFmtInt8><<<g, 256, 0, st>>>(a)

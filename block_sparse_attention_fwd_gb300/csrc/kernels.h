@@ -77,7 +77,7 @@ struct NormFwd {
   uint8_t* codes;                 // 8-bit output, with scales [rows, groups]
   float* scales;
   float eps;
-  int group, fmt;
+  int group, fmt, shift;          // shift: from a column to its group, set by the launch
   bool w_f32;                     // the weight is fp32, whatever x is
 };
 struct NormBwd {
@@ -87,7 +87,7 @@ struct NormBwd {
   const float *scales, *rstd;
   void* g_x;
   float* partial;                 // [norm_bwd_parts, cols], or null without g_w
-  int group, fmt;
+  int group, fmt, shift;
   bool w_f32;
 };
 cudaError_t launch_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st);
@@ -141,9 +141,7 @@ struct Rope {
   const int32_t* pos;             // [B or 1, n, axes]
   int64_t pos_batch;              // 0: shared by the batches
   const uint64_t* freqs;          // [pairs], turns in 64-bit fixed point
-  int lanes;                      // set by the launch
-  uint32_t q_units, k_units;
-  int64_t units;
+  int lanes, tile;                // set by the launch
 };
 cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st);
 

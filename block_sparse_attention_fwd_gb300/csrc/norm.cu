@@ -16,113 +16,414 @@ namespace bl {
 
 namespace {
 
-// A row is held by LPR lanes of a warp (LPR = 8, 16, 32: up to 64, 128, 256
-// columns) or by the whole block (LPR = 0), each thread NV chunks of it.
-template <typename T, int LPR, int NV, bool VEC, bool Q8>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(NormFwd a) {
-  __shared__ uint32_t buf[2][32];
-  constexpr int TPR = LPR;
-  const int rows_here = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
-  const int t = LPR ? threadIdx.x % (LPR ? LPR : 1) : threadIdx.x;
-  const int step = LPR ? TPR : blockDim.x;      // chunks between a thread's own
+// A row is held by LPR lanes of a warp (8, 16 or 32, each with NV chunks: up to
+// 1024 columns) or by the whole block (LPR = 0).
+template <int LPR>
+struct Rows {
+  int here, mine, t, step;      // rows of the block, this thread's; its first chunk and their distance
+  __device__ __forceinline__ Rows() {
+    if constexpr (LPR != 0) {
+      here = blockDim.x / LPR;
+      mine = threadIdx.x / LPR;
+      t = threadIdx.x % LPR;
+      step = LPR;
+    } else {
+      here = 1;
+      mine = 0;
+      t = threadIdx.x;
+      step = blockDim.x;
+    }
+  }
+};
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float (*buf)[32], int& slot) {
+  if constexpr (LPR != 0) return lanes_sum(v, LPR);
+  v = block_sum(v, buf, slot);
+  slot ^= 1;
+  return v;
+}
+
+// FMT8: 0 without the 8-bit output, else its format.
+template <typename T, int LPR, int NV, bool VEC, int FMT8>
+__global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
+  __shared__ float buf[2][32];
+  const Rows<LPR> R;
   const int cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
   int slot = 0;
   // the loop is uniform over the block (lanes past the last row work on zeros)
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows;
-       row0 += (int64_t)gridDim.x * rows_here) {
-    const int64_t row = row0 + (LPR ? threadIdx.x / (LPR ? LPR : 1) : 0);
+  for (int64_t row0 = (int64_t)blockIdx.x * R.here; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * R.here) {
+    const int64_t row = row0 + R.mine;
     const bool in = row < a.rows;
     float h[NV][8];
     float ss = 0.f;
+    Chunk<T> x[NV], r[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
+      const int col = (R.t + k * R.step) * 8;
       const int valid = in ? cols - col : 0;
-      const Chunk<T> x =
-          load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col, valid);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x.e[i]);
+      x[k] = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col, valid);
+      if (a.r) r[k] = load8<T, VEC>(static_cast<const T*>(a.r) + row * a.r_stride + col, valid);
     }
-    if (a.r) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int col = (t + k * step) * 8;
-        const int valid = in ? cols - col : 0;
-        const Chunk<T> r =
-            load8<T, VEC>(static_cast<const T*>(a.r) + row * a.r_stride + col, valid);
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      const int valid = in ? cols - col : 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r.e[i]);
+      for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x[k].e[i]);
+      if (a.r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r[k].e[i]);
         if (a.h) store8<T, VEC>(static_cast<T*>(a.h) + row * cols + col, h[k], valid);
       }
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
-    if constexpr (LPR != 0) {
-      ss = lanes_sum(ss, LPR);
-    } else {
-      ss = block_sum(ss, buf, slot);
-      slot ^= 1;
     }
-    const float rstd = 1.f / sqrtf(fmaf(ss, inv_cols, a.eps));
-    if (t == 0 && in && a.rstd) a.rstd[row] = rstd;
-    uint32_t top = 0;
+    ss = row_sum<LPR>(ss, buf, slot);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+    if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
+    float top = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
+      const int col = (R.t + k * R.step) * 8;
       const int valid = in ? cols - col : 0;
       float w[8];
       load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[i];
       if (a.y) store8<T, VEC>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
-      if constexpr (Q8) {
-        uint32_t m = amax_bits8(h[k]);
+      if constexpr (FMT8 != 0) {
+        float m = amax8(h[k]);
         if (a.group) {
-          m = lanes_max(m, min(a.group / 8, LPR ? LPR : 32));
-          const float scale = scale_of(m, a.fmt);
-          const Codes c = encode8(a.fmt, h[k], scale);
-          store_codes<VEC>(a.codes + row * cols + col, c, valid);
-          if (valid > 0 && col % a.group == 0)
-            a.scales[row * a.groups + col / a.group] = scale;
+          m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
+          const float scale = scale_of(m, FMT8);
+          store_codes<VEC>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale), valid);
+          if (valid > 0 && (col & (a.group - 1)) == 0)
+            a.scales[row * a.groups + (col >> a.shift)] = scale;
         } else {
-          top = max(top, m);
+          top = amax2(top, m);
         }
       }
     }
-    if constexpr (Q8) {
+    if constexpr (FMT8 != 0) {
       if (!a.group) {
         if constexpr (LPR != 0) {
-          top = lanes_max(top, LPR);
+          top = lanes_amax(top, LPR);
         } else {
-          top = block_max(top, buf, slot);
+          top = block_amax(top, buf, slot);
           slot ^= 1;
         }
-        const float scale = scale_of(top, a.fmt);
+        const float scale = scale_of(top, FMT8);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int col = (t + k * step) * 8;
+          const int col = (R.t + k * R.step) * 8;
           const int valid = in ? cols - col : 0;
-          store_codes<VEC>(a.codes + row * cols + col, encode8(a.fmt, h[k], scale), valid);
+          store_codes<VEC>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale), valid);
         }
-        if (t == 0 && in) a.scales[row] = scale;
+        if (R.t == 0 && in) a.scales[row] = scale;
       }
     }
   }
 }
 
-// One pass over the rows: g_x, and per block the partial sums of g_w over the
-// block's rows, which stay in registers until the end ([grid, cols] fp32 in
-// the workspace).  FMT 0 reads h in the type T, otherwise its 8-bit codes.
+// The same for rows whose chunks are whole and aligned, on a grid that fills the
+// GPU once: a block takes rows gridDim.x apart, and x and r of the next S - 1
+// of them are on their way to shared memory meanwhile, each thread's chunks into
+// places of its own.  Loading straight into registers instead leaves the
+// memory idle while a row is reduced.
+template <typename T, int LPR, int NV, int FMT8, int S>
+__global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd a) {
+  constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
+  __shared__ float buf[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Rows<LPR> R;
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.f / (float)cols;
+  const int nt = blockDim.x;
+  const int64_t stride = (int64_t)gridDim.x * R.here;
+  // the thread's place in stage s, chunk k: x, and r another nt * CB behind
+  auto place = [&](int s, int k) -> uint8_t* {
+    return ring + (s * NV + k) * nt * 2 * CB + threadIdx.x * 16;
+  };
+  auto fetch = [&](int s, int64_t row) {
+    if (row < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+      const T* r = static_cast<const T*>(a.r) + row * a.r_stride;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (R.t + k * R.step) * 8;
+        if (col < cols) {
+          uint8_t* p = place(s, k);
+#pragma unroll
+          for (int v = 0; v < CB / 16; ++v) {
+            copy_async<16>(p + v * nt * 16, x + col + v * (16 / sizeof(T)));
+            if (a.r) copy_async<16>(p + nt * CB + v * nt * 16, r + col + v * (16 / sizeof(T)));
+          }
+        }
+      }
+    }
+    copy_commit();
+  };
+  auto chunk = [&](const uint8_t* p) {
+    Chunk<T> c;
+#pragma unroll
+    for (int v = 0; v < CB / 16; ++v)
+      reinterpret_cast<uint4*>(&c)[v] = *reinterpret_cast<const uint4*>(p + v * nt * 16);
+    return c;
+  };
+  const int64_t first = (int64_t)blockIdx.x * R.here;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
+  float w[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int col = (R.t + k * R.step) * 8;
+    load_weight8<T, true>(a.w, a.w_f32, col, cols - col, w[k]);
+  }
+  int slot = 0, now = 0;
+  for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
+    const int64_t row = row0 + R.mine;
+    const bool in = row < a.rows;
+    fetch(now == 0 ? S - 1 : now - 1, row + (S - 1) * stride);
+    copy_wait<S - 1>();
+    float h[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      if (in && col < cols) {
+        const uint8_t* p = place(now, k);
+        const Chunk<T> x = chunk(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x.e[i]);
+        if (a.r) {
+          const Chunk<T> r = chunk(p + nt * CB);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r.e[i]);
+          if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * cols + col, h[k], 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
+      }
+    }
+    ss = row_sum<LPR>(ss, buf, slot);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+    if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      const int valid = in && col < cols ? 8 : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[k][i];
+      if (a.y) store8<T, true>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
+      if constexpr (FMT8 != 0) {
+        float m = amax8(h[k]);
+        if (a.group) {
+          m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
+          const float scale = scale_of(m, FMT8);
+          store_codes<true>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale), valid);
+          if (valid > 0 && (col & (a.group - 1)) == 0)
+            a.scales[row * a.groups + (col >> a.shift)] = scale;
+        } else {
+          top = amax2(top, m);
+        }
+      }
+    }
+    if constexpr (FMT8 != 0) {
+      if (!a.group) {
+        if constexpr (LPR != 0) {
+          top = lanes_amax(top, LPR);
+        } else {
+          top = block_amax(top, buf, slot);
+          slot ^= 1;
+        }
+        const float scale = scale_of(top, FMT8);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int col = (R.t + k * R.step) * 8;
+          store_codes<true>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale),
+                            in && col < cols ? 8 : 0);
+        }
+        if (R.t == 0 && in) a.scales[row] = scale;
+      }
+    }
+    now = now == S - 1 ? 0 : now + 1;
+  }
+}
+
+// The end of a backward block: its threads' sums of g_w over the block's rows
+// go to the block's row of a.partial.
+template <int LPR, int NV, bool VEC>
+__device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>& R,
+                                              const float (&acc)[NV][8], float* part) {
+  const int cols = (int)a.cols;
+  float* out = a.partial + (int64_t)blockIdx.x * cols;
+  if constexpr (LPR != 0) {
+    // the block's row slots are added in their order
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        part[R.mine * (LPR * NV * 8) + (R.t + k * LPR) * 8 + i] = acc[k][i];
+    __syncthreads();
+    for (int col = threadIdx.x; col < cols; col += blockDim.x) {
+      float s = 0.f;
+      for (int r = 0; r < R.here; ++r) s += part[r * (LPR * NV * 8) + col];
+      out[col] = s;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      store8<float, VEC>(out + col, acc[k], cols - col);
+    }
+  }
+}
+
+// The backward of rows whose chunks are whole and aligned: one pass over the
+// rows.  A block stays for a run of rows, gridDim.x apart, and keeps its sums
+// of g_w in registers; g_y, h (or its codes and scales) and g_h of the next
+// S - 1 rows are on their way to shared memory meanwhile, each thread's
+// chunks into places of its own.
+template <typename T, int LPR, int NV, int FMT, int S>
+__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(NV == 4 ? 128 : 96)
+    norm_bwd_ring_kernel(NormBwd a) {
+  constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
+  constexpr int HB = FMT ? 8 : CB;                   // of h's
+  __shared__ float buf[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
+  const Rows<LPR> R;
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.f / (float)cols;
+  const int nt = blockDim.x;
+  // [stage][k] places of nt chunks: g_y, g_h, h, then (FMT) nt scales
+  const int stage_bytes = NV * nt * (2 * CB + HB + (FMT ? 4 : 0));
+  const int64_t stride = (int64_t)gridDim.x * R.here;
+  auto place = [&](int s, int k) -> uint8_t* {
+    return ring + s * stage_bytes + k * nt * (2 * CB + HB + (FMT ? 4 : 0));
+  };
+  auto fetch = [&](int s, int64_t row) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (R.t + k * R.step) * 8;
+        if (col >= cols) continue;
+        uint8_t* p = place(s, k);
+        const int64_t at = row * cols + col;
+#pragma unroll
+        for (int v = 0; v < CB / 16; ++v) {
+          copy_async<16>(p + (v * nt + threadIdx.x) * 16,
+                         reinterpret_cast<const uint8_t*>(a.g_y) + at * sizeof(T) + v * 16);
+          if (a.g_h)
+            copy_async<16>(p + nt * CB + (v * nt + threadIdx.x) * 16,
+                           reinterpret_cast<const uint8_t*>(a.g_h) + at * sizeof(T) + v * 16);
+          if constexpr (FMT == 0)
+            copy_async<16>(p + nt * 2 * CB + (v * nt + threadIdx.x) * 16,
+                           reinterpret_cast<const uint8_t*>(a.h) + at * sizeof(T) + v * 16);
+        }
+        if constexpr (FMT != 0) {
+          copy_async<8>(p + nt * 2 * CB + threadIdx.x * 8, a.codes + at);
+          copy_async<4>(p + nt * (2 * CB + 8) + threadIdx.x * 4,
+                        a.scales + row * a.groups + (col >> a.shift));
+        }
+      }
+    }
+    copy_commit();
+  };
+  auto chunk = [&](const uint8_t* p) {
+    Chunk<T> c;
+#pragma unroll
+    for (int v = 0; v < CB / 16; ++v)
+      reinterpret_cast<uint4*>(&c)[v] =
+          *reinterpret_cast<const uint4*>(p + (v * nt + threadIdx.x) * 16);
+    return c;
+  };
+  auto unit = [&](const uint8_t* p, float rstd, float (&u)[8]) {
+    if constexpr (FMT == 0) {
+      const Chunk<T> c = chunk(p + nt * 2 * CB);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = to_f32(c.e[i]) * rstd;
+    } else {
+      const uint2 raw = *reinterpret_cast<const uint2*>(p + nt * 2 * CB + threadIdx.x * 8);
+      const float s = *reinterpret_cast<const float*>(p + nt * (2 * CB + 8) + threadIdx.x * 4);
+      decode8<FMT>(Codes{{raw.x, raw.y}}, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = u[i] * s * rstd;
+    }
+  };
+
+  float acc[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
+  const int64_t first = (int64_t)blockIdx.x * R.here;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
+  int slot = 0, now = 0;
+  float rstd = first + R.mine < a.rows ? a.rstd[first + R.mine] : 0.f;
+  for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
+    const int64_t row = row0 + R.mine;
+    const bool in = row < a.rows;
+    fetch(now == 0 ? S - 1 : now - 1, row + (S - 1) * stride);
+    const float rstd_next = row + stride < a.rows ? a.rstd[row + stride] : 0.f;
+    float wg[NV][8], u[NV][8];                       // wg: first the weight alone
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      load_weight8<T, true>(a.w, a.w_f32, col, cols - col, wg[k]);
+    }
+    copy_wait<S - 1>();
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      if (!in || col >= cols) continue;
+      const uint8_t* p = place(now, k);
+      const Chunk<T> gy = chunk(p);
+      unit(p, rstd, u[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = to_f32(gy.e[i]);
+        acc[k][i] = fmaf(g, u[k][i], acc[k][i]);
+        wg[k][i] *= g;
+        dot = fmaf(wg[k][i], u[k][i], dot);
+      }
+    }
+    const float c = row_sum<LPR>(dot, buf, slot) * inv_cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      if (!in || col >= cols) continue;
+      const uint8_t* p = place(now, k);
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = rstd * (wg[k][i] - u[k][i] * c);
+      if (a.g_h) {
+        const Chunk<T> e = chunk(p + nt * CB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += to_f32(e.e[i]);
+      }
+      store8<T, true>(static_cast<T*>(a.g_x) + row * cols + col, g, 8);
+    }
+    rstd = rstd_next;
+    now = now == S - 1 ? 0 : now + 1;
+  }
+  if (a.partial) write_partial<LPR, NV, true>(a, R, acc, reinterpret_cast<float*>(ring));
+}
+
+// The backward of any other rows, straight from global memory.
 template <typename T, int LPR, int NV, bool VEC, int FMT>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwd a) {
-  __shared__ uint32_t buf[2][32];
-  __shared__ float part[LPR ? 512 * 8 : 1];
-  const int rows_here = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
-  const int t = LPR ? threadIdx.x % (LPR ? LPR : 1) : threadIdx.x;
-  const int step = LPR ? LPR : blockDim.x;
+__global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
+  __shared__ float buf[2][32];
+  __shared__ float part[LPR ? 256 * 8 * NV : 1];
+  const Rows<LPR> R;
   const int cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
   float acc[NV][8];
@@ -131,58 +432,51 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwd a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
   int slot = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows;
-       row0 += (int64_t)gridDim.x * rows_here) {
-    const int64_t row = row0 + (LPR ? threadIdx.x / (LPR ? LPR : 1) : 0);
+  auto load_unit = [&](int64_t row, int col, int valid, float rstd, float (&u)[8]) {
+    if constexpr (FMT == 0) {
+      const Chunk<T> h = load8<T, VEC>(static_cast<const T*>(a.h) + row * cols + col, valid);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = to_f32(h.e[i]) * rstd;
+    } else {
+      const Codes c = load_codes<VEC>(a.codes + row * cols + col, valid);
+      const float s = valid > 0 ? a.scales[row * a.groups + (col >> a.shift)] : 0.f;
+      decode8<FMT>(c, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = u[i] * s * rstd;
+    }
+  };
+  for (int64_t row0 = (int64_t)blockIdx.x * R.here; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * R.here) {
+    const int64_t row = row0 + R.mine;
     const bool in = row < a.rows;
     const float rstd = in ? a.rstd[row] : 0.f;
     Chunk<T> gy[NV];
-    float u[NV][8];
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
+      const int col = (R.t + k * R.step) * 8;
       const int valid = in ? cols - col : 0;
       gy[k] = load8<T, VEC>(static_cast<const T*>(a.g_y) + row * cols + col, valid);
-      if constexpr (FMT == 0) {
-        const Chunk<T> h = load8<T, VEC>(static_cast<const T*>(a.h) + row * cols + col, valid);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[k][i] = to_f32(h.e[i]) * rstd;
-      } else {
-        const Codes c = load_codes<VEC>(a.codes + row * cols + col, valid);
-        const float s = valid > 0 ? a.scales[row * a.groups + (a.group ? col / a.group : 0)] : 0.f;
-        decode8<FMT>(c, u[k]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[k][i] = u[k][i] * s * rstd;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
-      float w[8];
+      float w[8], u[8];
+      load_unit(row, col, valid, rstd, u);
       load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float g = to_f32(gy[k].e[i]);
-        acc[k][i] = fmaf(g, u[k][i], acc[k][i]);
-        dot = fmaf(g * w[i], u[k][i], dot);
+        acc[k][i] = fmaf(g, u[i], acc[k][i]);
+        dot = fmaf(g * w[i], u[i], dot);
       }
     }
-    if constexpr (LPR != 0) {
-      dot = lanes_sum(dot, LPR);
-    } else {
-      dot = block_sum(dot, buf, slot);
-      slot ^= 1;
-    }
-    const float c = dot * inv_cols;
+    const float c = row_sum<LPR>(dot, buf, slot) * inv_cols;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
+      const int col = (R.t + k * R.step) * 8;
       const int valid = in ? cols - col : 0;
-      float w[8], g[8];
+      float w[8], u[8], g[8];
+      load_unit(row, col, valid, rstd, u);             // from the caches
       load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = rstd * (to_f32(gy[k].e[i]) * w[i] - u[k][i] * c);
+      for (int i = 0; i < 8; ++i) g[i] = rstd * (to_f32(gy[k].e[i]) * w[i] - u[i] * c);
       if (a.g_h) {
         const Chunk<T> e = load8<T, VEC>(static_cast<const T*>(a.g_h) + row * cols + col, valid);
 #pragma unroll
@@ -191,25 +485,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwd a) {
       store8<T, VEC>(static_cast<T*>(a.g_x) + row * cols + col, g, valid);
     }
   }
-  if (!a.partial) return;
-  float* out = a.partial + (int64_t)blockIdx.x * cols;
-  if constexpr (LPR != 0) {
-    // the block's row slots are added in their order
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[threadIdx.x * 8 + i] = acc[0][i];
-    __syncthreads();
-    for (int col = threadIdx.x; col < cols; col += blockDim.x) {
-      float s = 0.f;
-      for (int r = 0; r < rows_here; ++r) s += part[r * (LPR * 8) + col];
-      out[col] = s;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (t + k * step) * 8;
-      store8<float, VEC>(out + col, acc[k], cols - col);
-    }
-  }
+  if (a.partial) write_partial<LPR, NV, VEC>(a, R, acc, part);
 }
 
 // g_w[col] = sum of the blocks' partial sums, 32 columns a block, 32 slices of
@@ -237,105 +513,164 @@ __global__ void __launch_bounds__(1024) norm_gw_kernel(const float* __restrict__
   }
 }
 
-// Threads, blocks and chunks a thread of a launch over rows of `cols` columns.
+// Lanes a row (0: the block), chunks a thread and threads of a launch over rows
+// of `cols` columns.  Up to 512 columns a warp holds whole rows; beyond, a block
+// of as few threads as hold the row with two chunks each, one chunk up to 1024
+// columns, where blocks are small.
 struct Plan {
-  int lpr, nv, threads;
-  int64_t blocks;
+  int lpr, nv, threads, here;
 };
-Plan plan(int64_t rows, int64_t cols, int max_blocks) {
+Plan plan(int64_t cols, int max_threads) {
   const int chunks = (int)((cols + 7) / 8);
   Plan p;
-  if (chunks <= 32) {
+  if (chunks <= 64) {
     p.lpr = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
-    p.nv = 1;
+    p.nv = chunks <= 32 ? 1 : 2;
     p.threads = 256;
-    p.blocks = (rows + 256 / p.lpr - 1) / (256 / p.lpr);
+    p.here = 256 / p.lpr;
   } else {
     p.lpr = 0;
-    p.nv = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
+    p.nv = chunks <= 128 ? 1 : chunks <= 2 * max_threads ? 2 : 4;
     p.threads = ((chunks + p.nv - 1) / p.nv + 31) / 32 * 32;
-    p.blocks = rows;
+    p.here = 1;
   }
-  if (p.blocks > max_blocks) p.blocks = max_blocks;
   return p;
 }
 
-constexpr int kFwdBlocks = 152 * 8, kBwdBlocks = 152 * 4;
+constexpr int kSMs = 152;
+constexpr size_t kMaxSmem = 220 * 1024;
 
-template <typename T, bool VEC, bool Q8>
-void fwd(const NormFwd& a, const Plan& p, cudaStream_t st) {
-  const unsigned g = (unsigned)p.blocks;
-  if (p.lpr == 8)
-    norm_fwd_kernel<T, 8, 1, VEC, Q8><<<g, p.threads, 0, st>>>(a);
-  else if (p.lpr == 16)
-    norm_fwd_kernel<T, 16, 1, VEC, Q8><<<g, p.threads, 0, st>>>(a);
-  else if (p.lpr == 32)
-    norm_fwd_kernel<T, 32, 1, VEC, Q8><<<g, p.threads, 0, st>>>(a);
-  else if (p.nv == 1)
-    norm_fwd_kernel<T, 0, 1, VEC, Q8><<<g, p.threads, 0, st>>>(a);
-  else if (p.nv == 2)
-    norm_fwd_kernel<T, 0, 2, VEC, Q8><<<g, p.threads, 0, st>>>(a);
-  else
-    norm_fwd_kernel<T, 0, 4, VEC, Q8><<<g, p.threads, 0, st>>>(a);
+// Blocks that are resident at once: `regs` a thread, `smem` bytes a block.
+int resident(int threads, int regs, size_t smem) {
+  int n = 65536 / (regs * threads);
+  const int by_smem = (int)(kMaxSmem / (smem + 1536));
+  if (n > by_smem) n = by_smem;
+  if (n > 2048 / threads) n = 2048 / threads;
+  if (n < 1) n = 1;
+  return kSMs * n;
+}
+unsigned grid(int64_t rows, int here, int most) {
+  const int64_t blocks = (rows + here - 1) / here;
+  return (unsigned)(blocks < most ? blocks : most);
 }
 
-template <typename T, bool VEC, int FMT>
-void bwd(const NormBwd& a, const Plan& p, cudaStream_t st) {
-  const unsigned g = (unsigned)p.blocks;
-  if (p.lpr == 8)
-    norm_bwd_kernel<T, 8, 1, VEC, FMT><<<g, p.threads, 0, st>>>(a);
-  else if (p.lpr == 16)
-    norm_bwd_kernel<T, 16, 1, VEC, FMT><<<g, p.threads, 0, st>>>(a);
-  else if (p.lpr == 32)
-    norm_bwd_kernel<T, 32, 1, VEC, FMT><<<g, p.threads, 0, st>>>(a);
-  else if (p.nv == 1)
-    norm_bwd_kernel<T, 0, 1, VEC, FMT><<<g, p.threads, 0, st>>>(a);
-  else if (p.nv == 2)
-    norm_bwd_kernel<T, 0, 2, VEC, FMT><<<g, p.threads, 0, st>>>(a);
-  else
-    norm_bwd_kernel<T, 0, 4, VEC, FMT><<<g, p.threads, 0, st>>>(a);
+// Calls f(lanes a row, chunks a thread) as compile-time constants.
+template <int N> struct Int { static constexpr int value = N; };
+template <typename F>
+void with_plan(const Plan& p, F&& f) {
+  if (p.lpr == 8) f(Int<8>(), Int<1>());
+  else if (p.lpr == 16) f(Int<16>(), Int<1>());
+  else if (p.lpr == 32 && p.nv == 1) f(Int<32>(), Int<1>());
+  else if (p.lpr == 32) f(Int<32>(), Int<2>());
+  else if (p.nv == 1) f(Int<0>(), Int<1>());
+  else if (p.nv == 2) f(Int<0>(), Int<2>());
+  else f(Int<0>(), Int<4>());
+}
+
+// Raises a kernel's limit of dynamic shared memory where a launch needs it.
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;           // static shared memory counts too
+  return cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)bytes);
+}
+
+template <typename T, int FMT8>
+cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
+  const Plan p = plan(a.cols, 1024);
+  cudaError_t e = cudaSuccess;
+  with_plan(p, [&](auto lpr, auto nv) {
+    constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
+    if constexpr (N != 4) {
+      const size_t stage = (size_t)N * p.threads * 2 * sizeof(Chunk<T>);
+      auto ring = [&](auto stages) {
+        constexpr int S = decltype(stages)::value;
+        auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S>;
+        const size_t smem = S * stage;
+        e = allow_smem(k, smem);
+        if (e == cudaSuccess)
+          k<<<grid(a.rows, p.here, resident(p.threads, 64, smem)), p.threads, smem, st>>>(a);
+      };
+      if (vec && 3 * stage <= kMaxSmem / 2)
+        ring(Int<3>());
+      else if (vec && 2 * stage <= kMaxSmem)
+        ring(Int<2>());
+      else
+        norm_fwd_kernel<T, L, N, false, FMT8>
+            <<<grid(a.rows, p.here, kSMs * 32), p.threads, 0, st>>>(a);
+    }
+  });
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Registers a thread of the backward's kernels (their caps).
+constexpr int bwd_regs(int lpr, int nv) { return nv == 4 ? 128 : lpr && nv == 1 ? 64 : 96; }
+
+template <typename T, int FMT>
+cudaError_t bwd(const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
+  const Plan p = plan(a.cols, 512);
+  cudaError_t e = cudaSuccess;
+  with_plan(p, [&](auto lpr, auto nv) {
+    constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
+    constexpr int S = L == 0 && N == 4 ? 2 : 3;
+    constexpr int CB = (int)sizeof(Chunk<T>);
+    size_t smem = (size_t)S * N * p.threads * (2 * CB + (FMT ? 12 : CB));
+    const size_t part = L ? (size_t)256 * 8 * N * 4 : 0;
+    if (smem < part) smem = part;
+    const bool ring = vec && smem <= kMaxSmem;
+    *blocks = grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N), ring ? smem : 0));
+    if (ring) {
+      auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S>;
+      e = allow_smem(k, smem);
+      if (e == cudaSuccess) k<<<*blocks, p.threads, smem, st>>>(a);
+    } else {
+      norm_bwd_kernel<T, L, N, false, FMT><<<*blocks, p.threads, 0, st>>>(a);
+    }
+  });
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
-int norm_bwd_parts(int64_t rows, int64_t cols) { return (int)plan(rows, cols, kBwdBlocks).blocks; }
+int norm_bwd_parts(int64_t rows, int64_t cols) {
+  const Plan p = plan(cols, 512);
+  return (int)grid(rows, p.here, resident(p.threads, bwd_regs(p.lpr, p.nv), 0));
+}
 
-cudaError_t launch_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st) {
+cudaError_t launch_norm_fwd(int dtype, const NormFwd& in, cudaStream_t st) {
+  NormFwd a = in;
   if (a.rows == 0) return cudaSuccess;
-  const Plan p = plan(a.rows, a.cols, kFwdBlocks);
+  a.shift = group_shift(a.group);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
                      aligned_to(a.x, 16) && aligned_to(a.r, 16) && aligned_to(a.h, 16) &&
                      aligned_to(a.y, 16) && aligned_to(a.w, 16) && aligned_to(a.codes, 8);
-    if (a.codes)
-      vec ? fwd<T, true, true>(a, p, st) : fwd<T, false, true>(a, p, st);
-    else
-      vec ? fwd<T, true, false>(a, p, st) : fwd<T, false, false>(a, p, st);
-    return cudaGetLastError();
+    const int fmt = a.codes ? a.fmt : 0;
+    return fmt == 0          ? fwd<T, 0>(a, vec, st)
+           : fmt == kFmtInt8 ? fwd<T, kFmtInt8>(a, vec, st)
+                             : fwd<T, kFmtE4m3>(a, vec, st);
   });
 }
 
-cudaError_t launch_norm_bwd(int dtype, const NormBwd& a, void* g_w, cudaStream_t st) {
-  const Plan p = plan(a.rows, a.cols, kBwdBlocks);
+cudaError_t launch_norm_bwd(int dtype, const NormBwd& in, void* g_w, cudaStream_t st) {
+  NormBwd a = in;
+  a.shift = group_shift(a.group);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && aligned_to(a.g_y, 16) && aligned_to(a.h, 16) &&
                      aligned_to(a.g_h, 16) && aligned_to(a.g_x, 16) && aligned_to(a.w, 16) &&
                      aligned_to(a.codes, 8) && aligned_to(a.partial, 16);
+    int blocks = 0;
     if (a.rows > 0) {
-      if (!a.codes)
-        vec ? bwd<T, true, 0>(a, p, st) : bwd<T, false, 0>(a, p, st);
-      else if (a.fmt == kFmtInt8)
-        vec ? bwd<T, true, kFmtInt8>(a, p, st) : bwd<T, false, kFmtInt8>(a, p, st);
-      else
-        vec ? bwd<T, true, kFmtE4m3>(a, p, st) : bwd<T, false, kFmtE4m3>(a, p, st);
-      const cudaError_t e = cudaGetLastError();
+      const cudaError_t e = !a.codes              ? bwd<T, 0>(a, vec, &blocks, st)
+                            : a.fmt == kFmtInt8   ? bwd<T, kFmtInt8>(a, vec, &blocks, st)
+                                                  : bwd<T, kFmtE4m3>(a, vec, &blocks, st);
       if (e != cudaSuccess) return e;
     }
     if (g_w) {
       norm_gw_kernel<T><<<(unsigned)((a.cols + 31) / 32), 1024, 0, st>>>(
-          a.partial, a.rows ? (int)p.blocks : 0, (int)a.cols, g_w, a.w_f32);
+          a.partial, blocks, (int)a.cols, g_w, a.w_f32);
       return cudaGetLastError();
     }
     return cudaSuccess;

@@ -15,10 +15,11 @@
 // fp64, whose rate here is low, and without a table to read.  The upper 32
 // bits, as a signed number of half turns, go to sincospi in fp32.
 //
-// The pass is bound by HBM: q and k once in, once out.  A group of lanes
-// covers one head of one token with 16-byte vectors; a thread takes the same
-// vector of U heads, so that the sines are formed once for U heads and U
-// loads are in flight.
+// The pass is bound by HBM: q and k once in, once out.  A block takes a tile of
+// tokens.  It forms the tile's sines and cosines once, in shared memory, and
+// then goes over the (token, head) units of the tile, 256 / lanes of them at a
+// time, a group of lanes with 16-byte vectors on each; a thread has the vectors
+// of U units in flight, the first of them from before the sines are formed.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -35,89 +36,115 @@ __device__ __forceinline__ void turn(const Rope& a, const int32_t* pos, int p, f
   if (a.inverse) s = -s;
 }
 
-// VECW elements (16 bytes) of a head at a time.
 template <typename T, int U, bool HALF>
 __global__ void __launch_bounds__(256) rope_kernel(Rope a) {
   constexpr int W = 16 / sizeof(T);
+  constexpr int NV = HALF ? 2 : 1;                   // vectors of a unit a thread holds
+  constexpr int NP = HALF ? W : W / 2;               // pairs in them
   struct alignas(16) Vec { T e[W]; };
-  const int lanes = a.lanes;                       // lanes a head
-  const int here = 256 / lanes;                    // units a block
-  const int g = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int64_t unit = (int64_t)blockIdx.x * here + g;
-  if (g >= here || unit >= a.units) return;
-  const uint32_t per_token = a.q_units + a.k_units;
-  const uint32_t token = (uint32_t)unit / per_token;
-  uint32_t hc = (uint32_t)unit % per_token;
-  const uint32_t b = token / (uint32_t)a.n, i = token % (uint32_t)a.n;
-  const bool is_k = hc >= a.q_units;
-  if (is_k) hc -= a.q_units;
-  const int heads = is_k ? a.Hk : a.H;
-  const int h0 = hc * U;
-  const T* in = static_cast<const T*>(is_k ? a.k : a.q);
-  T* out = static_cast<T*>(is_k ? a.k_out : a.q_out);
-  const int64_t* si = is_k ? a.ks : a.qs;
-  const int64_t* so = is_k ? a.kos : a.qos;
-  in += b * si[0] + i * si[1] + h0 * si[2];
-  out += b * so[0] + i * so[1] + h0 * so[2];
-  const int32_t* pos = a.pos + b * a.pos_batch + (int64_t)i * a.axes;
+  // (cos, sin) of the tile's tokens.  The pairs of a token lie in planes of two
+  // pairs a lane, so that neighbouring lanes read neighbouring 16 bytes.
+  extern __shared__ float4 table[];
+  const int lanes = a.lanes, step = 256 / lanes;
+  const int g = threadIdx.x / lanes, lane = threadIdx.x - g * lanes;
+  const int per_token = a.H + a.Hk;
+  const int64_t tok0 = (int64_t)blockIdx.x * a.tile;
+  const int toks = (int)min((int64_t)a.tile, (int64_t)a.B * a.n - tok0);
+  const int holders = (a.pairs + NP - 1) / NP;       // lanes that hold pairs
+  const int planes = NP / 2;
+  const int p0 = lane * NP;
+  const bool turns = lane < holders;
+  const bool works = g < step && (turns || a.copy);
+  // the thread's elements of a head
+  const int e0 = HALF ? (turns ? p0 : 2 * a.pairs + (lane - holders) * W) : 2 * p0;
 
-  if constexpr (HALF) {
-    const int turning = a.pairs / W;               // lanes that turn pairs
-    if (lane < turning) {
-      const int p0 = lane * W;
-      Vec u[U], v[U];
+  // the next unit: its token, head, and that token's heads
+  int tok = g / per_token, head = g - tok * per_token;
+  const int tok_step = step / per_token, head_step = step - tok_step * per_token;
+  const T *q_in, *k_in;
+  T *q_out, *k_out;
+  auto seek = [&]() {
+    const uint32_t t = (uint32_t)tok0 + tok;
+    const uint32_t b = t / (uint32_t)a.n, i = t - b * (uint32_t)a.n;
+    q_in = static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + e0;
+    q_out = static_cast<T*>(a.q_out) + b * a.qos[0] + i * a.qos[1] + e0;
+    k_in = static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + e0;
+    k_out = static_cast<T*>(a.k_out) + b * a.kos[0] + i * a.kos[1] + e0;
+  };
+  seek();
+  Vec v[U][NV];
+  T* dst[U];
+  int at[U];                                          // token of the tile, or -1
+  auto load = [&]() {
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (h0 + k < heads) {
-          u[k] = *reinterpret_cast<const Vec*>(in + k * si[2] + p0);
-          v[k] = *reinterpret_cast<const Vec*>(in + k * si[2] + p0 + a.pairs);
-        }
-      float c[W], s[W];
-#pragma unroll
-      for (int j = 0; j < W; ++j) turn(a, pos, p0 + j, c[j], s[j]);
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (h0 + k < heads) {
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const float x = to_f32(u[k].e[j]), y = to_f32(v[k].e[j]);
-            u[k].e[j] = from_f32<T>(x * c[j] - y * s[j]);
-            v[k].e[j] = from_f32<T>(x * s[j] + y * c[j]);
-          }
-          *reinterpret_cast<Vec*>(out + k * so[2] + p0) = u[k];
-          *reinterpret_cast<Vec*>(out + k * so[2] + p0 + a.pairs) = v[k];
-        }
-    } else if (a.copy) {
-      const int e0 = 2 * a.pairs + (lane - turning) * W;
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (h0 + k < heads)
-          *reinterpret_cast<Vec*>(out + k * so[2] + e0) =
-              *reinterpret_cast<const Vec*>(in + k * si[2] + e0);
-    }
-  } else {
-    const int p0 = lane * (W / 2);
-    if (p0 >= a.pairs && !a.copy) return;
-    Vec u[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (h0 + k < heads) u[k] = *reinterpret_cast<const Vec*>(in + k * si[2] + 2 * p0);
-    float c[W / 2], s[W / 2];
-#pragma unroll
-    for (int j = 0; j < W / 2; ++j)
-      if (p0 + j < a.pairs) turn(a, pos, p0 + j, c[j], s[j]);
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (h0 + k < heads) {
-#pragma unroll
-        for (int j = 0; j < W / 2; ++j)
-          if (p0 + j < a.pairs) {
-            const float x = to_f32(u[k].e[2 * j]), y = to_f32(u[k].e[2 * j + 1]);
-            u[k].e[2 * j] = from_f32<T>(x * c[j] - y * s[j]);
-            u[k].e[2 * j + 1] = from_f32<T>(x * s[j] + y * c[j]);
-          }
-        *reinterpret_cast<Vec*>(out + k * so[2] + 2 * p0) = u[k];
+    for (int u = 0; u < U; ++u) {
+      at[u] = works && tok < toks ? tok : -1;
+      if (at[u] < 0) continue;
+      const bool is_k = head >= a.H;
+      const int h = is_k ? head - a.H : head;
+      const T* src = (is_k ? k_in : q_in) + h * (is_k ? a.ks[2] : a.qs[2]);
+      dst[u] = (is_k ? k_out : q_out) + h * (is_k ? a.kos[2] : a.qos[2]);
+      v[u][0] = *reinterpret_cast<const Vec*>(src);
+      if constexpr (HALF)
+        if (turns) v[u][1] = *reinterpret_cast<const Vec*>(src + a.pairs);
+      const int was = tok;
+      tok += tok_step;
+      head += head_step;
+      if (head >= per_token) {
+        head -= per_token;
+        ++tok;
       }
+      if (tok != was) seek();
+    }
+  };
+
+  load();
+  for (int x = threadIdx.x; x < toks * a.pairs; x += 256) {
+    const int t = x / a.pairs, p = x - t * a.pairs;
+    const uint32_t b = ((uint32_t)tok0 + t) / (uint32_t)a.n;
+    const uint32_t i = (uint32_t)tok0 + t - b * (uint32_t)a.n;
+    float2 cs;
+    turn(a, a.pos + b * a.pos_batch + (int64_t)i * a.axes, p, cs.x, cs.y);
+    const int l = p / NP, j = p % NP;
+    reinterpret_cast<float2*>(table)[((t * planes + j / 2) * holders + l) * 2 + j % 2] = cs;
+  }
+  __syncthreads();
+  while (at[0] >= 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at[u] < 0) continue;
+      if (turns) {
+        const float4* cs = table + at[u] * planes * holders + lane;
+#pragma unroll
+        for (int j = 0; j < planes; ++j) {
+          const float4 c = cs[j * holders];
+          if constexpr (HALF) {
+            const float x0 = to_f32(v[u][0].e[2 * j]), x1 = to_f32(v[u][0].e[2 * j + 1]);
+            const float y0 = to_f32(v[u][1].e[2 * j]), y1 = to_f32(v[u][1].e[2 * j + 1]);
+            reinterpret_cast<Pair<T>*>(&v[u][0])[j] =
+                Pair<T>(x0 * c.x - y0 * c.y, x1 * c.z - y1 * c.w);
+            reinterpret_cast<Pair<T>*>(&v[u][1])[j] =
+                Pair<T>(x0 * c.y + y0 * c.x, x1 * c.w + y1 * c.z);
+          } else {
+            // the last vector may pass the last pair
+            if (p0 + 2 * j < a.pairs) {
+              const float x = to_f32(v[u][0].e[4 * j]), y = to_f32(v[u][0].e[4 * j + 1]);
+              reinterpret_cast<Pair<T>*>(&v[u][0])[2 * j] =
+                  Pair<T>(x * c.x - y * c.y, x * c.y + y * c.x);
+            }
+            if (p0 + 2 * j + 1 < a.pairs) {
+              const float x = to_f32(v[u][0].e[4 * j + 2]), y = to_f32(v[u][0].e[4 * j + 3]);
+              reinterpret_cast<Pair<T>*>(&v[u][0])[2 * j + 1] =
+                  Pair<T>(x * c.z - y * c.w, x * c.w + y * c.z);
+            }
+          }
+        }
+      }
+      *reinterpret_cast<Vec*>(dst[u]) = v[u][0];
+      if constexpr (HALF)
+        if (turns) *reinterpret_cast<Vec*>(dst[u] + a.pairs) = v[u][1];
+    }
+    load();
   }
 }
 
@@ -155,19 +182,30 @@ __global__ void __launch_bounds__(256) rope_any_kernel(Rope a) {
   }
 }
 
-template <typename T, int U>
-void rope_launch(Rope a, cudaStream_t st) {
-  a.q_units = (a.H + U - 1) / U;
-  a.k_units = (a.Hk + U - 1) / U;
-  a.units = (int64_t)a.B * a.n * (a.q_units + a.k_units);
+// Tokens of a block's tile: enough (token, head) units that every thread gets
+// several, as far as there are tokens for two blocks an SM.
+int tile_tokens(int64_t tokens, int heads, int groups) {
+  int64_t tile = (8 * groups + heads - 1) / heads;
+  if (tile > 32) tile = 32;
+  const int64_t fill = tokens / (2 * 152);
+  if (tile > fill) tile = fill;
+  return tile < 1 ? 1 : (int)tile;
+}
+
+template <typename T, bool HALF>
+cudaError_t rope_launch(Rope a, cudaStream_t st) {
   constexpr int W = 16 / sizeof(T);
-  a.lanes = a.half ? a.pairs / W + (a.d - 2 * a.pairs) / W : a.d / W;
-  const int here = 256 / a.lanes;
-  const unsigned g = (unsigned)((a.units + here - 1) / here);
-  if (a.half)
-    rope_kernel<T, U, true><<<g, 256, 0, st>>>(a);
-  else
-    rope_kernel<T, U, false><<<g, 256, 0, st>>>(a);
+  a.lanes = HALF ? a.pairs / W + (a.d - 2 * a.pairs) / W : a.d / W;
+  const int64_t tokens = (int64_t)a.B * a.n;
+  a.tile = tile_tokens(tokens, a.H + a.Hk, 256 / a.lanes);
+  // the table of a tile stays within 32 KB
+  constexpr int NP = HALF ? W : W / 2;
+  const int padded = (a.pairs + NP - 1) / NP * NP;
+  while (a.tile > 1 && (int64_t)a.tile * padded * 8 > 32768) a.tile /= 2;
+  const size_t smem = (size_t)a.tile * padded * 8;
+  const unsigned g = (unsigned)((tokens + a.tile - 1) / a.tile);
+  rope_kernel<T, HALF ? 2 : 4, HALF><<<g, 256, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -178,7 +216,7 @@ cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(z)>;
     constexpr int W = 16 / sizeof(T);
     bool vec = a.d % W == 0 && a.d / W <= 256 && (!a.half || a.pairs % W == 0) &&
-               (int64_t)a.B * a.n * (a.H + a.Hk) < (int64_t)1 << 31;
+               (int64_t)a.B * a.n < (int64_t)1 << 31;
     for (int i = 0; i < 3; ++i)
       vec = vec && a.qs[i] % W == 0 && a.qos[i] % W == 0 &&
             (!a.Hk || (a.ks[i] % W == 0 && a.kos[i] % W == 0));
@@ -188,12 +226,9 @@ cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st) {
       const int64_t total = (int64_t)a.B * a.n * (a.H + a.Hk) * (a.d - a.pairs);
       const int64_t blocks = (total + 255) / 256;
       rope_any_kernel<T><<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, st>>>(a);
-    } else if ((int64_t)a.B * a.n * (a.H + a.Hk) >= 152 * 128) {
-      rope_launch<T, 4>(a, st);
-    } else {
-      rope_launch<T, 1>(a, st);
+      return cudaGetLastError();
     }
-    return cudaGetLastError();
+    return a.half ? rope_launch<T, true>(a, st) : rope_launch<T, false>(a, st);
   });
 }
 

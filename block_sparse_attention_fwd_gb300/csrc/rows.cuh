@@ -7,12 +7,13 @@
 //
 // Also the 8-bit format: a group of consecutive elements of a row shares one
 // fp32 scale,
-//   scale = max(amax / qmax, 2^-126),   qmax = 127 (int8) or 448 (e4m3),
+//   scale = amax * fl32(1 / qmax), at least 2^-126 and at most the largest
+//           number whose product with qmax is finite; qmax = 127 (int8) or 448
+//           (e4m3),
 //   code  = round to nearest even of fl32(x * fl32(1 / scale)),
 //   value = code * scale.
-// The lower bound keeps 1 / scale finite, so an all-zero group needs no case
-// of its own; where scale * qmax would round past the largest fp32 number the
-// scale is one step lower.  A NaN or an infinity in the group makes the scale NaN (codes
+// The bounds keep 1 / scale and every value finite, so an all-zero group needs
+// no case of its own.  A NaN or an infinity in the group makes the scale NaN (codes
 // 0): the whole group loads as NaN instead of as a wrong number.
 #pragma once
 
@@ -25,6 +26,8 @@
 namespace bl {
 
 constexpr int kFmtInt8 = 1, kFmtE4m3 = 2;
+// The largest fp32 numbers whose products with 127 and 448 are finite.
+constexpr float kTopInt8 = 0x1.020406p+121f, kTopE4m3 = 0x1.249248p+119f;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -61,11 +64,33 @@ __device__ __forceinline__ Chunk<T> load8(const T* __restrict__ p, int valid) {
   return c;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], int valid) {
+// Two values rounded to T, in one 32-bit word (two words of fp32).
+template <typename T> struct Pair;
+template <> struct Pair<float> {
+  float2 v;
+  __device__ __forceinline__ Pair(float a, float b) : v(make_float2(a, b)) {}
+};
+template <> struct Pair<__half> {
+  __half2 v;
+  __device__ __forceinline__ Pair(float a, float b) : v(__floats2half2_rn(a, b)) {}
+};
+template <> struct Pair<__nv_bfloat16> {
+  __nv_bfloat162 v;
+  __device__ __forceinline__ Pair(float a, float b) : v(__floats2bfloat162_rn(a, b)) {}
+};
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> pack8(const float (&f)[8]) {
   Chunk<T> c;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c.e[i] = from_f32<T>(f[i]);
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<Pair<T>*>(&c)[i] = Pair<T>(f[2 * i], f[2 * i + 1]);
+  return c;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], int valid) {
+  const Chunk<T> c = pack8<T>(f);
   constexpr int NW = sizeof(Chunk<T>) / 16;
   if constexpr (VEC) {
     if (valid > 0) {
@@ -133,32 +158,34 @@ __device__ __forceinline__ void decode8(const Codes& c, float (&f)[8]) {
   }
 }
 
-// Largest magnitude of 8 values as bits: of non-negative floats the integer
-// order is the numeric one, with infinity and then every NaN on top, so a
-// maximum of bits lets no NaN slip through.
-__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-  return m;
+// Largest magnitude of 8 values, NaN if there is one among them; the sign of
+// the result is arbitrary (a maximum of magnitudes in one instruction).
+__device__ __forceinline__ float amax2(float a, float b) {
+  float d;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float amax8(const float (&f)[8]) {
+  return amax2(amax2(amax2(f[0], f[1]), amax2(f[2], f[3])),
+               amax2(amax2(f[4], f[5]), amax2(f[6], f[7])));
 }
 
-__device__ __forceinline__ float scale_of(uint32_t amax_bits, int fmt) {
-  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
-  const float qmax = fmt == kFmtInt8 ? 127.f : 448.f;
-  float s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits), qmax), 1.17549435e-38f);
-  if (isinf(__fmul_rn(s, qmax))) s = __uint_as_float(__float_as_uint(s) - 1u);
-  return s;
+// The scale of a group whose largest magnitude is |amax|.
+__device__ __forceinline__ float scale_of(float amax, int fmt) {
+  const bool i8 = fmt == kFmtInt8;
+  const float a = fabsf(amax);
+  float s = fmaxf(__fmul_rn(a, i8 ? 1.f / 127.f : 1.f / 448.f), 1.17549435e-38f);
+  s = fminf(s, i8 ? kTopInt8 : kTopE4m3);
+  return a <= 3.402823466e38f ? s : __uint_as_float(0x7fffffffu);
 }
 
 // The codes of 8 values of a group with this scale.  |x / scale| stays below
-// qmax (1 + 2^-22), which rounds to qmax, so nothing is clamped.  int8: adding
+// qmax (1 + 2^-21), which rounds to qmax, so nothing is clamped.  int8: adding
 // 1.5 * 2^23 rounds to an integer (ties to even) and leaves its two's
 // complement in the low mantissa byte.
 template <int FMT>
 __device__ __forceinline__ Codes encode8(const float (&f)[8], float scale) {
   Codes c{{0u, 0u}};
-  if (isnan(scale)) return c;
   const float inv = __frcp_rn(scale);
   if constexpr (FMT == kFmtInt8) {
     uint32_t b[8];
@@ -177,6 +204,7 @@ __device__ __forceinline__ Codes encode8(const float (&f)[8], float scale) {
                     << (16 * (i % 2));
     }
   }
+  if (isnan(scale)) c = Codes{{0u, 0u}};
   return c;
 }
 
@@ -190,33 +218,55 @@ __device__ __forceinline__ void decode8(int fmt, const Codes& c, float (&f)[8]) 
     decode8<kFmtE4m3>(c, f);
 }
 
-// Maximum over `width` neighbouring lanes (a power of two up to 32).
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int width) {
-  for (int o = width / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+// Over `width` neighbouring lanes (a power of two up to 32; uniform).
+__device__ __forceinline__ float lanes_amax(float v, int width) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < width) v = amax2(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 __device__ __forceinline__ float lanes_sum(float v, int width) {
-  for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Sum (maximum) over the block: warp partials through one of two slots of
-// `buf` (uint32 [2][32]), which the caller alternates, so that one barrier a
-// reduction is enough: a slot is written again only after the barrier of the
-// reduction in between.  Every thread gets the result, added in the same order.
-__device__ __forceinline__ float block_sum(float v, uint32_t (*buf)[32], int slot) {
+// Sum (largest magnitude) over the block: warp partials through one of two
+// slots of `buf`, which the caller alternates, so that one barrier a reduction
+// is enough: a slot is written again only after the barrier of the reduction
+// in between.  Every thread gets the result, formed in the same order.
+__device__ __forceinline__ float block_sum(float v, float (*buf)[32], int slot) {
   v = lanes_sum(v, 32);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) buf[slot][warp] = __float_as_uint(v);
-  __syncthreads();
-  return lanes_sum(lane < warps ? __uint_as_float(buf[slot][lane]) : 0.f, 32);
-}
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t (*buf)[32], int slot) {
-  v = lanes_max(v, 32);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) buf[slot][warp] = v;
   __syncthreads();
-  return lanes_max(lane < warps ? buf[slot][lane] : 0u, 32);
+  return lanes_sum(lane < warps ? buf[slot][lane] : 0.f, 32);
+}
+__device__ __forceinline__ float block_amax(float v, float (*buf)[32], int slot) {
+  v = lanes_amax(v, 32);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) buf[slot][warp] = v;
+  __syncthreads();
+  return lanes_amax(lane < warps ? buf[slot][lane] : 0.f, 32);
+}
+
+// Asynchronous copies of 4, 8 or 16 bytes from global to shared memory.  The
+// row kernels give every thread its own places, which it fills for rows ahead
+// and reads itself, so that waiting for its own copies is all it needs.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // A weight row of type T or fp32 (or none: ones).
@@ -248,6 +298,11 @@ cudaError_t with_type(int dtype, F&& f) {
   if (dtype == 0) return f((__nv_bfloat16*)nullptr);
   if (dtype == 1) return f((__half*)nullptr);
   return f((float*)nullptr);
+}
+
+// Shift from a column to its group (one group a row: any column to 0).
+inline int group_shift(int group) {
+  return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : 31;
 }
 
 inline int64_t groups_of(int64_t cols, int group) {

@@ -305,8 +305,8 @@ typedef enum { BL_INT8 = 1, BL_E4M3 = 2 } bl_format8;
 /* A [rows, cols] tensor in 8 bits: one fp32 scale for every `group`
  * consecutive elements of a row (32, 64 or 128; the last group of a row may
  * be cut), or one a row (group = 0).
- *   scale = max(amax / qmax, 2^-126), qmax = 127 (int8) or 448 (e4m3); one
- *           step lower where scale * qmax would overflow fp32
+ *   scale = amax * fl32(1 / qmax), at least 2^-126 and at most the largest number
+ *           whose product with qmax is finite; qmax = 127 (int8) or 448 (e4m3)
  *   code  = round to nearest even of fl32(x * fl32(1 / scale))
  *   value = code * scale
  * A group that holds a NaN or an infinity gets the scale NaN and loads as NaN.

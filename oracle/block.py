@@ -101,9 +101,11 @@ def save8(x, fmt, group):
         part = x[:, g * size:(g + 1) * size]
         bad = ~np.isfinite(part).all(axis=1)
         amax = np.abs(np.where(bad[:, None], 0, part)).max(axis=1)
-        scale = np.maximum(amax / qmax, np.float32(2.0 ** -126))
-        with np.errstate(over="ignore"):
-            scale = np.where(np.isinf(scale * qmax), np.nextafter(scale, np.float32(0)), scale)
+        scale = np.maximum(amax * (np.float32(1) / qmax), np.float32(2.0 ** -126))
+        top = np.float32(float(np.finfo(np.float32).max) / float(qmax))
+        if float(top) * float(qmax) > float(np.finfo(np.float32).max):
+            top = np.nextafter(top, np.float32(0))
+        scale = np.minimum(scale, top)
         q = np.where(bad[:, None], np.float32(0), part) * (np.float32(1) / scale)[:, None]
         assert q.dtype == np.float32
         codes[:, g * size:(g + 1) * size] = np.rint(q) if fmt == "int8" else round_e4m3(q)
