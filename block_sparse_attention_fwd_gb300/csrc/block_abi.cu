@@ -157,7 +157,7 @@ bl_status bl_rope(const bl_rope_args* r, void* stream) {
   if ((r->B > 1 && a.qos[0] < r->d) || (r->Hk && r->B > 1 && a.kos[0] < r->d))
     return BL_ERR_INVALID_ARG;
   if (r->positions_batch_stride != 0 &&
-      r->positions_batch_stride < (int64_t)r->n * r->axes)
+      r->positions_batch_stride != (int64_t)r->n * r->axes)
     return BL_ERR_INVALID_ARG;
   a.B = r->B; a.n = r->n; a.H = r->H; a.Hk = r->Hk; a.d = r->d;
   a.pairs = r->pairs; a.axes = r->axes;

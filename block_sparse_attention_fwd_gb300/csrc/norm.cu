@@ -286,51 +286,59 @@ __device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>&
   }
 }
 
+// Registers a thread of the backward may take (the launch counts on them).
+constexpr int bwd_regs(int lpr, int nv) { return nv >= 3 ? 128 : nv == 2 ? 96 : lpr ? 64 : 72; }
+
 // The backward of rows whose chunks are whole and aligned: one pass over the
-// rows.  A block stays for a run of rows, gridDim.x apart, and keeps its sums
-// of g_w in registers; g_y, h (or its codes and scales) and g_h of the next
-// S - 1 rows are on their way to shared memory meanwhile, each thread's
-// chunks into places of its own.
+// rows.  A block takes rows gridDim.x apart and keeps its sums of g_w in
+// registers; g_y, h (or its codes and scales) and g_h of the next S - 1 rows are
+// on their way to shared memory meanwhile, each thread's chunks into places of
+// its own.  With v = g_y rstd the formulas need the fewest operations,
+//   g_w += v h,  d = sum of (w v) h,  g_x = w v - (rstd^2 d / cols) h + g_h,
+// on packed pairs of fp32.
 template <typename T, int LPR, int NV, int FMT, int S>
-__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(NV == 4 ? 128 : 96)
+__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV))
     norm_bwd_ring_kernel(NormBwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
-  constexpr int HB = FMT ? 8 : CB;                   // of h's
+  constexpr int HB = FMT ? 12 : CB;                  // of h's: codes and a scale
+  constexpr bool KEEP_W = NV <= 2;                   // the weight stays in registers
   __shared__ float buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Rows<LPR> R;
   const int cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
   const int nt = blockDim.x;
-  // [stage][k] places of nt chunks: g_y, g_h, h, then (FMT) nt scales
-  const int stage_bytes = NV * nt * (2 * CB + HB + (FMT ? 4 : 0));
   const int64_t stride = (int64_t)gridDim.x * R.here;
-  auto place = [&](int s, int k) -> uint8_t* {
-    return ring + s * stage_bytes + k * nt * (2 * CB + HB + (FMT ? 4 : 0));
-  };
-  auto fetch = [&](int s, int64_t row) {
+  // [stage][k]: nt chunks of g_y, of g_h, of h (FMT: codes, then scales)
+  const int k_bytes = nt * (2 * CB + HB), stage_bytes = NV * k_bytes;
+  uint8_t* const mine = ring + threadIdx.x * 16;
+  bool has[NV];                                      // whether the thread has a chunk k
+#pragma unroll
+  for (int k = 0; k < NV; ++k) has[k] = (R.t + k * R.step) * 8 < cols;
+
+  auto fetch = [&](uint8_t* stage, int64_t row) {
     if (row < a.rows) {
+      const int64_t at = row * cols + R.t * 8;
+      const T* gy = static_cast<const T*>(a.g_y) + at;
+      const T* gh = static_cast<const T*>(a.g_h) + at;
+      const T* h = static_cast<const T*>(a.h) + at;
+      const uint8_t* codes = a.codes + at;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int col = (R.t + k * R.step) * 8;
-        if (col >= cols) continue;
-        uint8_t* p = place(s, k);
-        const int64_t at = row * cols + col;
+        if (!has[k]) continue;
+        uint8_t* p = stage + k * k_bytes;
+        const int off = k * R.step * 8;
 #pragma unroll
         for (int v = 0; v < CB / 16; ++v) {
-          copy_async<16>(p + (v * nt + threadIdx.x) * 16,
-                         reinterpret_cast<const uint8_t*>(a.g_y) + at * sizeof(T) + v * 16);
-          if (a.g_h)
-            copy_async<16>(p + nt * CB + (v * nt + threadIdx.x) * 16,
-                           reinterpret_cast<const uint8_t*>(a.g_h) + at * sizeof(T) + v * 16);
-          if constexpr (FMT == 0)
-            copy_async<16>(p + nt * 2 * CB + (v * nt + threadIdx.x) * 16,
-                           reinterpret_cast<const uint8_t*>(a.h) + at * sizeof(T) + v * 16);
+          constexpr int E = 16 / sizeof(T);
+          copy_async<16>(p + v * nt * 16, gy + off + v * E);
+          if (a.g_h) copy_async<16>(p + nt * CB + v * nt * 16, gh + off + v * E);
+          if constexpr (FMT == 0) copy_async<16>(p + nt * 2 * CB + v * nt * 16, h + off + v * E);
         }
         if constexpr (FMT != 0) {
-          copy_async<8>(p + nt * 2 * CB + threadIdx.x * 8, a.codes + at);
-          copy_async<4>(p + nt * (2 * CB + 8) + threadIdx.x * 4,
-                        a.scales + row * a.groups + (col >> a.shift));
+          copy_async<8>(p + nt * 2 * CB - (int)threadIdx.x * 8, codes + off);
+          copy_async<4>(p + nt * (2 * CB + 8) - (int)threadIdx.x * 12,
+                        a.scales + row * a.groups + ((R.t * 8 + off) >> a.shift));
         }
       }
     }
@@ -340,82 +348,101 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(NV == 4 ? 128 : 9
     Chunk<T> c;
 #pragma unroll
     for (int v = 0; v < CB / 16; ++v)
-      reinterpret_cast<uint4*>(&c)[v] =
-          *reinterpret_cast<const uint4*>(p + (v * nt + threadIdx.x) * 16);
+      reinterpret_cast<uint4*>(&c)[v] = *reinterpret_cast<const uint4*>(p + v * nt * 16);
     return c;
   };
-  auto unit = [&](const uint8_t* p, float rstd, float (&u)[8]) {
+  auto load_h = [&](const uint8_t* p, uint64_t (&h)[4]) {
     if constexpr (FMT == 0) {
-      const Chunk<T> c = chunk(p + nt * 2 * CB);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = to_f32(c.e[i]) * rstd;
+      unpack2(chunk(p + nt * 2 * CB), h);
     } else {
-      const uint2 raw = *reinterpret_cast<const uint2*>(p + nt * 2 * CB + threadIdx.x * 8);
-      const float s = *reinterpret_cast<const float*>(p + nt * (2 * CB + 8) + threadIdx.x * 4);
-      decode8<FMT>(Codes{{raw.x, raw.y}}, u);
+      const uint2 raw =
+          *reinterpret_cast<const uint2*>(p + nt * 2 * CB - (int)threadIdx.x * 8);
+      const float s =
+          *reinterpret_cast<const float*>(p + nt * (2 * CB + 8) - (int)threadIdx.x * 12);
+      float f[8];
+      decode8<FMT>(Codes{{raw.x, raw.y}}, f);
+      const uint64_t ss = f2_pack(s, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = u[i] * s * rstd;
+      for (int i = 0; i < 4; ++i) h[i] = fmul2(f2_pack(f[2 * i], f[2 * i + 1]), ss);
     }
   };
+  auto load_w = [&](int k, uint64_t (&w)[4]) {
+    float f[8];
+    const int col = (R.t + k * R.step) * 8;
+    load_weight8<T, true>(a.w, a.w_f32, col, has[k] ? 8 : 0, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+  };
 
-  float acc[NV][8];
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
   const int64_t first = (int64_t)blockIdx.x * R.here;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
-  int slot = 0, now = 0;
+  for (int s = 0; s < S - 1; ++s) fetch(mine + s * stage_bytes, first + s * stride + R.mine);
+  uint64_t acc[NV][4], w[KEEP_W ? NV : 1][4];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[k][i] = 0;
+    if constexpr (KEEP_W) load_w(k, w[k]);
+  }
+  int slot = 0, now = 0, fill = S - 1;
   float rstd = first + R.mine < a.rows ? a.rstd[first + R.mine] : 0.f;
   for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
     const int64_t row = row0 + R.mine;
-    const bool in = row < a.rows;
-    fetch(now == 0 ? S - 1 : now - 1, row + (S - 1) * stride);
+    const bool in = LPR == 0 || row < a.rows;
+    fetch(mine + fill * stage_bytes, row + (S - 1) * stride);
     const float rstd_next = row + stride < a.rows ? a.rstd[row + stride] : 0.f;
-    float wg[NV][8], u[NV][8];                       // wg: first the weight alone
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      load_weight8<T, true>(a.w, a.w_f32, col, cols - col, wg[k]);
-    }
     copy_wait<S - 1>();
-    float dot = 0.f;
+    const uint8_t* stage = mine + now * stage_bytes;
+    uint64_t wv[NV][4], h[NV][4], dot = 0;
+    const uint64_t rr = f2_pack(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      if (!in || col >= cols) continue;
-      const uint8_t* p = place(now, k);
-      const Chunk<T> gy = chunk(p);
-      unit(p, rstd, u[k]);
+      if (!in || !has[k]) continue;
+      const uint8_t* p = stage + k * k_bytes;
+      uint64_t g[4];
+      unpack2(chunk(p), g);
+      load_h(p, h[k]);
+      if constexpr (!KEEP_W) load_w(k, w[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float g = to_f32(gy.e[i]);
-        acc[k][i] = fmaf(g, u[k][i], acc[k][i]);
-        wg[k][i] *= g;
-        dot = fmaf(wg[k][i], u[k][i], dot);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t v = fmul2(g[i], rr);
+        acc[k][i] = ffma2(v, h[k][i], acc[k][i]);
+        wv[k][i] = fmul2(v, w[KEEP_W ? k : 0][i]);
+        dot = ffma2(wv[k][i], h[k][i], dot);
       }
     }
-    const float c = row_sum<LPR>(dot, buf, slot) * inv_cols;
+    float d0, d1;
+    f2_unpack(dot, d0, d1);
+    const float d = row_sum<LPR>(d0 + d1, buf, slot);
+    const float c = -(d * inv_cols) * (rstd * rstd);
+    const uint64_t cc = f2_pack(c, c);
+    T* out = static_cast<T*>(a.g_x) + row * cols + R.t * 8;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      if (!in || col >= cols) continue;
-      const uint8_t* p = place(now, k);
-      float g[8];
+      if (!in || !has[k]) continue;
+      uint64_t g[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = rstd * (wg[k][i] - u[k][i] * c);
+      for (int i = 0; i < 4; ++i) g[i] = ffma2(h[k][i], cc, wv[k][i]);
       if (a.g_h) {
-        const Chunk<T> e = chunk(p + nt * CB);
+        uint64_t e[4];
+        unpack2(chunk(stage + k * k_bytes + nt * CB), e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] += to_f32(e.e[i]);
+        for (int i = 0; i < 4; ++i) g[i] = fadd2(g[i], e[i]);
       }
-      store8<T, true>(static_cast<T*>(a.g_x) + row * cols + col, g, 8);
+      store8(out + k * R.step * 8, g);
     }
     rstd = rstd_next;
     now = now == S - 1 ? 0 : now + 1;
+    fill = fill == S - 1 ? 0 : fill + 1;
   }
-  if (a.partial) write_partial<LPR, NV, true>(a, R, acc, reinterpret_cast<float*>(ring));
+  if (a.partial) {
+    float sum[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f2_unpack(acc[k][i], sum[k][2 * i], sum[k][2 * i + 1]);
+    write_partial<LPR, NV, true>(a, R, sum, reinterpret_cast<float*>(ring));
+  }
 }
 
 // The backward of any other rows, straight from global memory.
@@ -514,18 +541,18 @@ __global__ void __launch_bounds__(1024) norm_gw_kernel(const float* __restrict__
 }
 
 // Lanes a row (0: the block), chunks a thread and threads of a launch over rows
-// of `cols` columns.  Up to 512 columns a warp holds whole rows; beyond, a block
-// of as few threads as hold the row with two chunks each, one chunk up to 1024
-// columns, where blocks are small.
+// of `cols` columns.  Up to warp_chunks chunks a warp holds whole rows and needs
+// no barrier; beyond, a block of as few threads as hold the row with two chunks
+// each, one chunk up to 1024 columns, where blocks are small.
 struct Plan {
   int lpr, nv, threads, here;
 };
-Plan plan(int64_t cols, int max_threads) {
+Plan plan(int64_t cols, int max_threads, int warp_chunks) {
   const int chunks = (int)((cols + 7) / 8);
   Plan p;
-  if (chunks <= 64) {
+  if (chunks <= warp_chunks) {
     p.lpr = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
-    p.nv = chunks <= 32 ? 1 : 2;
+    p.nv = (chunks + 31) / 32;
     p.threads = 256;
     p.here = 256 / p.lpr;
   } else {
@@ -561,7 +588,8 @@ void with_plan(const Plan& p, F&& f) {
   if (p.lpr == 8) f(Int<8>(), Int<1>());
   else if (p.lpr == 16) f(Int<16>(), Int<1>());
   else if (p.lpr == 32 && p.nv == 1) f(Int<32>(), Int<1>());
-  else if (p.lpr == 32) f(Int<32>(), Int<2>());
+  else if (p.lpr == 32 && p.nv == 2) f(Int<32>(), Int<2>());
+  else if (p.lpr == 32) f(Int<32>(), Int<3>());
   else if (p.nv == 1) f(Int<0>(), Int<1>());
   else if (p.nv == 2) f(Int<0>(), Int<2>());
   else f(Int<0>(), Int<4>());
@@ -577,11 +605,11 @@ cudaError_t allow_smem(K* kernel, size_t bytes) {
 
 template <typename T, int FMT8>
 cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
-  const Plan p = plan(a.cols, 1024);
+  const Plan p = plan(a.cols, 1024, 64);
   cudaError_t e = cudaSuccess;
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    if constexpr (N != 4) {
+    if constexpr (N <= 2) {
       const size_t stage = (size_t)N * p.threads * 2 * sizeof(Chunk<T>);
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
@@ -603,12 +631,9 @@ cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// Registers a thread of the backward's kernels (their caps).
-constexpr int bwd_regs(int lpr, int nv) { return nv == 4 ? 128 : lpr && nv == 1 ? 64 : 96; }
-
 template <typename T, int FMT>
 cudaError_t bwd(const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
-  const Plan p = plan(a.cols, 512);
+  const Plan p = plan(a.cols, 512, 96);
   cudaError_t e = cudaSuccess;
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
@@ -633,7 +658,7 @@ cudaError_t bwd(const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
 }  // namespace
 
 int norm_bwd_parts(int64_t rows, int64_t cols) {
-  const Plan p = plan(cols, 512);
+  const Plan p = plan(cols, 512, 96);
   return (int)grid(rows, p.here, resident(p.threads, bwd_regs(p.lpr, p.nv), 0));
 }
 

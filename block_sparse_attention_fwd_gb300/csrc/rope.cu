@@ -12,8 +12,10 @@
 // F_p = round(f_p / (2 pi) * 2^64), so position * F_p modulo 2^64 is the angle
 // modulo one turn: an integer product keeps what an fp32 product loses (at
 // position 10^6 and f = 1 half a step of the angle is 0.03 rad), without
-// fp64, whose rate here is low, and without a table to read.  The upper 32
-// bits, as a signed number of half turns, go to sincospi in fp32.
+// fp64, whose rate here is low, and without a table to read.  Its upper two
+// bits, rounded, are the quadrant; the rest, |x| <= pi / 4, goes through the
+// Taylor series of sine and cosine (to x^9 and x^8: the next terms are below
+// 2^-25), which is an order of magnitude less work than the general functions.
 //
 // The pass is bound by HBM: q and k once in, once out.  A block takes a tile of
 // tokens.  It forms the tile's sines and cosines once, in shared memory, and
@@ -27,13 +29,31 @@ namespace bl {
 
 namespace {
 
-__device__ __forceinline__ void turn(const Rope& a, const int32_t* pos, int p, float& c, float& s) {
+// (cos, sin) of an angle in 2^-32 turns.
+__device__ __forceinline__ float2 cos_sin(uint32_t angle) {
+  const uint32_t quadrant = (angle + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(angle - (quadrant << 30)) * 1.46291807926716e-9f;   // 2 pi / 2^32
+  const float x2 = x * x;
+  float s = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(s, x2, 1.f / 120.f);
+  s = fmaf(s, x2, -1.f / 6.f);
+  s = fmaf(s * x2, x, x);
+  float c = fmaf(x2, 1.f / 40320.f, -1.f / 720.f);
+  c = fmaf(c, x2, 1.f / 24.f);
+  c = fmaf(c, x2, -0.5f);
+  c = fmaf(c, x2, 1.f);
+  // a quarter turn takes (c, s) to (-s, c)
+  const float a = quadrant & 1 ? s : c, b = quadrant & 1 ? c : s;
+  return make_float2((quadrant + 1) & 2 ? -a : a, quadrant & 2 ? -b : b);
+}
+
+__device__ __forceinline__ float2 turn(const Rope& a, const int32_t* pos, int p) {
   int axis = 0;
 #pragma unroll
   for (int e = 0; e < 3; ++e) axis += p >= a.ends[e] ? 1 : 0;
   const uint64_t angle = (uint64_t)(int64_t)pos[axis] * a.freqs[p];
-  sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-  if (a.inverse) s = -s;
+  const uint32_t hi = (uint32_t)(angle >> 32);
+  return cos_sin(a.inverse ? 0u - hi : hi);
 }
 
 template <typename T, int U, bool HALF>
@@ -99,14 +119,22 @@ __global__ void __launch_bounds__(256) rope_kernel(Rope a) {
   };
 
   load();
-  for (int x = threadIdx.x; x < toks * a.pairs; x += 256) {
-    const int t = x / a.pairs, p = x - t * a.pairs;
-    const uint32_t b = ((uint32_t)tok0 + t) / (uint32_t)a.n;
-    const uint32_t i = (uint32_t)tok0 + t - b * (uint32_t)a.n;
-    float2 cs;
-    turn(a, a.pos + b * a.pos_batch + (int64_t)i * a.axes, p, cs.x, cs.y);
-    const int l = p / NP, j = p % NP;
-    reinterpret_cast<float2*>(table)[((t * planes + j / 2) * holders + l) * 2 + j % 2] = cs;
+  {
+    int t = threadIdx.x / a.pairs, p = threadIdx.x - t * a.pairs;
+    const int t_step = 256 / a.pairs, p_step = 256 - t_step * a.pairs;
+    while (t < toks) {
+      const uint32_t token = (uint32_t)tok0 + t;
+      const int64_t at_pos = a.pos_batch ? (int64_t)token : (int64_t)(token % (uint32_t)a.n);
+      const float2 cs = turn(a, a.pos + at_pos * a.axes, p);
+      const int l = p / NP, j = p % NP;
+      reinterpret_cast<float2*>(table)[((t * planes + j / 2) * holders + l) * 2 + j % 2] = cs;
+      t += t_step;
+      p += p_step;
+      if (p >= a.pairs) {
+        p -= a.pairs;
+        ++t;
+      }
+    }
   }
   __syncthreads();
   while (at[0] >= 0) {
@@ -174,8 +202,8 @@ __global__ void __launch_bounds__(256) rope_any_kernel(Rope a) {
       continue;
     }
     const int e0 = a.half ? p : 2 * p, e1 = a.half ? p + a.pairs : 2 * p + 1;
-    float c, s;
-    turn(a, a.pos + b * a.pos_batch + i * a.axes, p, c, s);
+    const float2 cs = turn(a, a.pos + b * a.pos_batch + i * a.axes, p);
+    const float c = cs.x, s = cs.y;
     const float u = to_f32(in[e0]), v = to_f32(in[e1]);
     out[e0] = from_f32<T>(u * c - v * s);
     out[e1] = from_f32<T>(u * s + v * c);
@@ -183,11 +211,11 @@ __global__ void __launch_bounds__(256) rope_any_kernel(Rope a) {
 }
 
 // Tokens of a block's tile: enough (token, head) units that every thread gets
-// several, as far as there are tokens for two blocks an SM.
+// several, as far as there are tokens for four blocks an SM.
 int tile_tokens(int64_t tokens, int heads, int groups) {
   int64_t tile = (8 * groups + heads - 1) / heads;
   if (tile > 32) tile = 32;
-  const int64_t fill = tokens / (2 * 152);
+  const int64_t fill = tokens / (4 * 152);
   if (tile > fill) tile = fill;
   return tile < 1 ? 1 : (int)tile;
 }

@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "common.cuh"
+
 namespace bl {
 
 constexpr int kFmtInt8 = 1, kFmtE4m3 = 2;
@@ -86,6 +88,26 @@ __device__ __forceinline__ Chunk<T> pack8(const float (&f)[8]) {
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<Pair<T>*>(&c)[i] = Pair<T>(f[2 * i], f[2 * i + 1]);
   return c;
+}
+
+// The chunk as four packed pairs of fp32 (f2_* in common.cuh).
+template <typename T>
+__device__ __forceinline__ void unpack2(const Chunk<T>& c, uint64_t (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack(to_f32(c.e[2 * i]), to_f32(c.e[2 * i + 1]));
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* __restrict__ p, const uint64_t (&f)[4]) {
+  Chunk<T> c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f[i], lo, hi);
+    reinterpret_cast<Pair<T>*>(&c)[i] = Pair<T>(lo, hi);
+  }
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(c) / 16; ++i)
+    reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&c)[i];
 }
 
 template <typename T, bool VEC>

@@ -382,8 +382,8 @@ bl_status bl_rms_norm_bwd(int64_t rows, int64_t cols, int dtype, const void* g_y
  *   q, q_out  [B, n, H, d] of dtype, k, k_out [B, n, Hk, d]; Hk = 0: no k.
  *             Element strides {batch, token, head}, the dim stride is 1.
  *             q_out may be q itself (with the same strides), likewise k_out.
- *   positions [B, n, axes] int32, contiguous; the batches are
- *             positions_batch_stride elements apart (0: all share the first).
+ *   positions [B, n, axes] int32, contiguous: positions_batch_stride is n * axes,
+ *             or 0 for [n, axes] that all batches share.
  *   freqs     [pairs] uint64 on the device: round(f_p / (2 pi) * 2^64) modulo
  *             2^64, f_p in radians a position.
  * 1 <= pairs <= d / 2.  Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
