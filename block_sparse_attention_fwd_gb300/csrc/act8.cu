@@ -3,6 +3,8 @@
 // loading, and the expansion of an attention's q, k and v into its backward's
 // workspace.  The format is in rows.cuh.  All passes are bound by HBM: x once
 // in, one byte an element and the scales out, or the other way round.
+#include <type_traits>
+
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -165,24 +167,42 @@ __global__ void __launch_bounds__(256) act_load_flat_kernel(const uint8_t* __res
   }
 }
 
-template <typename T, bool VEC, int FMT>
+// Rows of any width: codes and values lie back to back whatever the width, so a
+// thread still moves 8 of them with vector instructions (VEC).  WHOLE: the width
+// is a multiple of 8, so the 8 share a scale; otherwise the scale is looked up
+// anew where a row or a group begins.
+template <typename T, bool VEC, bool WHOLE, int FMT>
 __global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
-  const int64_t per_row = (a.cols + 7) / 8;
-  const int64_t total = a.rows * per_row;
-  const int shift = a.group ? __ffs(a.group) - 1 : 62;
-  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < total;
-       x += (int64_t)gridDim.x * blockDim.x) {
-    int64_t row, j;
-    div_mod(x, per_row, row, j);
-    const int64_t col = j * 8;
-    const int valid = (int)min((int64_t)8, a.cols - col);
-    const Codes c = load_codes<VEC>(a.codes + row * a.cols + col, valid);
-    const float scale = a.scales[row * a.groups + (col >> shift)];
+  const int64_t total = a.rows * a.cols;
+  const int shift = group_shift(a.group);
+  const int64_t stride = (int64_t)gridDim.x * 256 * 8;
+  for (int64_t x = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; x < total; x += stride) {
+    int64_t row, col;
+    div_mod(x, a.cols, row, col);
+    const int valid = (int)min((int64_t)8, total - x);
+    const Codes c = VEC && valid == 8 ? load_codes<true>(a.codes + x, 8)
+                                      : load_codes<false>(a.codes + x, valid);
     float f[8];
     decode8<FMT>(c, f);
+    float scale = a.scales[row * a.groups + (col >> shift)];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= scale;
-    store8<T, VEC>(static_cast<T*>(a.x) + row * a.cols + col, f, valid);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (!WHOLE) {
+        if (i > 0 && i < valid && (col == a.cols || (col & ((1ll << shift) - 1)) == 0)) {
+          if (col == a.cols) {
+            col = 0;
+            ++row;
+          }
+          scale = a.scales[row * a.groups + (col >> shift)];
+        }
+        ++col;
+      }
+      f[i] *= scale;
+    }
+    if (VEC && valid == 8)
+      store8<T, true>(static_cast<T*>(a.x) + x, f, 8);
+    else
+      store8<T, false>(static_cast<T*>(a.x) + x, f, valid);
   }
 }
 
@@ -233,6 +253,10 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
   // one scale a row of 32, 64 or 128 elements is one scale a group
   if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
+  if (!a.group) {
+    const cudaError_t e = launch_row_save(dtype, a, st);
+    if (e != cudaErrorNotSupported) return e;
+  }
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
@@ -276,7 +300,7 @@ cudaError_t launch_act_load(int dtype, const ActLoad& in, cudaStream_t st) {
   if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
-    const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.codes, 8);
+    const bool vec = aligned_to(a.x, 16) && aligned_to(a.codes, 8);
     const int shift = aligned_to(a.x, 16) && aligned_to(a.codes, 16)
                           ? flat_shift(a.cols, a.group) : -1;
     if (shift >= 0) {
@@ -291,13 +315,20 @@ cudaError_t launch_act_load(int dtype, const ActLoad& in, cudaStream_t st) {
                                                                      shift);
       return cudaGetLastError();
     }
-    const unsigned g = blocks_for((a.rows * ((a.cols + 7) / 8) + 255) / 256);
+    const unsigned g = blocks_for((a.rows * a.cols + 2047) / 2048);
+    auto launch = [&](auto fmt) {
+      constexpr int F = decltype(fmt)::value;
+      if (!vec)
+        act_load_kernel<T, false, false, F><<<g, 256, 0, st>>>(a);
+      else if (a.cols % 8 == 0)
+        act_load_kernel<T, true, true, F><<<g, 256, 0, st>>>(a);
+      else
+        act_load_kernel<T, true, false, F><<<g, 256, 0, st>>>(a);
+    };
     if (a.fmt == kFmtInt8)
-      vec ? act_load_kernel<T, true, kFmtInt8><<<g, 256, 0, st>>>(a)
-          : act_load_kernel<T, false, kFmtInt8><<<g, 256, 0, st>>>(a);
+      launch(std::integral_constant<int, kFmtInt8>());
     else
-      vec ? act_load_kernel<T, true, kFmtE4m3><<<g, 256, 0, st>>>(a)
-          : act_load_kernel<T, false, kFmtE4m3><<<g, 256, 0, st>>>(a);
+      launch(std::integral_constant<int, kFmtE4m3>());
     return cudaGetLastError();
   });
 }

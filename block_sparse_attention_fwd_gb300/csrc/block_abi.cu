@@ -26,6 +26,16 @@ bool act8_ok(const bl_act8* a, int64_t rows) {
 }
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Bytes of the scratch that lets the attention backward's work items be single
+// query heads, or 0 where it does not pay: without groups there is nothing to
+// split, and with an item for every SM the extra passes over fp32 tiles cost
+// more than the idle SMs do.
+size_t part_bytes(const bl::Shape& sh) {
+  if (sh.H == sh.Hk || sh.block_q != 128 || sh.block_k != 128) return 0;
+  if ((int64_t)sh.T_c * sh.Hk * sh.B >= 152) return 0;
+  return 2 * (size_t)sh.B * sh.n * sh.H * sh.d * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -173,7 +183,8 @@ size_t bl_attn_bwd_act8_workspace_bytes(const bl_shape* shape) {
   bl::Shape sh;
   if (bl::check_shape(shape, &sh) != BL_OK || sh.strided) return 0;
   const size_t tokens = (size_t)sh.B * sh.n * sh.d * 2;
-  return up256(bl_bwd_workspace_bytes(shape)) + up256(tokens * sh.H) + 2 * up256(tokens * sh.Hk);
+  return up256(bl_bwd_workspace_bytes(shape)) + up256(tokens * sh.H) +
+         2 * up256(tokens * sh.Hk) + part_bytes(sh);
 }
 
 bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_act8* k8,
@@ -205,6 +216,7 @@ bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_ac
   uint8_t* q = ws + up256(bl_bwd_workspace_bytes(shape));
   uint8_t* k = q + up256(tokens * sh.H);
   uint8_t* v = k + up256(tokens * sh.Hk);
+  float* part = part_bytes(sh) ? reinterpret_cast<float*>(v + up256(tokens * sh.Hk)) : nullptr;
   bl::Expand e{};
   uint8_t* out[3] = {q, k, v};
   for (int i = 0; i < 3; ++i) {
@@ -223,7 +235,7 @@ bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_ac
       sh, q, k, v, o, o8 ? static_cast<const uint8_t*>(o8->codes) : nullptr,
       o8 ? o8->scales : nullptr, q8->format, g_o, lse, scale, lists ? lists->q_idx : nullptr,
       lists ? lists->q_cnt : nullptr, g_q, g_k, g_v, ws_D, ws_dq, ws_sub, ws_status,
-      (cudaStream_t)stream));
+      (cudaStream_t)stream, part));
 }
 
 }  // extern "C"

@@ -163,7 +163,7 @@ cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const
                             int o_fmt, const void* g_o, const float* lse, float scale,
                             const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
                             void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
-                            int32_t* ws_status, cudaStream_t st) {
+                            int32_t* ws_status, cudaStream_t st, float* part) {
   const int64_t rows = (int64_t)sh.B * sh.n * sh.H;
   const int fmt = o_codes ? o_fmt : 0;
   auto pre = sh.d == 64 ? (fmt == 0          ? launch_pre<64, 0>
@@ -176,7 +176,7 @@ cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_bwd_tc(sh, q, k, v, g_o, lse, ws_D, q_idx, q_cnt, g_k, g_v, ws_dq, ws_sub, ws_status,
-                    scale, st);
+                    scale, st, part);
   if (e != cudaSuccess) return e;
   const int64_t n4 = rows * sh.d / 4;
   unsigned cblocks = (unsigned)((n4 + 255) / 256);

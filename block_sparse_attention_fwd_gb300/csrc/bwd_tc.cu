@@ -204,7 +204,12 @@ __device__ __forceinline__ bool failed(const int* f) { return *(volatile const i
 // tiles of the mask, computed as 128 x 128 tiles with the dropped quarters'
 // P^T set to 0).
 // WL: the launch runs under a non-default wait limit (bl_set_wait_limit).
-template <int D, bool MASKED, bool SUB, bool WL>
+// PART: the items are (key tile, query head) instead of (key tile, kv head):
+// sh.Hk is sh.H, K and V are read at head hk / kv_div, and dV and s dK of an
+// item go as fp32 tiles to g_v and g_k [B,n,H,D] (contiguous), which
+// sum_heads_kernel adds up over each group.  It keeps the GPU busy where few
+// key tiles and kv heads leave most SMs without an item.
+template <int D, bool MASKED, bool SUB, bool WL, bool PART>
 __global__ void __launch_bounds__(512, 1) bwd_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(512, 1) bwd_tc_kernel(
     const float* __restrict__ Dv, const int32_t* __restrict__ q_idx,
     const int32_t* __restrict__ q_cnt, __nv_bfloat16* __restrict__ g_k,
     __nv_bfloat16* __restrict__ g_v, int32_t* __restrict__ status, Shape sh, float scale,
-    float scale_log2, uint64_t wait_ns) {
+    float scale_log2, uint64_t wait_ns, int kv_div) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -350,9 +355,11 @@ __global__ void __launch_bounds__(512, 1) bwd_tc_kernel(
             if (lane == 0) {
               mbar_expect_tx(&bars.kv_full, 2 * C::TILE);
               for (int c = 0; c < C::CHK; ++c) {
-                tma_load_4d(sm + C::OFF_K + c * C::CHUNK, &tm_k, &bars.kv_full, c * 64, it.hk,
+                tma_load_4d(sm + C::OFF_K + c * C::CHUNK, &tm_k, &bars.kv_full, c * 64,
+                            PART ? it.hk / kv_div : it.hk,
                             it.j * 128, it.b);
-                tma_load_4d(sm + C::OFF_V + c * C::CHUNK, &tm_v, &bars.kv_full, c * 64, it.hk,
+                tma_load_4d(sm + C::OFF_V + c * C::CHUNK, &tm_v, &bars.kv_full, c * 64,
+                            PART ? it.hk / kv_div : it.hk,
                             it.j * 128, it.b);
               }
             }
@@ -732,45 +739,78 @@ __global__ void __launch_bounds__(512, 1) bwd_tc_kernel(
         uint8_t* wstage = sm + C::OFF_DS + half * C::CHUNK + q4 * 32 * 128;   // 1024-aligned
         uint8_t* srow = wstage + lane * 128;
         const int row0 = ie.j * 128 + q4 * 32;
+if constexpr (PART) {
 #pragma unroll
-        for (int hc = 0; hc < C::CHK; ++hc) {       // 64 columns = one 128-byte row
-          if (hc > 0) {                               // the previous store has read the rows
-            if (lane == 0) bulk_wait_read0();
-            __syncwarp();
-          }
-#pragma unroll
-          for (int c32 = 0; c32 < 2; ++c32) {
+          for (int c32 = 0; c32 < D / 32; ++c32) {    // 32 fp32 columns = one 128-byte row
+            if (c32 > 0) {
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
+            }
             uint32_t a[32];
-            tmem_ld32(lane_base + col + hc * 64 + c32 * 32, a);
+            tmem_ld32(lane_base + col + c32 * 32, a);
             tmem_ld_wait();
 #pragma unroll
-            for (int x8 = 0; x8 < 4; ++x8) {
-              const int chunk = c32 * 4 + x8;
-              *reinterpret_cast<uint4*>(srow + ((chunk ^ (lane & 7)) << 4)) = make_uint4(
-                  pack_bf16(__uint_as_float(a[8 * x8]) * mul, __uint_as_float(a[8 * x8 + 1]) * mul),
-                  pack_bf16(__uint_as_float(a[8 * x8 + 2]) * mul,
-                            __uint_as_float(a[8 * x8 + 3]) * mul),
-                  pack_bf16(__uint_as_float(a[8 * x8 + 4]) * mul,
-                            __uint_as_float(a[8 * x8 + 5]) * mul),
-                  pack_bf16(__uint_as_float(a[8 * x8 + 6]) * mul,
-                            __uint_as_float(a[8 * x8 + 7]) * mul));
+            for (int x4 = 0; x4 < 8; ++x4)
+              *reinterpret_cast<float4*>(srow + ((x4 ^ (lane & 7)) << 4)) = make_float4(
+                  __uint_as_float(a[4 * x4]) * mul, __uint_as_float(a[4 * x4 + 1]) * mul,
+                  __uint_as_float(a[4 * x4 + 2]) * mul, __uint_as_float(a[4 * x4 + 3]) * mul);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < sh.n) {
+              tma_store_4d(half == 0 ? &tm_gv : &tm_gk, wstage, c32 * 32, ie.hk, row0, ie.b);
+              bulk_commit();
             }
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0 && row0 < sh.n) {
-            tma_store_4d(half == 0 ? &tm_gv : &tm_gk, wstage, hc * 64, ie.hk, row0, ie.b);
-            bulk_commit();
+        } else {
+#pragma unroll
+          for (int hc = 0; hc < C::CHK; ++hc) {       // 64 columns = one 128-byte row
+            if (hc > 0) {                               // the previous store has read the rows
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int c32 = 0; c32 < 2; ++c32) {
+              uint32_t a[32];
+              tmem_ld32(lane_base + col + hc * 64 + c32 * 32, a);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x8 = 0; x8 < 4; ++x8) {
+                const int chunk = c32 * 4 + x8;
+                *reinterpret_cast<uint4*>(srow + ((chunk ^ (lane & 7)) << 4)) = make_uint4(
+                    pack_bf16(__uint_as_float(a[8 * x8]) * mul, __uint_as_float(a[8 * x8 + 1]) * mul),
+                    pack_bf16(__uint_as_float(a[8 * x8 + 2]) * mul,
+                              __uint_as_float(a[8 * x8 + 3]) * mul),
+                    pack_bf16(__uint_as_float(a[8 * x8 + 4]) * mul,
+                              __uint_as_float(a[8 * x8 + 5]) * mul),
+                    pack_bf16(__uint_as_float(a[8 * x8 + 6]) * mul,
+                              __uint_as_float(a[8 * x8 + 7]) * mul));
+              }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < sh.n) {
+              tma_store_4d(half == 0 ? &tm_gv : &tm_gk, wstage, hc * 64, ie.hk, row0, ie.b);
+              bulk_commit();
+            }
           }
         }
         store_pending = true;
       } else {
         const int row = ie.j * 128 + r;
-        uint4* dst = reinterpret_cast<uint4*>(
-            half == 0 ? g_v + bshd(sh.vs, ie.b, row, ie.hk) : g_k + bshd(sh.ks, ie.b, row, ie.hk));
-        if (row < sh.n) {
+        if constexpr (PART) {
+          float4* dst = reinterpret_cast<float4*>(half == 0 ? g_v : g_k) +
+                        (((int64_t)ie.b * sh.n + row) * sh.H + ie.hk) * (D / 4);
+          if (row < sh.n) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / 4; ++c) dst[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(half == 0 ? g_v + bshd(sh.vs, ie.b, row, ie.hk)
+                                                          : g_k + bshd(sh.ks, ie.b, row, ie.hk));
+          if (row < sh.n) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
       fence_before_sync();
@@ -882,30 +922,64 @@ int sm_count() {
   return count[dev];
 }
 
-template <int D, bool MASKED, bool SUB, bool WL>
+// g_k and g_v (blockIdx.y) from the query heads' parts: the sum over the G heads
+// of a group, in their order, rounded to bf16.  Thread = 4 elements of one kv
+// head's row; row4 = D / 4.
+__global__ void __launch_bounds__(256) sum_heads_kernel(const float4* __restrict__ part_k,
+                                                        const float4* __restrict__ part_v,
+                                                        uint2* __restrict__ g_k,
+                                                        uint2* __restrict__ g_v, int64_t n4, int G,
+                                                        int row4) {
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= n4) return;
+  const float4* in = (blockIdx.y ? part_v : part_k) + (x / row4) * G * row4 + x % row4;
+  float4 s = in[0];
+  for (int g = 1; g < G; ++g) {
+    const float4 p = in[(int64_t)g * row4];
+    s.x += p.x;
+    s.y += p.y;
+    s.z += p.z;
+    s.w += p.w;
+  }
+  (blockIdx.y ? g_v : g_k)[x] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// part: with PART, fp32 [2][B,n,H,D] for dK's and dV's tiles of each query head.
+template <int D, bool MASKED, bool SUB, bool WL, bool PART>
 cudaError_t launch_t(const Shape& sh, const void* q, const void* k, const void* v, const void* g_o,
                      const float* lse, const float* Dv, const int32_t* q_idx,
                      const int32_t* q_cnt, void* g_k, void* g_v, float* dq_acc, int32_t* status,
-                     float scale, cudaStream_t st) {
+                     float scale, float* part, cudaStream_t st) {
   using C = Cfg<D>;
+  float* part_v = part + (size_t)sh.B * sh.n * sh.H * D;
   CUtensorMap mq, mk, mv, mg, md, mgk, mgv;
   if (!make_bshd_map(&mq, q, sh.B, sh.n, sh.H, D, 128, sh.qs) ||
       !make_bshd_map(&mg, g_o, sh.B, sh.n, sh.H, D, 128, sh.os) ||
       !make_bshd_map(&mk, k, sh.B, sh.n, sh.Hk, D, 128, sh.ks) ||
       !make_bshd_map(&mv, v, sh.B, sh.n, sh.Hk, D, 128, sh.vs) ||
-      !make_bshd_map(&mgk, g_k, sh.B, sh.n, sh.Hk, D, 32, sh.ks) ||
-      !make_bshd_map(&mgv, g_v, sh.B, sh.n, sh.Hk, D, 32, sh.vs) ||
+      !(PART ? make_bshd_map_f32(&mgk, part, sh.B, sh.n, sh.H, D, 32)
+             : make_bshd_map(&mgk, g_k, sh.B, sh.n, sh.Hk, D, 32, sh.ks)) ||
+      !(PART ? make_bshd_map_f32(&mgv, part_v, sh.B, sh.n, sh.H, D, 32)
+             : make_bshd_map(&mgv, g_v, sh.B, sh.n, sh.Hk, D, 32, sh.vs)) ||
       !make_bshd_map_f32(&md, dq_acc, sh.B, sh.n, sh.H, D, 32))
     return cudaErrorInvalidValue;
   const int smem = C::BYTES + 1024;
-  auto kern = bwd_tc_kernel<D, MASKED, SUB, WL>;
+  auto kern = bwd_tc_kernel<D, MASKED, SUB, WL, PART>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)sh.T_c * sh.Hk * sh.B;
+  Shape walk = sh;
+  if (PART) walk.Hk = sh.H;
+  const int64_t items = (int64_t)walk.T_c * walk.Hk * walk.B;
   const int grid = (int)(items < sm_count() ? items : sm_count());
   kern<<<grid, 512, smem, st>>>(mq, mk, mv, mg, md, mgk, mgv, lse, Dv, q_idx, q_cnt,
-                                (__nv_bfloat16*)g_k, (__nv_bfloat16*)g_v, status, sh, scale,
-                                scale * kLog2e, wait_limit_ns());
+                                (__nv_bfloat16*)(PART ? (void*)part : g_k),
+                                (__nv_bfloat16*)(PART ? (void*)part_v : g_v), status, walk, scale,
+                                scale * kLog2e, wait_limit_ns(), sh.H / sh.Hk);
+  e = cudaGetLastError();
+  if (!PART || e != cudaSuccess) return e;
+  const int64_t n4 = (int64_t)sh.B * sh.n * sh.Hk * (D / 4);
+  sum_heads_kernel<<<dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, st>>>(
+      (const float4*)part, (const float4*)part_v, (uint2*)g_k, (uint2*)g_v, n4, sh.H / sh.Hk, D / 4);
   return cudaGetLastError();
 }
 
@@ -999,7 +1073,7 @@ cudaError_t launch_bwd_tc(const Shape& sh, const void* q, const void* k, const v
                           const void* g_o, const float* lse, const float* Dv,
                           const int32_t* q_idx, const int32_t* q_cnt, void* g_k, void* g_v,
                           float* dq_acc, int32_t* sub_ws, int32_t* status, float scale,
-                          cudaStream_t st) {
+                          cudaStream_t st, float* part) {
   const bool masked = sh.causal || sh.window;
   const bool sub = !(sh.block_q == 128 && sh.block_k == 128);
   const Shape s128 = tiles128(sh);
@@ -1017,9 +1091,15 @@ cudaError_t launch_bwd_tc(const Shape& sh, const void* q, const void* k, const v
   }
   auto run = [&](auto wl_c) {
     auto go = [&](auto d_c, auto m_c, auto s_c) {
-      return launch_t<decltype(d_c)::value, decltype(m_c)::value, decltype(s_c)::value,
-                      decltype(wl_c)::value>(s128, q, k, v, g_o, lse, Dv, q_idx, q_cnt, g_k, g_v,
-                                             dq_acc, status, scale, st);
+      constexpr int D = decltype(d_c)::value;
+      constexpr bool M = decltype(m_c)::value, SUB = decltype(s_c)::value;
+      constexpr bool WL = decltype(wl_c)::value;
+      if constexpr (!SUB && !WL)
+        if (part)
+          return launch_t<D, M, false, false, true>(s128, q, k, v, g_o, lse, Dv, q_idx, q_cnt,
+                                                    g_k, g_v, dq_acc, status, scale, part, st);
+      return launch_t<D, M, SUB, WL, false>(s128, q, k, v, g_o, lse, Dv, q_idx, q_cnt, g_k, g_v,
+                                            dq_acc, status, scale, nullptr, st);
     };
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;

@@ -36,13 +36,15 @@ cudaError_t launch_bwd(const Shape& sh, const void* q, const void* k, const void
 
 // tcgen05 dK/dV/dQ pass (head dim 64 or 128).  Shapes with 64-wide tiles run
 // as 128 x 128 tiles whose lists (built in sub_ws) carry 64 x 64 quarter masks.
+// part (contiguous tensors, 128 x 128 tiles): fp32 [2][B,n,H,d] scratch, work
+// items of single query heads whose dK and dV are summed over the groups after.
 bool bwd_tc_supported(const Shape& sh);
 size_t bwd_sub_lists_bytes(const Shape& sh);
 cudaError_t launch_bwd_tc(const Shape& sh, const void* q, const void* k, const void* v,
                           const void* g_o, const float* lse, const float* Dv,
                           const int32_t* q_idx, const int32_t* q_cnt, void* g_k, void* g_v,
                           float* dq_acc, int32_t* sub_ws, int32_t* status, float scale,
-                          cudaStream_t st);
+                          cudaStream_t st, float* part = nullptr);
 
 // tcgen05 forward with tile statistics for 128 x 128 tiles (head dim 64 or
 // 128).  logw != nullptr also writes the tile weights [B,H,T_r,T_c]; with
@@ -111,6 +113,9 @@ struct ActLoad {
   int group, fmt;
 };
 cudaError_t launch_act_save(int dtype, const ActSave& a, cudaStream_t st);
+// With one scale a row, where the row kernels of norm.cu take the rows
+// (cudaErrorNotSupported, and nothing launched, where they do not).
+cudaError_t launch_row_save(int dtype, const ActSave& a, cudaStream_t st);
 cudaError_t launch_act_load(int dtype, const ActLoad& a, cudaStream_t st);
 // Codes of up to three tensors [rows, d] with one scale a row, to bf16.
 struct Expand {
@@ -128,7 +133,7 @@ cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const
                             int o_fmt, const void* g_o, const float* lse, float scale,
                             const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
                             void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
-                            int32_t* ws_status, cudaStream_t st);
+                            int32_t* ws_status, cudaStream_t st, float* part = nullptr);
 
 // Rotary positions (rope.cu).  Strides {batch, token, head} in elements.
 struct Rope {

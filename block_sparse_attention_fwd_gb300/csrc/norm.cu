@@ -9,6 +9,8 @@
 //
 // Sums run in fp32; y comes from the unrounded h, so it is rounded once.
 // The passes are bound by HBM: each input read once, each output written once.
+#include <atomic>
+
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -131,8 +133,9 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
 // GPU once: a block takes rows gridDim.x apart, and x and r of the next S - 1
 // of them are on their way to shared memory meanwhile, each thread's chunks into
 // places of its own.  Loading straight into registers instead leaves the
-// memory idle while a row is reduced.
-template <typename T, int LPR, int NV, int FMT8, int S>
+// memory idle while a row is reduced.  NORM = false only saves x in 8 bits with
+// one scale a row: the same walk without the norm.
+template <typename T, int LPR, int NV, int FMT8, int S, bool NORM>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   __shared__ float buf[2][32];
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
 #pragma unroll
           for (int v = 0; v < CB / 16; ++v) {
             copy_async<16>(p + v * nt * 16, x + col + v * (16 / sizeof(T)));
-            if (a.r) copy_async<16>(p + nt * CB + v * nt * 16, r + col + v * (16 / sizeof(T)));
+            if (NORM && a.r) copy_async<16>(p + nt * CB + v * nt * 16, r + col + v * (16 / sizeof(T)));
           }
         }
       }
@@ -176,10 +179,12 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
   float w[NV][8];
+  if constexpr (NORM) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int col = (R.t + k * R.step) * 8;
-    load_weight8<T, true>(a.w, a.w_f32, col, cols - col, w[k]);
+    for (int k = 0; k < NV; ++k) {
+      const int col = (R.t + k * R.step) * 8;
+      load_weight8<T, true>(a.w, a.w_f32, col, cols - col, w[k]);
+    }
   }
   int slot = 0, now = 0;
   for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
@@ -197,33 +202,40 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
         const Chunk<T> x = chunk(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x.e[i]);
-        if (a.r) {
+        if (NORM && a.r) {
           const Chunk<T> r = chunk(p + nt * CB);
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r.e[i]);
           if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * cols + col, h[k], 8);
         }
+        if constexpr (NORM) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+          for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
       }
     }
-    ss = row_sum<LPR>(ss, buf, slot);
-    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
-    if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
+    float rstd = 1.f;
+    if constexpr (NORM) {
+      ss = row_sum<LPR>(ss, buf, slot);
+      rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+      if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
+    }
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = (R.t + k * R.step) * 8;
       const int valid = in && col < cols ? 8 : 0;
+      if constexpr (NORM) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[k][i];
-      if (a.y) store8<T, true>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
+        for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[k][i];
+        if (a.y) store8<T, true>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
+      }
       if constexpr (FMT8 != 0) {
         float m = amax8(h[k]);
-        if (a.group) {
+        if (NORM && a.group) {
           m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
           const float scale = scale_of(m, FMT8);
           store_codes<true>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale), valid);
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
       }
     }
     if constexpr (FMT8 != 0) {
-      if (!a.group) {
+      if (!NORM || !a.group) {
         if constexpr (LPR != 0) {
           top = lanes_amax(top, LPR);
         } else {
@@ -595,15 +607,21 @@ void with_plan(const Plan& p, F&& f) {
   else f(Int<0>(), Int<4>());
 }
 
-// Raises a kernel's limit of dynamic shared memory where a launch needs it.
-template <typename K>
-cudaError_t allow_smem(K* kernel, size_t bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;           // static shared memory counts too
-  return cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
+// Raises a kernel's limit of dynamic shared memory, once a device.
+template <auto* KERNEL>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kMaxSmem);
+  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return e;
 }
 
-template <typename T, int FMT8>
+template <typename T, int FMT8, bool NORM>
 cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
   const Plan p = plan(a.cols, 1024, 64);
   cudaError_t e = cudaSuccess;
@@ -613,9 +631,9 @@ cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
       const size_t stage = (size_t)N * p.threads * 2 * sizeof(Chunk<T>);
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
-        auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S>;
+        constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM>;
         const size_t smem = S * stage;
-        e = allow_smem(k, smem);
+        e = allow_smem<k>();
         if (e == cudaSuccess)
           k<<<grid(a.rows, p.here, resident(p.threads, 64, smem)), p.threads, smem, st>>>(a);
       };
@@ -623,9 +641,11 @@ cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
         ring(Int<3>());
       else if (vec && 2 * stage <= kMaxSmem)
         ring(Int<2>());
-      else
+      else if constexpr (NORM)
         norm_fwd_kernel<T, L, N, false, FMT8>
             <<<grid(a.rows, p.here, kSMs * 32), p.threads, 0, st>>>(a);
+      else
+        e = cudaErrorNotSupported;
     }
   });
   return e == cudaSuccess ? cudaGetLastError() : e;
@@ -645,8 +665,8 @@ cudaError_t bwd(const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
     const bool ring = vec && smem <= kMaxSmem;
     *blocks = grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N), ring ? smem : 0));
     if (ring) {
-      auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S>;
-      e = allow_smem(k, smem);
+      constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S>;
+      e = allow_smem<k>();
       if (e == cudaSuccess) k<<<*blocks, p.threads, smem, st>>>(a);
     } else {
       norm_bwd_kernel<T, L, N, false, FMT><<<*blocks, p.threads, 0, st>>>(a);
@@ -672,9 +692,23 @@ cudaError_t launch_norm_fwd(int dtype, const NormFwd& in, cudaStream_t st) {
                      aligned_to(a.x, 16) && aligned_to(a.r, 16) && aligned_to(a.h, 16) &&
                      aligned_to(a.y, 16) && aligned_to(a.w, 16) && aligned_to(a.codes, 8);
     const int fmt = a.codes ? a.fmt : 0;
-    return fmt == 0          ? fwd<T, 0>(a, vec, st)
-           : fmt == kFmtInt8 ? fwd<T, kFmtInt8>(a, vec, st)
-                             : fwd<T, kFmtE4m3>(a, vec, st);
+    return fmt == 0          ? fwd<T, 0, true>(a, vec, st)
+           : fmt == kFmtInt8 ? fwd<T, kFmtInt8, true>(a, vec, st)
+                             : fwd<T, kFmtE4m3, true>(a, vec, st);
+  });
+}
+
+cudaError_t launch_row_save(int dtype, const ActSave& s, cudaStream_t st) {
+  NormFwd a{};
+  a.rows = s.rows; a.cols = s.cols; a.x_stride = s.x_stride; a.groups = 1;
+  a.x = s.x; a.codes = s.codes; a.scales = s.scales;
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    if (a.cols > 16384 || a.cols % 8 || a.x_stride % 8 || !aligned_to(a.x, 16) ||
+        !aligned_to(a.codes, 8) || (sizeof(T) == 4 && a.cols > 8192))
+      return cudaErrorNotSupported;
+    return s.fmt == kFmtInt8 ? fwd<T, kFmtInt8, false>(a, true, st)
+                             : fwd<T, kFmtE4m3, false>(a, true, st);
   });
 }
 

@@ -323,7 +323,7 @@ cudaError_t with_type(int dtype, F&& f) {
 }
 
 // Shift from a column to its group (one group a row: any column to 0).
-inline int group_shift(int group) {
+inline __host__ __device__ int group_shift(int group) {
   return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : 31;
 }
 

@@ -20,15 +20,22 @@ from . import _lib
 
 def _launch(name, device, *args):
     """Calls a C entry point with the current stream of `device`."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    index = device.index
     fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, stream)
+    if _current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, stream)
+            code = fn(*args, _raw_stream(index))
     if code != 0:
         raise _lib.BLError(name, code)
+
+
+# The public calls build objects around these two numbers, which takes longer
+# than a small launch; they are the fallback.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _tensor(t, name, device=None, dtype=None, shape=None):
@@ -73,12 +80,16 @@ def _rows(t, name):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _lib.DTYPES:
         raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape = t.shape
+    cols = shape[-1] if shape else 0
+    if cols < 1:
         raise ValueError(f"{name} needs a last dim of at least one element")
+    if t.is_contiguous():
+        return t.numel() // cols, cols, cols
     stride = row_stride(t)
     if stride is None:
         raise ValueError(f"{name} with strides {tuple(t.stride())} is not a run of rows")
-    return t.numel() // t.shape[-1], t.shape[-1], stride
+    return t.numel() // cols, cols, stride
 
 
 # --- activations in 8 bits -----------------------------------------------------
@@ -205,39 +216,43 @@ def attn_bwd_act8_workspace_bytes(shape) -> int:
 
 # --- root-mean-square norm -------------------------------------------------------
 
-def _norm_args(x, weight, residual):
-    rows, cols, stride = _rows(x, "x")
-    if cols > _lib.NORM_MAX_COLS:
-        raise ValueError(f"rows of {cols} elements: the norm takes up to {_lib.NORM_MAX_COLS}")
-    r_stride = cols
-    if residual is not None:
-        if residual.dtype != x.dtype or residual.shape != x.shape or residual.device != x.device:
-            raise ValueError("the residual must have x's type, shape and device, got "
-                             f"{residual.dtype} {tuple(residual.shape)} on {residual.device}")
-        r_stride = _rows(residual, "residual")[2]
-    return rows, cols, stride, r_stride, _weight_dtype(weight, x.dtype, cols, x.device)
-
-
 def _weight_dtype(weight, dtype, cols, device):
     if weight is None:
         return _lib.DTYPES[dtype]
-    if weight.dtype not in (dtype, torch.float32):
+    if weight.dtype != dtype and weight.dtype != torch.float32:
         raise TypeError(f"weight must be {dtype} or fp32, got {weight.dtype}")
     _tensor(weight, "weight", device, None, (cols,))
     return _lib.DTYPES[weight.dtype]
 
 
 def _norm_fwd(x, weight, eps, residual, want_y, y8):
-    rows, cols, stride, r_stride, wtype = _norm_args(x, weight, residual)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _launch("bl_rms_norm_fwd", x.device, rows, cols, _lib.DTYPES[x.dtype], x.data_ptr(), stride,
-            None if residual is None else residual.data_ptr(), r_stride,
-            None if weight is None else weight.data_ptr(), wtype, eps,
-            None if y is None else y.data_ptr(), None if h is None else h.data_ptr(),
-            rstd.data_ptr(), None if y8 is None else ctypes.byref(y8.struct()))
+    rows, cols, stride = _rows(x, "x")
+    if cols > _lib.NORM_MAX_COLS:
+        raise ValueError(f"rows of {cols} elements: the norm takes up to {_lib.NORM_MAX_COLS}")
+    dtype, device, shape = x.dtype, x.device, x.shape
+    wtype = _weight_dtype(weight, dtype, cols, device)
+    h = r_ptr = h_ptr = None
+    r_stride = cols
+    if residual is not None:
+        if residual.dtype != dtype or residual.shape != shape or residual.device != device:
+            raise ValueError("the residual must have x's type, shape and device, got "
+                             f"{residual.dtype} {tuple(residual.shape)} on {residual.device}")
+        r_stride = _rows(residual, "residual")[2]
+        h = _like(x)
+        r_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
+    y = _like(x) if want_y else None
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    _launch("bl_rms_norm_fwd", device, rows, cols, _lib.DTYPES[dtype], x.data_ptr(), stride,
+            r_ptr, r_stride, None if weight is None else weight.data_ptr(), wtype, eps,
+            None if y is None else y.data_ptr(), h_ptr, rstd.data_ptr(),
+            None if y8 is None else ctypes.byref(y8.struct()))
     return y, x if h is None else h, rstd
+
+
+def _like(x):
+    """An empty contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else \
+        torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def rms_norm_fwd(x, weight, eps=1e-6, residual=None):
@@ -262,8 +277,8 @@ def rms_norm_bwd(g_y, h, rstd, weight, g_h=None, need_g_w=True):
     is added to g_x, which is the residual's gradient too.  g_w has the
     weight's type (fp32 without a weight: the gradient of a weight of ones);
     None when not needed."""
-    rows, cols, stride = _rows(g_y, "g_y")
-    if stride != cols and rows > 1:
+    rows, cols, _ = _rows(g_y, "g_y")
+    if not g_y.is_contiguous():
         raise ValueError("g_y must be contiguous")
     if cols > _lib.NORM_MAX_COLS:
         raise ValueError(f"rows of {cols} elements: the norm takes up to {_lib.NORM_MAX_COLS}")
@@ -281,8 +296,8 @@ def rms_norm_bwd(g_y, h, rstd, weight, g_h=None, need_g_w=True):
         raise ValueError(f"rstd has {rstd.numel()} elements for {rows} rows")
     if g_h is not None:
         _tensor(g_h, "g_h", dev, dtype, g_y.shape)
-    wtype = _weight_dtype(weight, dtype, cols, dev) if weight is not None else 2
-    g_x = torch.empty(g_y.shape, dtype=dtype, device=dev)
+    wtype = 2 if weight is None else _weight_dtype(weight, dtype, cols, dev)
+    g_x = torch.empty_like(g_y)
     g_w, ws, nbytes = None, None, 0
     if need_g_w:
         g_w = torch.empty(cols, dtype=torch.float32 if weight is None else weight.dtype, device=dev)

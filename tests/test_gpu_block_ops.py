@@ -406,6 +406,9 @@ ATTN = [
     (2, 300, 4, 2, 128, True, "e4m3", True),
     (1, 600, 3, 3, 128, False, "int8", True),
     (1, 129, 6, 2, 64, True, "e4m3", False),
+    (1, 257, 2, 2, 128, False, "e4m3", False),
+    (2, 513, 8, 2, 64, False, "int8", False),
+    (1, 400, 5, 1, 128, True, "int8", True),
 ]
 
 
@@ -419,6 +422,18 @@ def _attn_case(bl, B, n, H, Hk, d, causal, fmt, seed=20):
     lse = torch.empty((B, H, n), dtype=torch.float32, device="cuda")
     bl.attn_fwd(shape, q, k, v, d ** -0.5, o, lse)
     return shape, (q, k, v, o), g_o, lse, [bl.act_save(t, fmt) for t in (q, k, v, o)]
+
+
+def _same_kv_gradients(got, ref, other_order):
+    """G_K and G_V bit for bit; where few items make the call add the heads of a group in
+    another order, fp32 sums that differ by their last bits round to another bf16 value
+    now and then: with a share p of the elements one step (2^-8 at most) off, rel-L2 is
+    2^-8 sqrt(p), and p stays below 2^-6 (sums of 2^6 F around a step of 2^16 F)."""
+    for a, b in zip(got[1:], ref[1:]):
+        if other_order:
+            assert U.rel_l2(U.cpu(a), U.cpu(b)) <= 2.0 ** -11
+        else:
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("case", ATTN, ids=lambda c: f"n{c[1]}d{c[4]}{c[6]}")
@@ -436,7 +451,7 @@ def test_attention_backward_from_8_bits(bl, case):
         ref = [torch.empty_like(t) for t in (qb, kb, vb)]
         w2 = torch.empty(bl.bwd_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
         bl.attn_bwd(shape, qb, kb, vb, o, g_o, lse, scale, None, *ref, w2)
-        assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+        _same_kv_gradients(got, ref, H != Hk)
         assert U.rel_l2(U.cpu(got[0]), U.cpu(ref[0])) <= 1e-3 or n == 1
     if n == 1:
         # one key: P = exp(s q.k - lse) with the rounded q and k, G_V = P G_O, and G_Q and
@@ -465,7 +480,20 @@ def test_attention_backward_from_8_bits_keeps_a_mask(bl):
     ref = [torch.empty_like(t) for t in (q, k, v)]
     ws = torch.empty(bl.bwd_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
     bl.attn_bwd(shape, *(bl.act_load(t) for t in (q8, k8, v8)), o, g_o, lse, w.scale, lists, *ref, ws)
-    assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+    _same_kv_gradients(got, ref, True)
+    assert U.rel_l2(U.cpu(got[0]), U.cpu(ref[0])) <= 1e-3
+
+
+@pytest.mark.parametrize("B,n,H,Hk,bq", [(1, 10000, 4, 2, 128), (1, 700, 4, 2, 64)])
+def test_attention_backward_from_8_bits_of_kv_heads(bl, B, n, H, Hk, bq):
+    """Grouped heads with an item for every SM, or tiles of 64: bf16's own order of sums."""
+    _, (q, k, v, o), g_o, lse, (q8, k8, v8, _) = _attn_case(bl, B, n, H, Hk, 64, False, "int8")
+    shape = bl.make_shape(B, n, H, Hk, 64, bq, bq)
+    got = bl.attn_bwd_act8(shape, q8, k8, v8, o, g_o, lse, 0.125)
+    ref = [torch.empty_like(t) for t in (q, k, v)]
+    ws = torch.empty(bl.bwd_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    bl.attn_bwd(shape, *(bl.act_load(t) for t in (q8, k8, v8)), o, g_o, lse, 0.125, None, *ref, ws)
+    _same_kv_gradients(got, ref, False)
     assert U.rel_l2(U.cpu(got[0]), U.cpu(ref[0])) <= 1e-3
 
 
