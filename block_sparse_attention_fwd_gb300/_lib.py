@@ -164,7 +164,7 @@ def load():
     lib.bl_rms_norm_bwd_workspace_bytes.argtypes = [L, L]
     lib.bl_rms_norm_bwd_workspace_bytes.restype = Z
     lib.bl_rms_norm_bwd.argtypes = [L, L, I, P, P, A, P, P, I, P, P, P, P, Z, P]
-    lib.bl_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+    lib.bl_rope.argtypes = [P, P]          # a RopeArgs by reference, or its bytes
     lib.bl_attn_bwd_act8_workspace_bytes.argtypes = [S]
     lib.bl_attn_bwd_act8_workspace_bytes.restype = Z
     lib.bl_attn_bwd_act8.argtypes = [S, A, A, A, P, A, P, P, F, ctypes.POINTER(Lists), P, P, P, P,

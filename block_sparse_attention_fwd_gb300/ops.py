@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 
 import torch
 
@@ -110,9 +111,10 @@ class Act8:
             raise TypeError(f"an activation is bf16, fp16 or fp32, got {dtype}")
         _tensor(codes, "codes")
         _tensor(scales, "scales", codes.device, torch.float32)
-        if codes.dim() < 1 or codes.shape[-1] < 1:
+        shape = codes.shape
+        cols = shape[-1] if shape else 0
+        if cols < 1:
             raise ValueError("codes need a last dim of at least one element")
-        cols = codes.shape[-1]
         want = codes.numel() // cols * _groups(cols, group)
         if scales.numel() != want:
             raise ValueError(f"{scales.numel()} scales for {want} groups")
@@ -364,6 +366,7 @@ class RopePlan:
             raise ValueError(f"{pairs} finite frequencies are needed, got {len(freqs)}")
         self.head_dim, self.sections, self.layout, self.pairs = head_dim, sections, layout, pairs
         self.freqs = freqs
+        self.padded_sections = sections + (0,) * (4 - len(sections))
         self.fixed = torch.tensor(_fixed_point_freqs(freqs), dtype=torch.int64, device=device)
 
 
@@ -404,27 +407,32 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
     axes = len(plan.sections)
     batched = positions.dim() == 3
     _tensor(positions, "positions", dev, torch.int32, (B, n, axes) if batched else (n, axes))
-    a = _lib.RopeArgs()
-    a.B, a.n, a.H, a.Hk, a.d = B, n, H, 0 if k is None else k.shape[2], d
-    a.pairs, a.axes = plan.pairs, axes
-    a.sections[:axes] = plan.sections
-    a.interleaved, a.inverse, a.dtype = plan.layout == "interleaved", inverse, _lib.DTYPES[dtype]
-    a.positions, a.freqs = positions.data_ptr(), plan.fixed.data_ptr()
-    a.positions_batch_stride = n * axes if batched else 0
-    a.q_strides[:] = _rope_strides(q, "q", dtype, B, n, d)
-    q_out = q if inplace else torch.empty((B, n, H, d), dtype=dtype, device=dev)
-    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-    a.q_out_strides[:] = q_out.stride()[:3]
-    k_out = None
+    none = (0, 0, 0)
+    q_in, q_out = _rope_strides(q, "q", dtype, B, n, d), q
+    if not inplace:
+        q_out = torch.empty((B, n, H, d), dtype=dtype, device=dev)
+    q_st = q_out.stride()[:3]
+    Hk, k_ptr, k_out_ptr, k_in, k_st, k_out = 0, 0, 0, none, none, None
     if k is not None:
-        a.k_strides[:] = _rope_strides(k, "k", dtype, B, n, d)
+        Hk = k.shape[2]
+        k_in, k_out = _rope_strides(k, "k", dtype, B, n, d), k
         if k.device != dev:
             raise ValueError(f"k is on {k.device}, expected {dev}")
-        k_out = k if inplace else torch.empty(k.shape, dtype=dtype, device=dev)
-        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
-        a.k_out_strides[:] = k_out.stride()[:3]
-    _launch("bl_rope", dev, ctypes.byref(a))
+        if not inplace:
+            k_out = torch.empty((B, n, Hk, d), dtype=dtype, device=dev)
+        k_st = k_out.stride()[:3]
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    # bl_rope_args, field by field
+    args = _ROPE_ARGS.pack(
+        B, n, H, Hk, d, plan.pairs, axes, *plan.padded_sections, plan.layout == "interleaved",
+        bool(inverse), _lib.DTYPES[dtype], q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr,
+        *q_in, *k_in, *q_st, *k_st, positions.data_ptr(), n * axes if batched else 0,
+        plan.fixed.data_ptr())
+    _launch("bl_rope", dev, args)
     return q_out, k_out
+
+
+_ROPE_ARGS = struct.Struct("<14i4Q12qQqQ")
 
 
 def grid_positions(T, Y, X, device="cuda", dtype=torch.int32):

@@ -120,6 +120,16 @@ def test_rope_refuses(lib, kw):
     assert lib.bl_rope(ctypes.byref(_rope_args(**kw)), None) == 1
 
 
+def test_rope_arguments_are_laid_out_as_the_struct():
+    """The call packs bl_rope_args itself: the same bytes as the structure's."""
+    v = (2, 5, 4, 2, 64, 32, 2, 30, 2, 0, 0, 1, 0, 1, 11, 12, 13, 14, *range(20, 32), 41, 10, 43)
+    a = _rope_args(B=2, n=5, H=4, Hk=2, d=64, pairs=32, axes=2, sections=(30, 2, 0, 0), interleaved=1,
+                   inverse=0, dtype=1, q=11, k=12, q_out=13, k_out=14, q_strides=(20, 21, 22),
+                   k_strides=(23, 24, 25), q_out_strides=(26, 27, 28), k_out_strides=(29, 30, 31),
+                   positions=41, positions_batch_stride=10, freqs=43)
+    assert ops._ROPE_ARGS.pack(*v) == bytes(a)
+
+
 def test_rope_takes_empty_batches(lib):
     assert lib.bl_rope(None, None) == 1
     assert lib.bl_rope(ctypes.byref(_rope_args(B=0)), None) == 0

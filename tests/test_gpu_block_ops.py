@@ -183,7 +183,7 @@ def test_rope_refusals(bl):
 # --- norm -----------------------------------------------------------------------
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (1000, 64), (517, 128), (33, 129), (5, 256), (9, 264), (7, 1000),
-          (4, 1001), (6, 2048), (3, 5120), (2, 5123), (2, 16384)]
+          (4, 1001), (6, 2048), (3, 5120), (2, 5123), (700, 7168), (2, 16384)]
 
 
 def _norm_inputs(rows, cols, dtype, wtype):
