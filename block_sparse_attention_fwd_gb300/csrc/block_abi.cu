@@ -153,7 +153,7 @@ bl_status bl_rope(const bl_rope_args* r, void* stream) {
   for (int t = 0; t < 4; ++t)
     for (int i = 0; i < 3; ++i) {
       if (in[t][i] < 0) return BL_ERR_INVALID_ARG;
-      to[t][i] = in[t][i];
+      to[t][i] = t % 2 && !r->Hk ? 0 : in[t][i];     // no k: its strides say nothing
     }
   // the heads of an output may not lie on one another
   const bool q_same = r->q == r->q_out, k_same = r->Hk && r->k == r->k_out;

@@ -146,7 +146,8 @@ struct Rope {
   const int32_t* pos;             // [B or 1, n, axes]
   int64_t pos_batch;              // 0: shared by the batches
   const uint64_t* freqs;          // [pairs], turns in 64-bit fixed point
-  int lanes, tile;                // set by the launch
+  int lanes, tile;                // set by the launch, like:
+  bool flat, pos_flat;            // tokens (positions) of all batches equally spaced
 };
 cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st);
 

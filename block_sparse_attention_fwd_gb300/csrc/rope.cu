@@ -47,17 +47,20 @@ __device__ __forceinline__ float2 cos_sin(uint32_t angle) {
   return make_float2((quadrant + 1) & 2 ? -a : a, quadrant & 2 ? -b : b);
 }
 
-__device__ __forceinline__ float2 turn(const Rope& a, const int32_t* pos, int p) {
+__device__ __forceinline__ int axis_of(const Rope& a, int p) {
   int axis = 0;
 #pragma unroll
   for (int e = 0; e < 3; ++e) axis += p >= a.ends[e] ? 1 : 0;
-  const uint64_t angle = (uint64_t)(int64_t)pos[axis] * a.freqs[p];
-  const uint32_t hi = (uint32_t)(angle >> 32);
-  return cos_sin(a.inverse ? 0u - hi : hi);
+  return axis;
+}
+// The angle at a position of a pair with frequency f, in 2^-32 turns.
+__device__ __forceinline__ uint32_t angle_of(const Rope& a, const int32_t* pos, uint64_t f) {
+  const uint32_t hi = (uint32_t)(((uint64_t)(int64_t)__ldg(pos) * f) >> 32);
+  return a.inverse ? 0u - hi : hi;
 }
 
 template <typename T, int U, bool HALF>
-__global__ void __launch_bounds__(256) rope_kernel(Rope a) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(Rope a) {
   constexpr int W = 16 / sizeof(T);
   constexpr int NV = HALF ? 2 : 1;                   // vectors of a unit a thread holds
   constexpr int NP = HALF ? W : W / 2;               // pairs in them
@@ -75,23 +78,14 @@ __global__ void __launch_bounds__(256) rope_kernel(Rope a) {
   const int p0 = lane * NP;
   const bool turns = lane < holders;
   const bool works = g < step && (turns || a.copy);
-  // the thread's elements of a head
-  const int e0 = HALF ? (turns ? p0 : 2 * a.pairs + (lane - holders) * W) : 2 * p0;
+  // the thread's elements of a head: HALF has two vectors, of the halves of its
+  // pairs or next to each other behind them (the last may lack its second)
+  const int e0 = HALF ? (turns ? p0 : 2 * a.pairs + (lane - holders) * 2 * W) : 2 * p0;
+  const int second = turns ? a.pairs : W;
+  const bool two = HALF && (turns || e0 + W < a.d);
 
-  // the next unit: its token, head, and that token's heads
-  int tok = g / per_token, head = g - tok * per_token;
+  int tok = g / per_token, head = g - tok * per_token;      // the next unit's
   const int tok_step = step / per_token, head_step = step - tok_step * per_token;
-  const T *q_in, *k_in;
-  T *q_out, *k_out;
-  auto seek = [&]() {
-    const uint32_t t = (uint32_t)tok0 + tok;
-    const uint32_t b = t / (uint32_t)a.n, i = t - b * (uint32_t)a.n;
-    q_in = static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + e0;
-    q_out = static_cast<T*>(a.q_out) + b * a.qos[0] + i * a.qos[1] + e0;
-    k_in = static_cast<const T*>(a.k) + b * a.ks[0] + i * a.ks[1] + e0;
-    k_out = static_cast<T*>(a.k_out) + b * a.kos[0] + i * a.kos[1] + e0;
-  };
-  seek();
   Vec v[U][NV];
   T* dst[U];
   int at[U];                                          // token of the tile, or -1
@@ -99,40 +93,54 @@ __global__ void __launch_bounds__(256) rope_kernel(Rope a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       at[u] = works && tok < toks ? tok : -1;
-      if (at[u] < 0) continue;
-      const bool is_k = head >= a.H;
-      const int h = is_k ? head - a.H : head;
-      const T* src = (is_k ? k_in : q_in) + h * (is_k ? a.ks[2] : a.qs[2]);
-      dst[u] = (is_k ? k_out : q_out) + h * (is_k ? a.kos[2] : a.qos[2]);
-      v[u][0] = *reinterpret_cast<const Vec*>(src);
-      if constexpr (HALF)
-        if (turns) v[u][1] = *reinterpret_cast<const Vec*>(src + a.pairs);
-      const int was = tok;
+      if (at[u] >= 0) {
+        const uint32_t t = (uint32_t)tok0 + tok;
+        const bool is_k = head >= a.H;
+        const int h = is_k ? head - a.H : head;
+        const int64_t* si = is_k ? a.ks : a.qs;
+        const int64_t* so = is_k ? a.kos : a.qos;
+        const T* src = static_cast<const T*>(is_k ? a.k : a.q) + e0 + (int64_t)h * (int)si[2];
+        dst[u] = static_cast<T*>(is_k ? a.k_out : a.q_out) + e0 + (int64_t)h * (int)so[2];
+        if (a.flat) {                                 // the batches follow one another
+          src += (int64_t)t * (int)si[1];
+          dst[u] += (int64_t)t * (int)so[1];
+        } else {
+          const uint32_t b = t / (uint32_t)a.n, i = t - b * (uint32_t)a.n;
+          src += b * si[0] + i * si[1];
+          dst[u] += b * so[0] + i * so[1];
+        }
+        v[u][0] = *reinterpret_cast<const Vec*>(src);
+        if constexpr (HALF)
+          if (two) v[u][1] = *reinterpret_cast<const Vec*>(src + second);
+      }
       tok += tok_step;
       head += head_step;
       if (head >= per_token) {
         head -= per_token;
         ++tok;
       }
-      if (tok != was) seek();
     }
   };
 
   load();
   {
-    int t = threadIdx.x / a.pairs, p = threadIdx.x - t * a.pairs;
-    const int t_step = 256 / a.pairs, p_step = 256 - t_step * a.pairs;
-    while (t < toks) {
-      const uint32_t token = (uint32_t)tok0 + t;
-      const int64_t at_pos = a.pos_batch ? (int64_t)token : (int64_t)(token % (uint32_t)a.n);
-      const float2 cs = turn(a, a.pos + at_pos * a.axes, p);
-      const int l = p / NP, j = p % NP;
-      reinterpret_cast<float2*>(table)[((t * planes + j / 2) * holders + l) * 2 + j % 2] = cs;
-      t += t_step;
-      p += p_step;
-      if (p >= a.pairs) {
-        p -= a.pairs;
-        ++t;
+    // A thread keeps its place in a token's part of the table, so its pair, and
+    // goes over the tokens `apart` at a time.
+    const int places = planes * holders * 2;
+    const int apart = places < 256 ? 256 / places : 1;
+    const int t0 = threadIdx.x / places;
+    for (int x = threadIdx.x - t0 * places; x < places && t0 < apart; x += 256) {
+      const int plane = x / (2 * holders), rest = x - plane * 2 * holders;
+      const int p = (rest >> 1) * NP + 2 * plane + (rest & 1);
+      if (p >= a.pairs) continue;
+      const uint64_t f = a.freqs[p];
+      const int32_t* pos = a.pos + axis_of(a, p);
+      float2* place = reinterpret_cast<float2*>(table) + x;
+#pragma unroll 4
+      for (int t = t0; t < toks; t += apart) {
+        const uint32_t token = (uint32_t)tok0 + t;
+        const uint32_t i = a.pos_flat ? token : token % (uint32_t)a.n;
+        place[t * places] = cos_sin(angle_of(a, pos + (int64_t)i * a.axes, f));
       }
     }
   }
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(256) rope_kernel(Rope a) {
       }
       *reinterpret_cast<Vec*>(dst[u]) = v[u][0];
       if constexpr (HALF)
-        if (turns) *reinterpret_cast<Vec*>(dst[u] + a.pairs) = v[u][1];
+        if (two) *reinterpret_cast<Vec*>(dst[u] + second) = v[u][1];
     }
     load();
   }
@@ -202,7 +210,8 @@ __global__ void __launch_bounds__(256) rope_any_kernel(Rope a) {
       continue;
     }
     const int e0 = a.half ? p : 2 * p, e1 = a.half ? p + a.pairs : 2 * p + 1;
-    const float2 cs = turn(a, a.pos + b * a.pos_batch + i * a.axes, p);
+    const float2 cs = 
+        cos_sin(angle_of(a, a.pos + b * a.pos_batch + i * a.axes + axis_of(a, p), a.freqs[p]));
     const float c = cs.x, s = cs.y;
     const float u = to_f32(in[e0]), v = to_f32(in[e1]);
     out[e0] = from_f32<T>(u * c - v * s);
@@ -210,11 +219,12 @@ __global__ void __launch_bounds__(256) rope_any_kernel(Rope a) {
   }
 }
 
-// Tokens of a block's tile: enough (token, head) units that every thread gets
-// several, as far as there are tokens for four blocks an SM.
-int tile_tokens(int64_t tokens, int heads, int groups) {
-  int64_t tile = (8 * groups + heads - 1) / heads;
-  if (tile > 32) tile = 32;
+// Tokens of a block's tile: four batches of U units for every thread, as far as
+// there are tokens for four blocks an SM.  Half as many units cost 8% at 40 + 40
+// heads of 128 (interleaved: 225 against 207 us), twice as many gain nothing.
+int tile_tokens(int64_t tokens, int heads, int groups, int U) {
+  int64_t tile = (4 * U * groups + heads - 1) / heads;
+  if (tile > 128) tile = 128;
   const int64_t fill = tokens / (4 * 152);
   if (tile > fill) tile = fill;
   return tile < 1 ? 1 : (int)tile;
@@ -223,16 +233,21 @@ int tile_tokens(int64_t tokens, int heads, int groups) {
 template <typename T, bool HALF>
 cudaError_t rope_launch(Rope a, cudaStream_t st) {
   constexpr int W = 16 / sizeof(T);
-  a.lanes = HALF ? a.pairs / W + (a.d - 2 * a.pairs) / W : a.d / W;
+  a.lanes = HALF ? a.pairs / W + ((a.d - 2 * a.pairs) / W + 1) / 2 : a.d / W;
   const int64_t tokens = (int64_t)a.B * a.n;
-  a.tile = tile_tokens(tokens, a.H + a.Hk, 256 / a.lanes);
+  a.flat = true;
+  for (const int64_t* st : {a.qs, a.qos, a.ks, a.kos})
+    a.flat = a.flat && (a.B == 1 || st[0] == (int64_t)a.n * st[1]);
+  a.pos_flat = a.B == 1 || a.pos_batch != 0;
+  constexpr int U = HALF ? 2 : 4;
+  a.tile = tile_tokens(tokens, a.H + a.Hk, 256 / a.lanes, U);
   // the table of a tile stays within 32 KB
   constexpr int NP = HALF ? W : W / 2;
   const int padded = (a.pairs + NP - 1) / NP * NP;
   while (a.tile > 1 && (int64_t)a.tile * padded * 8 > 32768) a.tile /= 2;
   const size_t smem = (size_t)a.tile * padded * 8;
   const unsigned g = (unsigned)((tokens + a.tile - 1) / a.tile);
-  rope_kernel<T, HALF ? 2 : 4, HALF><<<g, 256, smem, st>>>(a);
+  rope_kernel<T, U, HALF><<<g, 256, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -246,8 +261,8 @@ cudaError_t launch_rope(int dtype, const Rope& a, cudaStream_t st) {
     bool vec = a.d % W == 0 && a.d / W <= 256 && (!a.half || a.pairs % W == 0) &&
                (int64_t)a.B * a.n < (int64_t)1 << 31;
     for (int i = 0; i < 3; ++i)
-      vec = vec && a.qs[i] % W == 0 && a.qos[i] % W == 0 &&
-            (!a.Hk || (a.ks[i] % W == 0 && a.kos[i] % W == 0));
+      for (const int64_t* st : {a.qs, a.qos, a.ks, a.kos})
+        vec = vec && st[i] % W == 0 && (i == 0 || st[i] < (int64_t)1 << 31);
     vec = vec && aligned_to(a.q, 16) && aligned_to(a.q_out, 16) && aligned_to(a.k, 16) &&
           aligned_to(a.k_out, 16);
     if (!vec) {
