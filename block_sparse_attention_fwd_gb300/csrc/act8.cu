@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
 }
 
 // Rows of whole groups back to back in memory, as in the flat saving kernel.
-template <typename T, int FMT, int U>
+template <typename T, int FMT, int U, bool W32>
 __global__ void __launch_bounds__(256) act_load_flat_kernel(const uint8_t* __restrict__ codes,
                                                             const float* __restrict__ scales,
                                                             T* __restrict__ x, int64_t pieces,
@@ -155,15 +155,16 @@ __global__ void __launch_bounds__(256) act_load_flat_kernel(const uint8_t* __res
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t p = p0 + u * 256;
+    if (p >= pieces) return;
     const Codes c[2] = {{{raw[u].x, raw[u].y}}, {{raw[u].z, raw[u].w}}};
+    float f[2][8];
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      float f[8];
-      decode8<FMT>(c[v], f);
+      decode8<FMT>(c[v], f[v]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= scale[u];
-      store8<T, true>(x + p * 16 + v * 8, f, p < pieces ? 8 : 0);
+      for (int i = 0; i < 8; ++i) f[v][i] *= scale[u];
     }
+    store16<T, W32>(x + p * 16, f);
   }
 }
 
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
 // q, k and v of an attention, [tokens, heads, D] codes with one scale a
 // (token, head), to bf16.  16 codes a thread; the blocks of the three tensors
 // follow one another.
-template <int D, int FMT>
+template <int D, int FMT, bool W32>
 __global__ void __launch_bounds__(256) expand_kernel(Expand a) {
   int s = 0;
   int64_t blk = blockIdx.x;
@@ -220,14 +221,14 @@ __global__ void __launch_bounds__(256) expand_kernel(Expand a) {
   const uint4 raw = __ldg(reinterpret_cast<const uint4*>(a.codes[s]) + x);
   const float scale = __ldg(a.scales[s] + x / PER_ROW);
   const Codes c[2] = {{{raw.x, raw.y}}, {{raw.z, raw.w}}};
+  float f[2][8];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    float f[8];
-    decode8<FMT>(c[u], f);
+    decode8<FMT>(c[u], f[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= scale;
-    store8<__nv_bfloat16, true>(static_cast<__nv_bfloat16*>(a.out[s]) + x * 16 + u * 8, f, 8);
+    for (int i = 0; i < 8; ++i) f[u][i] *= scale;
   }
+  store16<__nv_bfloat16, W32>(static_cast<__nv_bfloat16*>(a.out[s]) + x * 16, f);
 }
 
 constexpr int64_t kMaxBlocks = 152 * 64;
@@ -307,12 +308,16 @@ cudaError_t launch_act_load(int dtype, const ActLoad& in, cudaStream_t st) {
       const int64_t pieces = a.rows * (a.cols / 16);
       const unsigned g = (unsigned)((pieces + 256 * kFlatU - 1) / (256 * kFlatU));
       auto* x = static_cast<T*>(a.x);
-      if (a.fmt == kFmtInt8)
-        act_load_flat_kernel<T, kFmtInt8, kFlatU><<<g, 256, 0, st>>>(a.codes, a.scales, x, pieces,
-                                                                     shift);
+      auto flat = [&](auto fmt, auto w32) {
+        act_load_flat_kernel<T, decltype(fmt)::value, kFlatU, decltype(w32)::value>
+            <<<g, 256, 0, st>>>(a.codes, a.scales, x, pieces, shift);
+      };
+      const std::integral_constant<int, kFmtInt8> i8;
+      const std::integral_constant<int, kFmtE4m3> e4;
+      if (aligned_to(a.x, 32))
+        a.fmt == kFmtInt8 ? flat(i8, std::true_type()) : flat(e4, std::true_type());
       else
-        act_load_flat_kernel<T, kFmtE4m3, kFlatU><<<g, 256, 0, st>>>(a.codes, a.scales, x, pieces,
-                                                                     shift);
+        a.fmt == kFmtInt8 ? flat(i8, std::false_type()) : flat(e4, std::false_type());
       return cudaGetLastError();
     }
     const unsigned g = blocks_for((a.rows * a.cols + 2047) / 2048);
@@ -341,12 +346,24 @@ cudaError_t launch_expand(int d, int fmt, const Expand& in, cudaStream_t st) {
     blocks += a.blocks[s];
   }
   const unsigned g = (unsigned)blocks;
-  if (d == 64)
-    fmt == kFmtInt8 ? expand_kernel<64, kFmtInt8><<<g, 256, 0, st>>>(a)
-                    : expand_kernel<64, kFmtE4m3><<<g, 256, 0, st>>>(a);
-  else
-    fmt == kFmtInt8 ? expand_kernel<128, kFmtInt8><<<g, 256, 0, st>>>(a)
-                    : expand_kernel<128, kFmtE4m3><<<g, 256, 0, st>>>(a);
+  bool w32 = true;
+  for (int s = 0; s < 3; ++s) w32 = w32 && aligned_to(a.out[s], 32);
+  auto launch = [&](auto dim, auto f) {
+    constexpr int D = decltype(dim)::value, F = decltype(f)::value;
+    if (w32)
+      expand_kernel<D, F, true><<<g, 256, 0, st>>>(a);
+    else
+      expand_kernel<D, F, false><<<g, 256, 0, st>>>(a);
+  };
+  const std::integral_constant<int, kFmtInt8> i8;
+  const std::integral_constant<int, kFmtE4m3> e4;
+  if (d == 64) {
+    const std::integral_constant<int, 64> dim;
+    fmt == kFmtInt8 ? launch(dim, i8) : launch(dim, e4);
+  } else {
+    const std::integral_constant<int, 128> dim;
+    fmt == kFmtInt8 ? launch(dim, i8) : launch(dim, e4);
+  }
   return cudaGetLastError();
 }
 

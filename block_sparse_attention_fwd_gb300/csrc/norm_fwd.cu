@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
     const int64_t row = row0 + R.mine;
     const bool in = row < a.rows;
     float h[NV][8];
-    float ss = 0.f;
+    float s0 = 0.f, s1 = 0.f;                          // as the ring kernel sums them
     Chunk<T> x[NV], r[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -42,9 +42,12 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
         if (a.h) store8<T, VEC>(static_cast<T*>(a.h) + row * cols + col, h[k], valid);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+      for (int i = 0; i < 8; i += 2) {
+        s0 = fmaf(h[k][i], h[k][i], s0);
+        s1 = fmaf(h[k][i + 1], h[k][i + 1], s1);
+      }
     }
-    ss = row_sum<LPR>(ss, buf, slot);
+    const float ss = row_sum<LPR>(s0 + s1, buf, slot);
     const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
     if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
     float top = 0.f;
@@ -141,76 +144,83 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
   const int64_t first = (int64_t)blockIdx.x * R.here;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
-  float w[NV][8];
+  uint64_t w[NV][4];                                 // pairs of fp32, like h
   if constexpr (NORM) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int col = (R.t + k * R.step) * 8;
-      load_weight8<T, true>(a.w, a.w_f32, col, cols - col, w[k]);
+      float f[8];
+      load_weight8<T, true>(a.w, a.w_f32, col, cols - col, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[k][i] = f2_pack(f[2 * i], f[2 * i + 1]);
     }
   }
-  int slot = 0, now = 0;
+  int slot = 0, now = 0, fill = S - 1;
   for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
     const int64_t row = row0 + R.mine;
-    const bool in = row < a.rows;
-    fetch(now == 0 ? S - 1 : now - 1, row + (S - 1) * stride);
+    const bool in = LPR == 0 || row < a.rows;
+    fetch(fill, row + (S - 1) * stride);
     copy_wait<S - 1>();
-    float h[NV][8];
-    float ss = 0.f;
+    uint64_t h[NV][4], ss = 0;
+    const int64_t at = row * cols + R.t * 8;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      if (in && col < cols) {
+      const bool has = in && (R.t + k * R.step) * 8 < cols;
+      if (has) {
         const uint8_t* p = place(now, k);
-        const Chunk<T> x = chunk(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x.e[i]);
+        unpack2(chunk(p), h[k]);
         if (NORM && a.r) {
-          const Chunk<T> r = chunk(p + nt * CB);
+          uint64_t r[4];
+          unpack2(chunk(p + nt * CB), r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r.e[i]);
-          if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * cols + col, h[k], 8);
+          for (int i = 0; i < 4; ++i) h[k][i] = fadd2(h[k][i], r[i]);
+          if (a.h) store8(static_cast<T*>(a.h) + at + k * R.step * 8, h[k]);
         }
         if constexpr (NORM) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+          for (int i = 0; i < 4; ++i) ss = ffma2(h[k][i], h[k][i], ss);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) h[k][i] = 0;
       }
     }
-    float rstd = 1.f;
     if constexpr (NORM) {
-      ss = row_sum<LPR>(ss, buf, slot);
-      rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+      float s0, s1;
+      f2_unpack(ss, s0, s1);
+      const float sum = row_sum<LPR>(s0 + s1, buf, slot);
+      const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
       if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
-    }
-    float top = 0.f;
+      const uint64_t rr = f2_pack(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in && col < cols ? 8 : 0;
-      if constexpr (NORM) {
+      for (int k = 0; k < NV; ++k) {
+        const bool has = in && (R.t + k * R.step) * 8 < cols;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[k][i];
-        if (a.y) store8<T, true>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
+        for (int i = 0; i < 4; ++i) h[k][i] = fmul2(fmul2(h[k][i], rr), w[k][i]);
+        if (a.y && has) store8(static_cast<T*>(a.y) + at + k * R.step * 8, h[k]);
       }
-      if constexpr (FMT8 != 0) {
-        float m = amax8(h[k]);
-        if (NORM && a.group) {
-          m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
-          const float scale = scale_of(m, FMT8);
-          store_codes<true>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale), valid);
-          if (valid > 0 && (col & (a.group - 1)) == 0)
-            a.scales[row * a.groups + (col >> a.shift)] = scale;
+    }
+    if constexpr (FMT8 != 0) {
+      float top = 0.f;
+      const bool grouped = NORM && a.group;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int col = (R.t + k * R.step) * 8;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(h[k][i], f[2 * i], f[2 * i + 1]);
+        const float m = amax8(f);
+        if (grouped) {
+          const float scale = scale_of(lanes_amax(m, min(a.group / 8, LPR ? LPR : 32)), FMT8);
+          if (in && col < cols) {
+            store_codes<true>(a.codes + at + k * R.step * 8, encode8<FMT8>(f, scale), 8);
+            if ((col & (a.group - 1)) == 0) a.scales[row * a.groups + (col >> a.shift)] = scale;
+          }
         } else {
           top = amax2(top, m);
         }
       }
-    }
-    if constexpr (FMT8 != 0) {
-      if (!NORM || !a.group) {
+      if (!grouped) {
         if constexpr (LPR != 0) {
           top = lanes_amax(top, LPR);
         } else {
@@ -220,13 +230,16 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
         const float scale = scale_of(top, FMT8);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int col = (R.t + k * R.step) * 8;
-          store_codes<true>(a.codes + row * cols + col, encode8<FMT8>(h[k], scale),
-                            in && col < cols ? 8 : 0);
+          if (!in || (R.t + k * R.step) * 8 >= cols) continue;
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f2_unpack(h[k][i], f[2 * i], f[2 * i + 1]);
+          store_codes<true>(a.codes + at + k * R.step * 8, encode8<FMT8>(f, scale), 8);
         }
         if (R.t == 0 && in) a.scales[row] = scale;
       }
     }
+    fill = fill == S - 1 ? 0 : fill + 1;
     now = now == S - 1 ? 0 : now + 1;
   }
 }

@@ -127,6 +127,28 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], i
   }
 }
 
+// 16 values rounded to T and written to 16 consecutive elements.  W32 (32-byte
+// aligned): a thread writes whole 32-byte sectors with one instruction each;
+// two 16-byte stores, 32 bytes apart from lane to lane, would write every sector
+// in two halves.
+template <typename T, bool W32>
+__device__ __forceinline__ void store16(T* __restrict__ p, const float (&f)[2][8]) {
+  if constexpr (W32) {
+    struct alignas(16) { Chunk<T> c[2]; } both = {{pack8<T>(f[0]), pack8<T>(f[1])}};
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&both);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(both) / 32; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                       reinterpret_cast<uint8_t*>(p) + 32 * i),
+                   "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]),
+                   "r"(w[8 * i + 4]), "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                   : "memory");
+  } else {
+    store8<T, true>(p, f[0], 8);
+    store8<T, true>(p + 8, f[1], 8);
+  }
+}
+
 template <bool VEC>
 __device__ __forceinline__ Codes load_codes(const uint8_t* __restrict__ p, int valid) {
   Codes c{{0u, 0u}};
