@@ -12,6 +12,8 @@ namespace bl {
 
 namespace {
 
+constexpr int kExpandU = 2;
+
 // Quotient and remainder by a divisor that does not change over a launch, in
 // 32 bits wherever the dividend allows.
 __device__ __forceinline__ void div_mod(int64_t x, int64_t d, int64_t& q, int64_t& r) {
@@ -208,27 +210,40 @@ __global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
 }
 
 // q, k and v of an attention, [tokens, heads, D] codes with one scale a
-// (token, head), to bf16.  16 codes a thread; the blocks of the three tensors
-// follow one another.
+// (token, head), to bf16: pieces of 16 as in the flat loading kernel.  The blocks
+// of the three tensors follow one another.
 template <int D, int FMT, bool W32>
 __global__ void __launch_bounds__(256) expand_kernel(Expand a) {
+  constexpr int PER_ROW = D / 16, U = kExpandU;
   int s = 0;
   int64_t blk = blockIdx.x;
   while (s < 2 && blk >= a.blocks[s]) blk -= a.blocks[s++];
-  const int64_t x = blk * 256 + threadIdx.x;          // 16 elements
-  constexpr int PER_ROW = D / 16;
-  if (x >= a.rows[s] * PER_ROW) return;
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(a.codes[s]) + x);
-  const float scale = __ldg(a.scales[s] + x / PER_ROW);
-  const Codes c[2] = {{{raw.x, raw.y}}, {{raw.z, raw.w}}};
-  float f[2][8];
+  const int64_t pieces = a.rows[s] * PER_ROW;
+  const int64_t p0 = blk * (256 * U) + threadIdx.x;
+  uint4 raw[U];
+  float scale[U];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    decode8<FMT>(c[u], f[u]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[u][i] *= scale;
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+    if (p < pieces) {
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(a.codes[s]) + p);
+      scale[u] = __ldg(a.scales[s] + p / PER_ROW);
+    }
   }
-  store16<__nv_bfloat16, W32>(static_cast<__nv_bfloat16*>(a.out[s]) + x * 16, f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + u * 256;
+    if (p >= pieces) return;
+    const Codes c[2] = {{{raw[u].x, raw[u].y}}, {{raw[u].z, raw[u].w}}};
+    float f[2][8];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      decode8<FMT>(c[v], f[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[v][i] *= scale[u];
+    }
+    store16<__nv_bfloat16, W32>(static_cast<__nv_bfloat16*>(a.out[s]) + p * 16, f);
+  }
 }
 
 constexpr int64_t kMaxBlocks = 152 * 64;
@@ -342,7 +357,7 @@ cudaError_t launch_expand(int d, int fmt, const Expand& in, cudaStream_t st) {
   Expand a = in;
   int64_t blocks = 0;
   for (int s = 0; s < 3; ++s) {
-    a.blocks[s] = (a.rows[s] * (d / 16) + 255) / 256;
+    a.blocks[s] = (a.rows[s] * (d / 16) + 256 * kExpandU - 1) / (256 * kExpandU);
     blocks += a.blocks[s];
   }
   const unsigned g = (unsigned)blocks;

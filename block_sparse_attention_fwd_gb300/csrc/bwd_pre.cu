@@ -17,17 +17,18 @@ namespace bl {
 
 namespace {
 
-// D[b,h,r] = sum_d G_O[b,r,h,d] * O[b,r,h,d].  One warp per (b, block of 32
+// D[b,h,r] = sum_d G_O[b,r,h,d] * O[b,r,h,d].  One warp per (b, block of ROWS
 // rows r, h), h fastest, so the eight warps of a block read neighbouring
 // heads of the same rows.  D / 8 lanes share a row (16 bytes of O and of G_O
 // each), and 32 / (D / 8) rows go per step; the loads of four steps are in
-// flight together.  Lane l keeps D of row r0 + l, so the warp writes its 32
-// values with one coalesced store.  The warp also zeroes its rows of the fp32
+// flight together.  Lane l keeps D of row r0 + l, so the warp writes its
+// values with one coalesced store.  ROWS is 32, or 8 where 32 would leave the
+// GPU short of warps (n = 1000, 8 heads of 128: 13.6 -> 5.6 us).  The warp also zeroes its rows of the fp32
 // dQ accumulator, and block 0 the status word and the word after it (the
 // tcgen05 backward's work-item counter), so no separate memset pass is needed.
 // FMT != 0: O comes as 8-bit codes ([B,n,H,D], one scale a row) and is never
 // expanded; the row's scale multiplies the finished sum of products.
-template <int D, int FMT>
+template <int D, int FMT, int ROWS>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __restrict__ o,
                                                       const __nv_bfloat16* __restrict__ g_o,
                                                       float* __restrict__ Dv,
@@ -37,20 +38,20 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
                                                       const float* __restrict__ o_scales) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPS = 32 / LPR;     // rows per step
-  constexpr int STEPS = 32 / RPS;
-  constexpr int U = 4;              // steps whose loads are in flight together
+  constexpr int STEPS = ROWS / RPS;
+  constexpr int U = STEPS < 4 ? STEPS : 4;   // steps whose loads are in flight together
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     status[0] = 0;
     status[1] = 0;
   }
-  const int nblk = (sh.n + 31) / 32;
+  const int nblk = (sh.n + ROWS - 1) / ROWS;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (w >= (int64_t)sh.B * nblk * sh.H) return;
   const int h = (int)(w % sh.H);
   const int64_t br = w / sh.H;
   const int b = (int)(br / nblk);
-  const int r0 = (int)(br % nblk) * 32;
+  const int r0 = (int)(br % nblk) * ROWS;
   const int sub = lane / LPR, c8 = (lane % LPR) * 8;
   float d_mine = 0.f;
 #pragma unroll
@@ -99,11 +100,11 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
       if (lane / RPS == s0 + u) d_mine = v;
     }
   }
-  if (r0 + lane < sh.n) Dv[((int64_t)b * sh.H + h) * sh.n + r0 + lane] = d_mine;
-  // zero the accumulator rows (b, r0..r0+31, h): D fp32 = D / 4 float4 per row
+  if (lane < ROWS && r0 + lane < sh.n) Dv[((int64_t)b * sh.H + h) * sh.n + r0 + lane] = d_mine;
+  // zero the accumulator rows (b, r0..r0+ROWS-1, h): D fp32 = D / 4 float4 per row
   constexpr int F4 = D / 4;
 #pragma unroll 4
-  for (int x = lane; x < 32 * F4; x += 32) {
+  for (int x = lane; x < ROWS * F4; x += 32) {
     const int r = r0 + x / F4;
     if (r < sh.n)
       reinterpret_cast<float4*>(dq_acc + (((int64_t)b * sh.n + r) * sh.H + h) * D)[x % F4] =
@@ -141,10 +142,17 @@ namespace {
 template <int D, int FMT>
 void launch_pre(const Shape& sh, const void* o, const uint8_t* o_codes, const float* o_scales,
                 const void* g_o, float* ws_D, float* ws_dq, int32_t* ws_status, cudaStream_t st) {
-  const int64_t warps = (int64_t)sh.B * ((sh.n + 31) / 32) * sh.H;
-  bwd_pre_kernel<D, FMT><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(
-      (const __nv_bfloat16*)o, (const __nv_bfloat16*)g_o, ws_D, ws_dq, ws_status, sh, o_codes,
-      o_scales);
+  auto launch = [&](auto kernel, int rows) {
+    const int64_t warps = (int64_t)sh.B * ((sh.n + rows - 1) / rows) * sh.H;
+    kernel<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>((const __nv_bfloat16*)o,
+                                                        (const __nv_bfloat16*)g_o, ws_D, ws_dq,
+                                                        ws_status, sh, o_codes, o_scales);
+  };
+  // 16 warps for each of 152 SMs
+  if ((int64_t)sh.B * ((sh.n + 31) / 32) * sh.H < 152 * 16)
+    launch(bwd_pre_kernel<D, FMT, 8>, 8);
+  else
+    launch(bwd_pre_kernel<D, FMT, 32>, 32);
 }
 
 }  // namespace
