@@ -32,6 +32,7 @@ import math
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib, ops
 
@@ -44,9 +45,10 @@ def default_tiles(n: int, d: int):
 class _BLAttnFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, scale, negl_prob, block_q, block_k, tile_stats, causal, window,
-                checkpoint=None, checkpoint_out=False):
+                checkpoint=None, checkpoint_out=False, checkpoint_in_forward=False):
         B, n, H, d = q.shape
         Hk = k.shape[2]
+        keep, (q, k, v) = _checkpoint_qkv((q, k, v), checkpoint, checkpoint_in_forward)
         shape = _lib.make_shape(B, n, H, Hk, d, block_q, block_k, causal, window)
         o = torch.empty_like(q)
         lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
@@ -66,7 +68,7 @@ class _BLAttnFn(torch.autograd.Function):
                     want, dtype=torch.float32, device=q.device)
         if logw is None:
             _lib.attn_fwd(shape, q, k, v, scale, o, lse, stats)
-        _save_qkvo(ctx, q, k, v, o, lse, checkpoint, checkpoint_out)
+        _save_qkvo(ctx, keep, o, lse, checkpoint if checkpoint_out else None)
         ctx.stats, ctx.logw = stats, logw
         ctx.cfg = (shape, scale, negl_prob)
         ctx.mark_non_differentiable(lse)
@@ -90,24 +92,28 @@ class _BLAttnFn(torch.autograd.Function):
                 print(f"[bl_attn] mask density per (batch, head): {dens.tolist()} "
                       f"backward skip fraction {1.0 - float(m.mean()):.4f}")
         if isinstance(q, ops.Act8):
-            return (*ops.attn_bwd_act8(shape, q, k, v, o, g_o, lse, scale, lists), *[None] * 9)
+            return (*ops.attn_bwd_act8(shape, q, k, v, o, g_o, lse, scale, lists), *[None] * 10)
         g_q = torch.empty_like(q)
         g_k = torch.empty_like(k)
         g_v = torch.empty_like(v)
         ws = torch.empty(_lib.bwd_workspace_bytes(shape), dtype=torch.uint8, device=q.device)
         _lib.attn_bwd(shape, q, k, v, o, g_o, lse, scale, lists, g_q, g_k, g_v, ws)
-        return (g_q, g_k, g_v, *[None] * 9)
+        return (g_q, g_k, g_v, *[None] * 10)
 
 
-def _save_qkvo(ctx, q, k, v, o, lse, checkpoint, checkpoint_out):
-    """Saves q, k, v, o and lse for the backward; with ``checkpoint`` q, k and v
-    (and with ``checkpoint_out`` o) in that 8-bit format, one scale a (token,
-    head)."""
-    keep = [q, k, v, o]
-    ctx.in8 = (0, 0, 0, 0)
-    if checkpoint is not None:
-        ctx.in8 = (1, 1, 1, int(checkpoint_out))
-        keep = [ops.act_save(t, checkpoint) if in8 else t for t, in8 in zip(keep, ctx.in8)]
+def _checkpoint_qkv(qkv, checkpoint, in_forward):
+    """What is kept of (q, k, v) for the backward, and what the forward reads: with
+    ``checkpoint`` Act8s, one scale a (token, head), and ``in_forward`` their values."""
+    if checkpoint is None:
+        return qkv, qkv
+    keep = [ops.act_save(t, checkpoint) for t in qkv]
+    return keep, [ops.act_load(t) for t in keep] if in_forward else qkv
+
+
+def _save_qkvo(ctx, keep, o, lse, o_format):
+    """Saves q, k, v (tensors or Act8s), o (in 8 bits with ``o_format``) and lse."""
+    keep = (*keep, o if o_format is None else ops.act_save(o, o_format))
+    ctx.in8 = tuple(int(isinstance(t, ops.Act8)) for t in keep)
     flat = []
     for t in keep:
         flat += [t.codes, t.scales] if isinstance(t, ops.Act8) else [t]
@@ -125,7 +131,9 @@ def _saved_qkvo(ctx):
 
 class _BLAttnVarlenFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, vl, scale, negl_prob, checkpoint=None, checkpoint_out=False):
+    def forward(ctx, q, k, v, vl, scale, negl_prob, checkpoint=None, checkpoint_out=False,
+                checkpoint_in_forward=False):
+        keep, (q, k, v) = _checkpoint_qkv((q, k, v), checkpoint, checkpoint_in_forward)
         o = torch.empty_like(q)
         lse = torch.empty(vl.sizes["lse"], dtype=torch.float32, device=q.device)
         stats = logw = None
@@ -139,7 +147,7 @@ class _BLAttnVarlenFn(torch.autograd.Function):
                 stats = torch.empty(vl.sizes["tile_stats"], dtype=torch.float32,
                                     device=q.device)
             _lib.attn_fwd_varlen(vl, q, k, v, scale, o, lse, stats)
-        _save_qkvo(ctx, q, k, v, o, lse, checkpoint, checkpoint_out)
+        _save_qkvo(ctx, keep, o, lse, checkpoint if checkpoint_out else None)
         ctx.stats, ctx.logw = stats, logw
         ctx.cfg = (vl, scale, negl_prob)
         ctx.mark_non_differentiable(lse)
@@ -161,7 +169,7 @@ class _BLAttnVarlenFn(torch.autograd.Function):
         ws = torch.empty(vl.sizes["bwd_workspace_bytes"], dtype=torch.uint8, device=q.device)
         _lib.attn_bwd_varlen(vl, q, k, v, o, g_o.contiguous(), lse, scale, lists, g_q, g_k, g_v,
                              ws)
-        return (g_q, g_k, g_v, *[None] * 5)
+        return (g_q, g_k, g_v, *[None] * 6)
 
 
 class _RopeFn(torch.autograd.Function):
@@ -172,6 +180,7 @@ class _RopeFn(torch.autograd.Function):
         return ops.rope(q, k, positions, plan)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_q, g_k):
         positions, = ctx.saved_tensors
         g_q, g_k = (g if g.stride(-1) == 1 else g.contiguous() for g in (g_q, g_k))
@@ -212,6 +221,7 @@ class _RMSNormFn(torch.autograd.Function):
         return (y, h) if ctx.added else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_y, g_h=None):
         *h, rstd, weight = ctx.saved_tensors
         if g_y is None:                    # only the stream behind the addition was used
@@ -261,21 +271,27 @@ class BLAttention(torch.nn.Module):
 
     ``q_norm`` and ``k_norm`` (``BLRMSNorm`` of head_dim or of heads * head_dim
     elements) and then ``rotary`` (``Rotary``; the call takes ``positions``) are
-    applied to the query and the key first.  ``checkpoint`` ("int8" or "e4m3")
-    keeps the q, k and v that the backward reads in 8 bits: the forward stays
-    exact, the gradients carry the rounding (``calibrate_negl_prob`` measures
-    it).  ``checkpoint_out`` does the same with the output; by default it stays
-    in bf16, the type in which the layer behind usually keeps it anyway."""
+    applied to the query and the key first.
+
+    ``checkpoint`` ("int8" or "e4m3") keeps the q, k and v that the backward reads
+    in 8 bits; ``checkpoint_out`` the output too, which by default stays in bf16,
+    the type in which the layer behind usually keeps it anyway.  By default the
+    forward stays exact and the gradients carry the rounding: the probabilities
+    that the backward forms from the rounded q and k no longer sum to one against
+    the exact log-sum-exp, which peaked attention amplifies.  With
+    ``checkpoint_in_forward`` the forward reads the rounded q, k and v too: its
+    output carries the rounding, and the gradients are exactly those of what it
+    computed.  ``calibrate_negl_prob`` measures either."""
 
     def __init__(self, negl_prob: float = 0.05, block_q: int | None = None,
                  block_k: int | None = None, causal: bool = False, window: int = 0,
                  q_norm: BLRMSNorm | None = None, k_norm: BLRMSNorm | None = None,
                  rotary: Rotary | None = None, checkpoint: str | None = None,
-                 checkpoint_out: bool = False):
+                 checkpoint_out: bool = False, checkpoint_in_forward: bool = False):
         super().__init__()
         _check_checkpoint(checkpoint)
-        if checkpoint_out and checkpoint is None:
-            raise ValueError("checkpoint_out needs a checkpoint format")
+        if (checkpoint_out or checkpoint_in_forward) and checkpoint is None:
+            raise ValueError("checkpoint_out and checkpoint_in_forward need a checkpoint format")
         if not (0.0 <= negl_prob < 1.0):
             raise ValueError("negl_prob must lie in [0, 1)")
         if window < 0 or (window and not causal):
@@ -285,6 +301,7 @@ class BLAttention(torch.nn.Module):
         self.causal, self.window = bool(causal), int(window)
         self.q_norm, self.k_norm, self.rotary = q_norm, k_norm, rotary
         self.checkpoint, self.checkpoint_out = checkpoint, bool(checkpoint_out)
+        self.checkpoint_in_forward = bool(checkpoint_in_forward)
 
     def _before(self, query, key, positions):
         """q/k norm and rotation of the query and the key."""
@@ -311,7 +328,7 @@ class BLAttention(torch.nn.Module):
         q, k, v = (t.contiguous() for t in (query, key, value))
         o, lse = _BLAttnFn.apply(q, k, v, float(scale), self.negl_prob, bq, bk, tile_stats,
                                  int(self.causal), self.window, self.checkpoint,
-                                 self.checkpoint_out)
+                                 self.checkpoint_out, self.checkpoint_in_forward)
         return (o, lse) if return_softmax_lse else o
 
     def varlen(self, query, key, value, cu_seqlens, scale=None, return_softmax_lse=False,
@@ -332,7 +349,7 @@ class BLAttention(torch.nn.Module):
             raise ValueError(f"cu_seqlens covers {vl.total} tokens, query has {total}")
         q, k, v = (t.contiguous() for t in (query, key, value))
         o, lse = _BLAttnVarlenFn.apply(q, k, v, vl, float(scale), self.negl_prob, self.checkpoint,
-                                       self.checkpoint_out)
+                                       self.checkpoint_out, self.checkpoint_in_forward)
         return (o, lse) if return_softmax_lse else o
 
 

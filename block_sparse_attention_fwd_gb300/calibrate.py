@@ -9,8 +9,9 @@ batch: it runs the forward with tile statistics and the dense backward once,
 then mask + sparse backward for every candidate negl_prob, measures the three
 gradients against the dense ones (``bl_grad_error``), and returns the largest
 candidate whose worst gradient meets the target.  With ``checkpoint`` the
-candidates' backward reads q, k and v (and o) from 8 bits, as
-``BLAttention(checkpoint=...)`` does, so the errors hold both roundings.
+candidates' backward (and with ``checkpoint_in_forward`` their forward) reads q,
+k and v (and with ``checkpoint_out`` o) from 8 bits, as ``BLAttention`` with the
+same arguments does, so the errors hold both roundings.
 
 Every step runs in libbl_attn.so; this module orders the calls and applies
 the selection rule (``select_negl``), which is plain host logic.
@@ -52,7 +53,8 @@ def select_negl(trials, max_rel_l2: float = 0.1, min_cos: float = 0.99):
 def calibrate_negl_prob(q, k, v, g_o, *, candidates=(0.005, 0.01, 0.02, 0.05, 0.1, 0.2),
                         max_rel_l2: float = 0.1, min_cos: float = 0.99, scale=None,
                         block: int = 128, causal: bool = False, window: int = 0,
-                        checkpoint: str | None = None, checkpoint_out: bool = False):
+                        checkpoint: str | None = None, checkpoint_out: bool = False,
+                        checkpoint_in_forward: bool = False):
     """Returns (negl_prob, trials) for bf16 device tensors q, g_o [B,n,H,d] and
     k, v [B,n,Hk,d]."""
     B, n, H, d = q.shape
@@ -79,6 +81,9 @@ def calibrate_negl_prob(q, k, v, g_o, *, candidates=(0.005, 0.01, 0.02, 0.05, 0.
     trials = []
     if checkpoint is not None:
         q8, k8, v8 = (ops.act_save(t, checkpoint) for t in (q, k, v))
+        if checkpoint_in_forward:
+            q, k, v = (ops.act_load(t) for t in (q8, k8, v8))
+            _lib.attn_fwd(shape, q, k, v, scale, o, lse, stats)
         o8 = ops.act_save(o, checkpoint) if checkpoint_out else o
     for negl in sorted(candidates):
         _lib.mask_from_stats(shape, stats, lse, float(negl), lists)

@@ -210,6 +210,8 @@ def test_modules_refuse():
         api.BLAttention(checkpoint="bf16")
     with pytest.raises(ValueError):
         api.BLAttention(checkpoint_out=True)
+    with pytest.raises(ValueError):
+        api.BLAttention(checkpoint_in_forward=True)
     t = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):                       # positions without a rotary module
         api.BLAttention()(t, t, t, positions=torch.zeros(4, 1, dtype=torch.int32))

@@ -58,7 +58,8 @@ def _attn64(q, k, v, causal):
 
 
 def _rel(a, b):
-    return float((a.double() - b.double()).norm() / b.double().norm())
+    a, b = a.detach().double(), b.detach().double()
+    return float((a - b).norm() / b.norm())
 
 
 # --- single modules --------------------------------------------------------------------
@@ -253,6 +254,44 @@ def test_attention_checkpoint_holds_half_the_bytes(bl, fmt):
     qkv, o, rows = 512 * 8 * 128, 512 * 4 * 128, 512 * 8 * 4
     assert held[None] - held[False] == qkv - rows
     assert held[False] - held[True] == o - 512 * 4 * 4
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_checkpoint_in_the_forward_is_the_gradient_of_what_it_computed(bl, fmt, varlen):
+    """The same as plain attention on the rounded tensors, forward and backward, bit for
+    bit (G_Q up to the order of its sums)."""
+    q, k, v = (_randn(1, 300, 3, 64, dtype=torch.bfloat16, seed=s).requires_grad_() for s in (80, 81, 82))
+    g = _randn(1, 300, 3, 64, dtype=torch.bfloat16, seed=83)
+    rounded = [bl.act_load(bl.act_save(t.detach(), fmt)).requires_grad_() for t in (q, k, v)]
+    got = []
+    for attn, x in ((bl.BLAttention(0.05, checkpoint=fmt, checkpoint_in_forward=True), (q, k, v)),
+                    (bl.BLAttention(0.05), rounded)):
+        if varlen:
+            o = attn.varlen(*(t[0] for t in x), [0, 100, 300])
+            got.append((o, *torch.autograd.grad(o, x, g[0])))
+        else:
+            o = attn(*x)
+            got.append((o, *torch.autograd.grad(o, x, g)))
+    for i, (a, b) in enumerate(zip(*got)):
+        if i == 1:
+            assert U.rel_l2(U.cpu(a), U.cpu(b)) <= 1e-3
+        else:
+            assert torch.equal(a, b), i
+
+
+def test_checkpoint_in_the_forward_on_peaked_attention(bl):
+    """Clustered scores of size 100: read by the forward too, int8 stays within the bar the
+    pages set for the sparse backward (rel-L2 0.1, cosine 0.99 against the dense gradients),
+    which the exact forward's gradients miss for G_Q."""
+    from block_sparse_attention_fwd_gb300 import inputs
+    from block_sparse_attention_fwd_gb300.calibrate import calibrate_negl_prob
+    w = inputs.custom("peaked8", B=1, n=2048, H=2, Hk=2, d=128, run=64, clusters=16, alpha=3.0)
+    q, k, v, go = (x.cuda() for x in inputs.generate(w, seed=7))
+    trials = [calibrate_negl_prob(q, k, v, go, candidates=(1e-4,), checkpoint="int8",
+                                  checkpoint_in_forward=f)[1][0] for f in (False, True)]
+    assert trials[1].worst_rel_l2 <= 0.1 and trials[1].worst_cos >= 0.99
+    assert trials[1].worst_rel_l2 < 0.5 * trials[0].worst_rel_l2
 
 
 def test_calibration_counts_the_checkpoint(bl):
