@@ -31,7 +31,9 @@ __device__ __forceinline__ void div_mod(int64_t x, int64_t d, int64_t& q, int64_
 // no division.  A lane holds 16 elements, so group / 16 = 2, 4 or 8
 // neighbouring lanes hold a group; a thread takes U such pieces, 256 apart, and
 // loads all of them before it works on any, which keeps U * 32 bytes of a
-// 16-bit type in flight for each thread.
+// 16-bit type in flight for each thread.  Bound by HBM: 168M bf16 elements to
+// int8 in 73 us, 6.9 TB/s (one chunk of 8 a thread and divisions to find the
+// row: 155 us).
 template <typename T, int FMT, int U>
 __global__ void __launch_bounds__(256) act_save_flat_kernel(const T* __restrict__ x,
                                                             uint8_t* __restrict__ codes,
@@ -91,7 +93,9 @@ __global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
 }
 
 // One scale a row: a warp (BLOCK: a block) goes over its row twice, for the
-// maximum and for the codes; the second reading comes from the caches.
+// maximum and for the codes; the second reading comes from the caches.  For rows
+// that the row kernels of norm_fwd.cu do not take (odd widths, more than 16384
+// columns).
 template <typename T, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
   __shared__ float buf[2][32];
@@ -136,6 +140,8 @@ __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
 }
 
 // Rows of whole groups back to back in memory, as in the flat saving kernel.
+// Bound by HBM: 168M codes to bf16 in 75 us, 6.7 TB/s (83 us with two 16-byte
+// stores a piece).
 template <typename T, int FMT, int U, bool W32>
 __global__ void __launch_bounds__(256) act_load_flat_kernel(const uint8_t* __restrict__ codes,
                                                             const float* __restrict__ scales,
@@ -211,7 +217,8 @@ __global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
 
 // q, k and v of an attention, [tokens, heads, D] codes with one scale a
 // (token, head), to bf16: pieces of 16 as in the flat loading kernel.  The blocks
-// of the three tensors follow one another.
+// of the three tensors follow one another.  Bound by HBM and, at attention
+// sizes, by the ramp up and down: 19M elements in 15 us.
 template <int D, int FMT, bool W32>
 __global__ void __launch_bounds__(256) expand_kernel(Expand a) {
   constexpr int PER_ROW = D / 16, U = kExpandU;

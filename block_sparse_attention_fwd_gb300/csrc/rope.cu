@@ -15,13 +15,17 @@
 // fp64, whose rate here is low, and without a table to read.  Its upper two
 // bits, rounded, are the quadrant; the rest, |x| <= pi / 4, goes through the
 // Taylor series of sine and cosine (to x^9 and x^8: the next terms are below
-// 2^-25), which is an order of magnitude less work than the general functions.
+// 2^-25), within 1.7 * 2^-24 of the exact values; the general sincospi took the
+// largest share of a pass over single heads (44 -> 36 us at 100000 tokens).
 //
 // The pass is bound by HBM: q and k once in, once out.  A block takes a tile of
 // tokens.  It forms the tile's sines and cosines once, in shared memory, and
 // then goes over the (token, head) units of the tile, 256 / lanes of them at a
 // time, a group of lanes with 16-byte vectors on each; a thread has the vectors
 // of U units in flight, the first of them from before the sines are formed.
+// Measured: 40 + 40 heads of 128 at 32760 tokens in 208 us, 6.5 TB/s
+// (interleaved), and 196 us, 6.8 TB/s (halves); each thread forming the sines of
+// its own vectors took 328 and 244 us.
 #include "kernels.h"
 #include "rows.cuh"
 
