@@ -94,15 +94,14 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
   }
 }
 
-// The same for rows whose chunks are whole and aligned, on a grid that fills the
-// GPU once: a block takes rows gridDim.x apart, and x and r of the next S - 1
-// of them are on their way to shared memory meanwhile, each thread's chunks into
-// places of its own.  Loading straight into registers instead leaves the
-// memory idle while a row is reduced.  Bound by HBM: 32760 x 5120 bf16 in 100 us,
-// with the residual in 196 us (6.8 TB/s), with the residual to e4m3 in 175 us
-// (6.7 TB/s; issue slots are 74% busy there).  FMT8: 0 without the 8-bit output, else
-// its format.  NORM = false only saves x in 8 bits with
-// one scale a row: the same walk without the norm.
+// The same for rows whose chunks are whole and aligned: a block takes rows
+// gridDim.x apart, and x and r of the next S - 1 of them are on their way to
+// shared memory meanwhile, each thread's chunks into places of its own.  Loading
+// straight into registers instead leaves the memory idle while a row is reduced.
+// Bound by HBM: 32760 x 5120 bf16 in 100 us, with the residual in 196 us
+// (6.8 TB/s), with the residual to e4m3 in 175 us (6.7 TB/s; issue slots are 74%
+// busy there).  FMT8: 0 without the 8-bit output, else its format.  NORM = false
+// only saves x in 8 bits with one scale a row: the same walk without the norm.
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk

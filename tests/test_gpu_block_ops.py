@@ -132,6 +132,18 @@ def test_rope_takes_views_and_works_in_place(bl):
     odd.copy_(want[0])
     assert torch.equal(bl.rope(odd, None, pos, plan, inverse=True)[0],
                        bl.rope(want[0], None, pos, plan, inverse=True)[0])
+    # batches that do not follow one another, and heads before tokens
+    long = _randn(2, 90, 4, 64, dtype=torch.bfloat16, seed=40)
+    part = long[:, 20:70]
+    ref = bl.rope(part.contiguous(), None, pos, plan)[0]
+    assert torch.equal(bl.rope(part, None, pos, plan)[0], ref)
+    before = long.clone()
+    bl.rope(part, None, pos, plan, inplace=True)
+    assert torch.equal(part, ref) and torch.equal(long[:, :20], before[:, :20])
+    assert torch.equal(long[:, 70:], before[:, 70:])
+    bhsd = _randn(2, 4, 50, 64, dtype=torch.bfloat16, seed=41)
+    ref = bl.rope(bhsd.transpose(1, 2).contiguous(), None, pos, plan)[0]
+    assert torch.equal(bl.rope(bhsd.transpose(1, 2), None, pos, plan)[0], ref)
     # packed tensors
     flat = bl.rope(want[0].flatten(0, 1), want[1].flatten(0, 1), pos.repeat(2, 1), plan)
     again = bl.rope(want[0], want[1], pos, plan)
