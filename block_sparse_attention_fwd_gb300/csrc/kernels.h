@@ -69,7 +69,7 @@ cudaError_t launch_grad_error(const void* a, const void* b, int64_t n, double* o
 cudaError_t launch_combine(int parts, int B, int n, int H, int d, const void* o_parts,
                            const float* lse_parts, void* o, float* lse, cudaStream_t st);
 
-// Rows of a root-mean-square norm (norm.cu).  Strides in elements; y, h, g_y,
+// Rows of a root-mean-square norm (norm.cuh).  Strides in elements; y, h, g_y,
 // g_x, g_h and codes are contiguous [rows, cols].
 struct NormFwd {
   int64_t rows, cols, x_stride, r_stride, groups;
@@ -113,7 +113,7 @@ struct ActLoad {
   int group, fmt;
 };
 cudaError_t launch_act_save(int dtype, const ActSave& a, cudaStream_t st);
-// With one scale a row, where the row kernels of norm.cu take the rows
+// With one scale a row, where the row kernels of norm_fwd.cu take the rows
 // (cudaErrorNotSupported, and nothing launched, where they do not).
 cudaError_t launch_row_save(int dtype, const ActSave& a, cudaStream_t st);
 cudaError_t launch_act_load(int dtype, const ActLoad& a, cudaStream_t st);

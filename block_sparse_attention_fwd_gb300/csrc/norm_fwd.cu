@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
   const int64_t stride = (int64_t)gridDim.x * R.here;
   // the thread's place in stage s, chunk k: x, and r another nt * CB behind
   auto place = [&](int s, int k) -> uint8_t* {
-    return ring + (s * NV + k) * nt * 2 * CB + threadIdx.x * 16;
+    return ring + (s * NV + k) * nt * (NORM ? 2 : 1) * CB + threadIdx.x * 16;
   };
   auto fetch = [&](int s, int64_t row) {
     if (row < a.rows) {
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
 // work on neighbouring rows: 5120 columns 84 -> 99% of the copy rate without and
 // 90 -> 101% with a residual, 128 columns 83 -> 96%; blocks of fewer rows lose it
 // again to filling their rings (4096 rows of 4096: 87 -> 70% at eight times).
-int fwd_blocks(int64_t rows, const Plan& p, size_t smem) {
-  const int once = resident(p.threads, 64, smem);
+int fwd_blocks(int64_t rows, const Plan& p, int regs, size_t smem) {
+  const int once = resident(p.threads, regs, smem);
   int64_t times = rows / ((int64_t)once * p.here * 6);
   if (times > 8) times = 8;
   if (times < 1) times = 1;
@@ -266,14 +266,14 @@ cudaError_t fwd(const NormFwd& a, bool vec, cudaStream_t st) {
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
     if constexpr (N <= 2) {
-      const size_t stage = (size_t)N * p.threads * 2 * sizeof(Chunk<T>);
+      const size_t stage = (size_t)N * p.threads * (NORM ? 2 : 1) * sizeof(Chunk<T>);
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
         constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM>;
         const size_t smem = S * stage;
         e = allow_smem<k>();
         if (e == cudaSuccess)
-          k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, smem)), p.threads, smem, st>>>(a);
+          k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, NORM ? 64 : 48, smem)), p.threads, smem, st>>>(a);
       };
       if (vec && (L != 0 || N == 1 || 3 * stage <= kMaxSmem / 2))
         ring(Int<NORM ? 3 : 2>());

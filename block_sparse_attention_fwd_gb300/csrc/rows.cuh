@@ -1,5 +1,5 @@
 // Rows of a matrix in chunks of 8 consecutive elements, the unit that the row
-// kernels (norm.cu, act8.cu) load, keep in registers and store: 16 bytes of
+// kernels (norm_fwd.cu, norm_bwd.cu, act8.cu) load, keep in registers and store: 16 bytes of
 // a 16-bit type, 32 of fp32, 8 of codes.  With VEC a chunk is whole and
 // aligned and moves in one or two vector instructions; otherwise element by
 // element under a count of valid elements (odd widths, views whose rows start
