@@ -194,19 +194,26 @@ __global__ void __launch_bounds__(256) act_load_kernel(ActLoad a) {
     float f[8];
     decode8<FMT>(c, f);
     float scale = a.scales[row * a.groups + (col >> shift)];
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (!WHOLE) {
-        if (i > 0 && i < valid && (col == a.cols || (col & ((1ll << shift) - 1)) == 0)) {
+      for (int i = 0; i < 8; ++i) f[i] *= scale;
+    } else {
+      // elements up to the next border, and those behind it
+      int here = (int)min(min(((col >> shift) + 1) << shift, a.cols) - col, (int64_t)8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i == here && i < valid) {
+          col += here;
           if (col == a.cols) {
             col = 0;
             ++row;
           }
           scale = a.scales[row * a.groups + (col >> shift)];
+          here += (int)min(min(((col >> shift) + 1) << shift, a.cols) - col, (int64_t)8);
+          col -= i;                                   // so that adding `here` leads on
         }
-        ++col;
+        f[i] *= scale;
       }
-      f[i] *= scale;
     }
     if (VEC && valid == 8)
       store8<T, true>(static_cast<T*>(a.x) + x, f, 8);
@@ -276,7 +283,11 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
   // one scale a row of 32, 64 or 128 elements is one scale a group
   if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
-  if (!a.group) {
+  const bool flat = a.x_stride == a.cols && flat_shift(a.cols, a.group) >= 0 &&
+                    aligned_to(a.x, 16) && aligned_to(a.codes, 16);
+  // whole rows, and groups of rows that are aligned at least
+  if (!flat && (!a.group || (a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
+                             aligned_to(a.codes, 8)))) {
     const cudaError_t e = launch_row_save(dtype, a, st);
     if (e != cudaErrorNotSupported) return e;
   }
@@ -284,9 +295,8 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
                      aligned_to(a.codes, 8);
-    const int shift = a.x_stride == a.cols && aligned_to(a.x, 16) && aligned_to(a.codes, 16)
-                          ? flat_shift(a.cols, a.group) : -1;
-    if (shift >= 0) {
+    if (flat) {
+      const int shift = flat_shift(a.cols, a.group);
       const int64_t pieces = a.rows * (a.cols / 16);
       const unsigned g = (unsigned)((pieces + 256 * kFlatU - 1) / (256 * kFlatU));
       auto* x = static_cast<const T*>(a.x);

@@ -42,6 +42,17 @@ struct Rows {
     }
   }
 };
+// Whether the lane in front (behind) of this one's holds the chunk in front
+// (behind): not across the ends of a warp or, with LPR, of a row's lanes.
+template <int LPR>
+__device__ __forceinline__ bool lane_in_front(const Rows<LPR>& R) {
+  return LPR ? R.t > 0 : (threadIdx.x & 31) > 0;
+}
+template <int LPR>
+__device__ __forceinline__ bool lane_behind(const Rows<LPR>& R) {
+  return LPR ? R.t < LPR - 1 : (threadIdx.x & 31) < 31;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v, float (*buf)[32], int& slot) {
   if constexpr (LPR != 0) return lanes_sum(v, LPR);
@@ -57,8 +68,9 @@ __device__ __forceinline__ float row_sum(float v, float (*buf)[32], int& slot) {
 struct Plan {
   int lpr, nv, threads, here;
 };
-inline Plan plan(int64_t cols, int max_threads, int warp_chunks) {
-  const int chunks = (int)((cols + 7) / 8);
+inline Plan plan(int64_t cols, int max_threads, int warp_chunks, bool odd = false) {
+  // rows that start anywhere need a place for one vector more
+  const int chunks = (int)((cols + 7) / 8) + (odd ? 1 : 0);
   Plan p;
   if (chunks <= warp_chunks) {
     p.lpr = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
@@ -90,6 +102,11 @@ inline unsigned grid(int64_t rows, int here, int most) {
   const int64_t blocks = (rows + here - 1) / here;
   return (unsigned)(blocks < most ? blocks : most);
 }
+
+// The ring kernels for rows of 16-bit types that start anywhere (norm_fwd_odd.cu,
+// norm_bwd_odd.cu); cudaErrorNotSupported where a row is too wide for them.
+cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st);
+cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 
 // Calls f(lanes a row, chunks a thread) as compile-time constants.
 template <int N> struct Int { static constexpr int value = N; };

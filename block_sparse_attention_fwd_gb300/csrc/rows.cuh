@@ -110,6 +110,18 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const uint64_t (&f)[4]
     reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&c)[i];
 }
 
+// Four pairs rounded to a 16-bit type.
+template <typename T>
+__device__ __forceinline__ void pack_words(const uint64_t (&f)[4], uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f[i], lo, hi);
+    const Pair<T> p(lo, hi);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], int valid) {
   const Chunk<T> c = pack8<T>(f);
@@ -307,10 +319,133 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
                  : "memory");
 }
+// The same for the first `size` bytes (0 to BYTES), the others become zero.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int size) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(size)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
+                 "r"(size)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Rows that start anywhere.  The aligned vectors that cover such a row are
+// copied whole; chunk c of the row lies in vectors c and c + 1, shifted by the
+// row's misalignment.  Writing, a lane's aligned vector is made of the end of the
+// chunk of the lane in front and the beginning of its own.
+
+// Bytes shift .. shift + 4 W of the 8 W bytes in w (4 W a power of two).
+template <int W>
+__device__ __forceinline__ void shift_bytes(uint32_t (&w)[2 * W], int shift, uint32_t (&out)[W]) {
+#pragma unroll
+  for (int step = W / 2; step > 0; step /= 2)
+    if (shift & (4 * step)) {
+#pragma unroll
+      for (int i = 0; i + step < 2 * W; ++i) w[i] = w[i + step];
+    }
+  const int bits = (shift & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
+}
+
+// Copies aligned vector c of the row of `cols` 16-bit elements at `row` (c = 0
+// holds its beginning); what lies behind the row's end becomes zero.  A vector may
+// begin up to 14 bytes in front of the row, within the same aligned 16 bytes.
+template <typename T>
+__device__ __forceinline__ void copy_odd(void* place, const T* row, int c, int cols) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+  const uintptr_t from = (at & ~(uintptr_t)15) + (uintptr_t)c * 16, end = at + (uintptr_t)cols * 2;
+  const int left = from < end ? (int)(end - from) : 0;
+  copy_async<16>(place, reinterpret_cast<const void*>(left ? from : at & ~(uintptr_t)15),
+                 left < 16 ? left : 16);
+}
+
+// The thread's chunk of a row that copy_odd brought to places `p`, one vector a
+// thread and then, nt places on, the next chunks of the same threads; t is the
+// thread's first chunk.
+template <typename T, int LPR>
+__device__ __forceinline__ Chunk<T> chunk_odd(const uint8_t* p, int t, int nt, const T* row) {
+  // behind the last lane of a row comes its first lane's next place
+  const uint8_t* next = LPR && t == LPR - 1 ? p + (nt - (LPR - 1)) * 16 : p + 16;
+  const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(next);
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  Chunk<T> c;
+  shift_bytes<4>(w, (int)(reinterpret_cast<uintptr_t>(row) & 15),
+                 *reinterpret_cast<uint32_t(*)[4]>(&c));
+  return c;
+}
+
+// The same for codes: vectors of 8 bytes.
+__device__ __forceinline__ void copy_odd8(void* place, const uint8_t* row, int c, int cols) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+  const uintptr_t from = (at & ~(uintptr_t)7) + (uintptr_t)c * 8, end = at + (uintptr_t)cols;
+  const int left = from < end ? (int)(end - from) : 0;
+  copy_async<8>(place, reinterpret_cast<const void*>(left ? from : at & ~(uintptr_t)7),
+                left < 8 ? left : 8);
+}
+template <int LPR>
+__device__ __forceinline__ Codes codes_odd(const uint8_t* p, int t, int nt, const uint8_t* row) {
+  const uint8_t* next = LPR && t == LPR - 1 ? p + (nt - (LPR - 1)) * 8 : p + 8;
+  const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(next);
+  uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+  Codes c;
+  shift_bytes<2>(w, (int)(reinterpret_cast<uintptr_t>(row) & 7), c.w);
+  return c;
+}
+
+// Writes the chunks (8 elements of W / 2 bytes) that the lanes hold to the row at
+// `row`: chunk c, of which `valid` elements exist.  `front` and `behind`: whether
+// the lane in front (behind) holds the chunk in front (behind), whose valid
+// elements are then those of a row of `cols`.  The whole warp takes part.
+template <int W>
+__device__ __forceinline__ void store_anywhere(uint8_t* row, int c, int valid, int cols, bool front,
+                                               bool behind, const uint32_t (&w)[W]) {
+  constexpr int E = W / 2;                            // bytes of an element
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & (4 * W - 1));
+  const int k = off / E;                              // elements of the chunk in front
+  uint32_t both[2 * W], out[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    both[i] = __shfl_up_sync(0xffffffffu, w[i], 1);
+    both[W + i] = w[i];
+  }
+  uint8_t* p = row + c * (4 * W);
+  const bool whole = valid >= 8 - k && (k == 0 || front);
+  if (whole) {
+    if (k == 0) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] = w[i];
+    } else {
+      shift_bytes<W>(both, 4 * W - off, out);
+    }
+    if constexpr (W == 4)
+      *reinterpret_cast<uint4*>(p - off) = make_uint4(out[0], out[1], out[2], out[3]);
+    else
+      *reinterpret_cast<uint2*>(p - off) = make_uint2(out[0], out[1]);
+  }
+  // what no lane's vector holds, element by element
+  const int next = min(cols - (c + 1) * 8, 8);        // valid elements of the chunk behind
+  const int from = whole ? 8 - k : 0;
+  const int to = behind && next >= 8 - k ? min(valid, 8 - k) : valid;
+  if (from < to) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= from && i < to) {
+        const uint32_t bits = w[i * E / 4] >> (8 * (i * E % 4));
+        if constexpr (E == 2)
+          reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)bits;
+        else
+          p[i] = (uint8_t)bits;
+      }
+  }
 }
 
 // A weight row of type T or fp32 (or none: ones).

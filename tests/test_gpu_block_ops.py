@@ -195,7 +195,8 @@ def test_rope_refusals(bl):
 # --- norm -----------------------------------------------------------------------
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (1000, 64), (517, 128), (33, 129), (5, 256), (9, 264), (7, 1000),
-          (4, 1001), (6, 2048), (3, 5120), (2, 5123), (700, 7168), (2, 16384)]
+          (4, 1001), (6, 2048), (3, 5120), (2, 5123), (700, 7168), (2, 16384), (5000, 7), (3001, 129), (2000, 250), (900, 777), (1501, 1001), (800, 5123),
+          (40, 16383)]
 
 
 def _norm_inputs(rows, cols, dtype, wtype):
@@ -224,7 +225,8 @@ def test_norm_forward(bl, rows, cols, dtype):
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (257, 64), (65, 128), (33, 136), (9, 264),
-                                       (5, 1000), (4, 1001), (3, 5120), (2, 16384)])
+                                       (5, 1000), (4, 1001), (3, 5120), (2, 16384), (3001, 129),
+                                       (900, 777), (700, 2563)])
 def test_norm_forward_in_8_bits(bl, rows, cols, group, fmt):
     """Codes stand for y within half a step of their format; y beside them is the plain call's."""
     t = torch.bfloat16
@@ -296,6 +298,76 @@ def test_norm_takes_views(bl):
         bl.rms_norm_fwd(big.transpose(0, 1)[..., :128], w)
 
 
+@pytest.mark.parametrize("cols", [24, 136, 1000, 2568])
+def test_norm_rows_that_start_anywhere(bl, cols):
+    """Every misalignment of base and stride: the aligned call's values (codes bit for bit)."""
+    rows = 37
+    w = _randn(cols, dtype=torch.float32, seed=cols)
+    x, r = _randn(rows, cols, dtype=torch.bfloat16, seed=1), _randn(rows, cols, dtype=torch.bfloat16, seed=2)
+    want = bl.rms_norm_fwd(x, w, residual=r)
+    want8 = bl.act_save(x, "int8", 32), bl.act_save(x, "e4m3", 0)
+    for off in range(8):
+        for pad in (0, 1, 3, 6):
+            buf = torch.full((rows * (cols + pad) + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+            view = buf[off:off + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+            view.copy_(x)
+            got = bl.rms_norm_fwd(view, w, residual=r)
+            # sums of the odd layout's threads may run in another order
+            for a, b in zip(got, want):
+                assert U.rel_l2(U.cpu(a), U.cpu(b)) <= 2.0 ** -10 and torch.isfinite(a).all()
+            for f, a in zip((("int8", 32), ("e4m3", 0)), want8):
+                b = bl.act_save(view, *f)
+                assert torch.equal(a.codes.view(torch.uint8), b.codes.view(torch.uint8))
+                assert torch.equal(a.scales, b.scales)
+
+
+@pytest.mark.parametrize("cols", [1, 9, 129, 264, 1001, 1030, 5123])
+@pytest.mark.parametrize("off", [0, 1, 3, 6])
+def test_outputs_that_start_anywhere_keep_their_neighbours(bl, cols, off):
+    """Through the C ABI, every output in the middle of a buffer: the bytes in front of it and
+    behind it stay, and all of its own are written."""
+    import ctypes
+    from block_sparse_attention_fwd_gb300 import _lib
+    lib = _lib.load()
+    rows, dev = 21, "cuda"
+    x, r = _randn(rows, cols, dtype=torch.bfloat16, seed=3), _randn(rows, cols, dtype=torch.bfloat16, seed=4)
+    n = rows * cols
+
+    def room(dtype, fill):
+        whole = torch.full((n + 64,), fill, dtype=dtype, device=dev)
+        return whole, whole[16 + off:16 + off + n]
+
+    def untouched(whole, fill):
+        return bool((whole[:16 + off] == fill).all() and (whole[16 + off + n:] == fill).all())
+
+    y, h, g = (room(torch.bfloat16, 7.0) for _ in range(3))
+    codes, saved = room(torch.int8, 77), room(torch.int8, 77)
+    scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    act = _lib.Act8Struct(codes[1].data_ptr(), scales.data_ptr(), 1, 0)
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.bl_rms_norm_fwd(rows, cols, 0, x.data_ptr(), cols, r.data_ptr(), cols, None, 0, 1e-6,
+                               y[1].data_ptr(), h[1].data_ptr(), rstd.data_ptr(), ctypes.byref(act), s) == 0
+    ry, rh, rr = bl.rms_norm_fwd(x, None, residual=r)
+    assert U.rel_l2(U.cpu(y[1]), U.cpu(ry).ravel()) <= 2.0 ** -10
+    assert torch.equal(h[1], rh.flatten())
+    assert untouched(y[0], 7.0) and untouched(h[0], 7.0) and untouched(codes[0], 77)
+    value = U.cpu(codes[1]).reshape(rows, cols) * U.cpu(scales)[:, None]
+    assert np.abs(value - U.cpu(ry)).max() <= 0.5 * U.cpu(scales).max() * 1.02 + 2.0 ** -8 * np.abs(U.cpu(ry)).max()
+    assert lib.bl_rms_norm_bwd(rows, cols, 0, x.data_ptr(), h[1].data_ptr(), None, rstd.data_ptr(), None,
+                               0, r.data_ptr(), g[1].data_ptr(), None, None, 0, s) == 0
+    want = bl.rms_norm_bwd(x, rh, rstd, None, g_h=r, need_g_w=False)[0]
+    assert U.rel_l2(U.cpu(g[1]), U.cpu(want).ravel()) <= 2.0 ** -9 and untouched(g[0], 7.0)
+    own = torch.empty(rows, dtype=torch.float32, device=dev)
+    act = _lib.Act8Struct(saved[1].data_ptr(), own.data_ptr(), 1, 0)
+    assert lib.bl_act_save(rows, cols, 0, x.data_ptr(), cols, ctypes.byref(act), s) == 0
+    ref = bl.act_save(x)
+    assert torch.equal(saved[1], ref.codes.flatten()) and untouched(saved[0], 77)
+    back = room(torch.bfloat16, 7.0)
+    assert lib.bl_act_load(rows, cols, 0, ctypes.byref(act), back[1].data_ptr(), s) == 0
+    assert torch.equal(back[1], bl.act_load(ref).flatten()) and untouched(back[0], 7.0)
+
+
 def test_norm_edge_rows(bl):
     """A zero row, an infinity and a NaN stay within their rows; no rows at all."""
     x = _randn(4, 512, dtype=torch.bfloat16, seed=11)
@@ -352,7 +424,8 @@ def _codes_np(a):
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (2, 5), (300, 64), (77, 128), (1, 32), (5, 96), (33, 130),
-                                       (4, 1000), (3, 1001), (2, 5120), (2, 20000)])
+                                       (4, 1000), (3, 1001), (2, 5120), (2, 20000), (3001, 129),
+                                       (900, 777), (500, 2563), (2000, 7)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_saved_codes_are_the_definition_bit_for_bit(bl, rows, cols, group, fmt, dtype):
     t = TYPES[dtype]
