@@ -284,17 +284,17 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
   // one scale a row of 32, 64 or 128 elements is one scale a group
   if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
   const bool flat = a.x_stride == a.cols && flat_shift(a.cols, a.group) >= 0 &&
-                    aligned_to(a.x, 16) && aligned_to(a.codes, 16);
+                    aligned_to(a.x, chunk_align(dtype)) && aligned_to(a.codes, 16);
   // whole rows, and groups of rows that are aligned at least
-  if (!flat && (!a.group || (a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
-                             aligned_to(a.codes, 8)))) {
+  if (!flat && (!a.group || (a.cols % 8 == 0 && a.x_stride % 8 == 0 &&
+                             aligned_to(a.x, chunk_align(dtype)) && aligned_to(a.codes, 8)))) {
     const cudaError_t e = launch_row_save(dtype, a, st);
     if (e != cudaErrorNotSupported) return e;
   }
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
-    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
-                     aligned_to(a.codes, 8);
+    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 &&
+                     aligned_to(a.x, chunk_align(dtype)) && aligned_to(a.codes, 8);
     if (flat) {
       const int shift = flat_shift(a.cols, a.group);
       const int64_t pieces = a.rows * (a.cols / 16);
@@ -333,7 +333,7 @@ cudaError_t launch_act_load(int dtype, const ActLoad& in, cudaStream_t st) {
   if (!a.group && (a.cols == 32 || a.cols == 64 || a.cols == 128)) a.group = (int)a.cols;
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
-    const bool vec = aligned_to(a.x, 16) && aligned_to(a.codes, 8);
+    const bool vec = aligned_to(a.x, chunk_align(dtype)) && aligned_to(a.codes, 8);
     const int shift = aligned_to(a.x, 16) && aligned_to(a.codes, 16)
                           ? flat_shift(a.cols, a.group) : -1;
     if (shift >= 0) {

@@ -137,9 +137,11 @@ cudaError_t launch_norm_bwd(int dtype, const NormBwd& in, void* g_w, cudaStream_
   a.shift = group_shift(a.group);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
-    const bool vec = a.cols % 8 == 0 && aligned_to(a.g_y, 16) && aligned_to(a.h, 16) &&
-                     aligned_to(a.g_h, 16) && aligned_to(a.g_x, 16) && aligned_to(a.w, 16) &&
-                     aligned_to(a.codes, 8) && aligned_to(a.partial, 16);
+    const size_t al = chunk_align(dtype);
+    const bool vec = a.cols % 8 == 0 && aligned_to(a.g_y, al) && aligned_to(a.h, al) &&
+                     aligned_to(a.g_h, al) && aligned_to(a.g_x, al) &&
+                     aligned_to(a.w, a.w_f32 ? 32 : 16) && aligned_to(a.codes, 8) &&
+                     aligned_to(a.partial, 32);
     int blocks = 0;
     if (a.rows > 0) {
       const cudaError_t e = !a.codes              ? bwd<T, 0>(dtype, a, vec, &blocks, st)

@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
 #pragma unroll
           for (int v = 0; v < CB / 16; ++v) {
             constexpr int E = 16 / sizeof(T);
-            copy_async<16>(p + v * nt * 16, gy + off + v * E);
-            if (a.g_h) copy_async<16>(p + plane + v * nt * 16, gh + off + v * E);
-            if constexpr (FMT == 0) copy_async<16>(p + 2 * plane + v * nt * 16, h + off + v * E);
+            copy_chunk<CB>(p + v * nt * 16, gy + off + v * E);
+            if (a.g_h) copy_chunk<CB>(p + plane + v * nt * 16, gh + off + v * E);
+            if constexpr (FMT == 0) copy_chunk<CB>(p + 2 * plane + v * nt * 16, h + off + v * E);
           }
           if constexpr (FMT != 0) copy_async<8>(codes_at(place, k), codes + off);
         }

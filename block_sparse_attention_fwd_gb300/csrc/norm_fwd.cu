@@ -119,9 +119,11 @@ cudaError_t launch_norm_fwd(int dtype, const NormFwd& in, cudaStream_t st) {
   a.shift = group_shift(a.group);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
+    const size_t al = chunk_align(dtype);
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
-                     aligned_to(a.x, 16) && aligned_to(a.r, 16) && aligned_to(a.h, 16) &&
-                     aligned_to(a.y, 16) && aligned_to(a.w, 16) && aligned_to(a.codes, 8);
+                     aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.h, al) &&
+                     aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) &&
+                     aligned_to(a.codes, 8);
     const int fmt = a.codes ? a.fmt : 0;
     return fmt == 0          ? fwd<T, 0>(dtype, a, vec, st)
            : fmt == kFmtInt8 ? fwd<T, kFmtInt8>(dtype, a, vec, st)
@@ -135,8 +137,8 @@ cudaError_t launch_row_save(int dtype, const ActSave& s, cudaStream_t st) {
   a.rows = s.rows; a.cols = s.cols; a.x_stride = s.x_stride; a.groups = s.groups;
   a.x = s.x; a.codes = s.codes; a.scales = s.scales;
   a.group = s.group; a.fmt = s.fmt; a.shift = group_shift(s.group);
-  const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) &&
-                   aligned_to(a.codes, 8);
+  const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 &&
+                   aligned_to(a.x, chunk_align(dtype)) && aligned_to(a.codes, 8);
   if (!vec) return fwd_odd(dtype, false, a, st);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;

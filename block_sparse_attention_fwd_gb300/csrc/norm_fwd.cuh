@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
 #pragma unroll
           for (int v = 0; v < CB / 16; ++v) {
             constexpr int E = 16 / sizeof(T);
-            copy_async<16>(p + v * nt * 16, x + c * 8 + v * E);
-            if (NORM && a.r) copy_async<16>(p + plane + v * nt * 16, r + c * 8 + v * E);
+            copy_chunk<CB>(p + v * nt * 16, x + c * 8 + v * E);
+            if (NORM && a.r) copy_chunk<CB>(p + plane + v * nt * 16, r + c * 8 + v * E);
           }
         }
       }

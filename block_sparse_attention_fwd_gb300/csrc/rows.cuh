@@ -49,16 +49,37 @@ struct alignas(8) Codes {
   uint32_t w[2];
 };
 
+// 16 or 32 bytes in one instruction each way (32: 32-byte aligned).  Two 16-byte
+// stores of a lane, 32 bytes apart from lane to lane, write every 32-byte sector
+// in two halves.
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[4]) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+}
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 8 elements at p, of which `valid` exist (the others read as zero).
 template <typename T, bool VEC>
 __device__ __forceinline__ Chunk<T> load8(const T* __restrict__ p, int valid) {
   Chunk<T> c;
-  constexpr int NW = sizeof(Chunk<T>) / 16;
   if constexpr (VEC) {
+    uint32_t(&w)[sizeof(c) / 4] = *reinterpret_cast<uint32_t(*)[sizeof(c) / 4]>(&c);
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
-      reinterpret_cast<uint4*>(&c)[i] =
-          valid > 0 ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < (int)(sizeof(c) / 4); ++i) w[i] = 0;
+    if (valid > 0) load_words(p, w);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c.e[i] = i < valid ? p[i] : from_f32<T>(0.f);
@@ -105,9 +126,7 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const uint64_t (&f)[4]
     f2_unpack(f[i], lo, hi);
     reinterpret_cast<Pair<T>*>(&c)[i] = Pair<T>(lo, hi);
   }
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(c) / 16; ++i)
-    reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&c)[i];
+  store_words(p, *reinterpret_cast<const uint32_t(*)[sizeof(c) / 4]>(&c));
 }
 
 // Four pairs rounded to a 16-bit type.
@@ -125,13 +144,8 @@ __device__ __forceinline__ void pack_words(const uint64_t (&f)[4], uint32_t (&w)
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], int valid) {
   const Chunk<T> c = pack8<T>(f);
-  constexpr int NW = sizeof(Chunk<T>) / 16;
   if constexpr (VEC) {
-    if (valid > 0) {
-#pragma unroll
-      for (int i = 0; i < NW; ++i)
-        reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&c)[i];
-    }
+    if (valid > 0) store_words(p, *reinterpret_cast<const uint32_t(*)[sizeof(c) / 4]>(&c));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -139,25 +153,22 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const float (&f)[8], i
   }
 }
 
-// 16 values rounded to T and written to 16 consecutive elements.  W32 (32-byte
-// aligned): a thread writes whole 32-byte sectors with one instruction each;
-// two 16-byte stores, 32 bytes apart from lane to lane, would write every sector
-// in two halves.
+// 16 values rounded to T and written to 16 consecutive elements, 32-byte aligned
+// with W32, 16-byte aligned without.
 template <typename T, bool W32>
 __device__ __forceinline__ void store16(T* __restrict__ p, const float (&f)[2][8]) {
-  if constexpr (W32) {
+  if constexpr (W32 && sizeof(T) == 2) {
     struct alignas(16) { Chunk<T> c[2]; } both = {{pack8<T>(f[0]), pack8<T>(f[1])}};
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&both);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(both) / 32; ++i)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                       reinterpret_cast<uint8_t*>(p) + 32 * i),
-                   "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]),
-                   "r"(w[8 * i + 4]), "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                   : "memory");
-  } else {
+    store_words(p, *reinterpret_cast<const uint32_t(*)[8]>(&both));
+  } else if constexpr (W32 || sizeof(T) == 2) {
     store8<T, true>(p, f[0], 8);
     store8<T, true>(p + 8, f[1], 8);
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      reinterpret_cast<float4*>(p)[v] = make_float4(f[v / 2][4 * (v % 2)], f[v / 2][4 * (v % 2) + 1],
+                                                    f[v / 2][4 * (v % 2) + 2],
+                                                    f[v / 2][4 * (v % 2) + 3]);
   }
 }
 
@@ -319,6 +330,20 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
                  : "memory");
 }
+// 16 bytes that share their 32-byte sector with another copy of the same thread:
+// through L1, so that the sector comes once.
+__device__ __forceinline__ void copy_async_half(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+// 16 bytes of a chunk of CB.
+template <int CB>
+__device__ __forceinline__ void copy_chunk(void* dst, const void* src) {
+  if constexpr (CB == 16)
+    copy_async<16>(dst, src);
+  else
+    copy_async_half(dst, src);
+}
 // The same for the first `size` bytes (0 to BYTES), the others become zero.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int size) {
@@ -469,6 +494,9 @@ __device__ __forceinline__ void load_weight8(const void* w, bool f32, int64_t co
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
+
+// Bytes that a vector of 8 elements wants to be aligned to.
+inline size_t chunk_align(int dtype) { return dtype == 2 ? 32 : 16; }
 
 // Calls f with a null pointer of the element type that `dtype` (BL_BF16,
 // BL_FP16, BL_FP32) names.
