@@ -183,7 +183,7 @@ class _RopeFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g_q, g_k):
         positions, = ctx.saved_tensors
-        g_q, g_k = (g if g.stride(-1) == 1 else g.contiguous() for g in (g_q, g_k))
+        g_q, g_k = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (g_q, g_k))
         return (*ops.rope(g_q, g_k, positions, ctx.plan, inverse=True), None, None)
 
 

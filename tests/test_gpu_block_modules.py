@@ -155,6 +155,19 @@ def test_rotary_module_gradients(bl):
     assert _rel(only, torch.autograd.grad(_rope64(q64, pos, rot.plan).sum(), q64)[0]) <= 2e-6
 
 
+def test_rotary_module_without_a_key(bl):
+    rot = bl.Rotary(64, (32,))
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")[:, None]
+    for shape in ((2, 9, 3, 64), (9, 3, 64)):                       # padded and packed
+        q, g = _randn(*shape, seed=31).requires_grad_(), _randn(*shape, seed=32)
+        a, none = rot(q, None, pos)
+        assert none is None
+        got, = torch.autograd.grad(a, [q], [g])
+        q64 = q.detach().double().reshape(-1, 9, 3, 64).requires_grad_()
+        ref, = torch.autograd.grad(_rope64(q64, pos, rot.plan), [q64], [g.double().view_as(q64)])
+        assert _rel(got.view_as(ref), ref) <= 2e-6
+
+
 # --- a block of them --------------------------------------------------------------------
 
 def _block(bl, causal, checkpoint, d=128, H=4, Hk=2, seed=15):
