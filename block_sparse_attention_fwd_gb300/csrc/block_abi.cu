@@ -36,6 +36,21 @@ size_t part_bytes(const bl::Shape& sh) {
   return 2 * (size_t)sh.B * sh.n * sh.H * sh.d * sizeof(float);
 }
 
+// Whether some head of k lies on elements of one of q's, where both have the
+// same strides: `gap` elements between their first ones, t[i] in [lo[i], hi[i]]
+// the distance of a head of k and one of q along dim i, dims from the largest
+// stride to the smallest.  Exact where each stride spans the dims behind it.
+bool heads_meet(int64_t gap, const int64_t* stride, const int64_t* lo, const int64_t* hi, int dims,
+                int64_t d) {
+  if (dims == 0) return gap > -d && gap < d;
+  const int64_t near = stride[0] ? -(gap / stride[0]) : 0;
+  for (int64_t s = near - 1; s <= near + 1; ++s) {
+    const int64_t t = s < lo[0] ? lo[0] : s > hi[0] ? hi[0] : s;
+    if (heads_meet(gap + t * stride[0], stride + 1, lo + 1, hi + 1, dims - 1, d)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +143,7 @@ bl_status bl_rms_norm_bwd(int64_t rows, int64_t cols, int dtype, const void* g_y
 bl_status bl_rope(const bl_rope_args* r, void* stream) {
   if (!r || r->B < 0 || r->n < 0 || r->H < 1 || r->Hk < 0 || r->d < 2) return BL_ERR_INVALID_ARG;
   if (r->H > 65535 || r->Hk > 65535 || r->d > 65536) return BL_ERR_INVALID_ARG;
+  if (((int64_t)r->H + r->Hk) * r->d > INT32_MAX) return BL_ERR_INVALID_ARG;
   if (r->pairs < 1 || r->pairs > r->d / 2 || r->axes < 1 || r->axes > 4) return BL_ERR_INVALID_ARG;
   if (!dtype_ok(r->dtype)) return BL_ERR_INVALID_ARG;
   if ((r->interleaved & ~1) || (r->inverse & ~1)) return BL_ERR_INVALID_ARG;
@@ -166,6 +182,30 @@ bl_status bl_rope(const bl_rope_args* r, void* stream) {
     return BL_ERR_INVALID_ARG;
   if ((r->B > 1 && a.qos[0] < r->d) || (r->Hk && r->B > 1 && a.kos[0] < r->d))
     return BL_ERR_INVALID_ARG;
+  // nor those of k on those of q, where both are views of one tensor
+  if (r->Hk) {
+    if (r->q_out == r->k_out) return BL_ERR_INVALID_ARG;
+    if (a.qos[0] == a.kos[0] && a.qos[1] == a.kos[1] && a.qos[2] == a.kos[2]) {
+      const int64_t span[3] = {r->B - 1, r->n - 1, 0};
+      int order[3] = {0, 1, 2};
+      for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+          if (a.qos[order[j]] < a.qos[order[j + 1]]) {
+            const int s = order[j];
+            order[j] = order[j + 1];
+            order[j + 1] = s;
+          }
+      int64_t stride[3], lo[3], hi[3];
+      for (int i = 0; i < 3; ++i) {
+        stride[i] = a.qos[order[i]];
+        lo[i] = order[i] == 2 ? -(int64_t)(r->H - 1) : -span[order[i]];
+        hi[i] = order[i] == 2 ? r->Hk - 1 : span[order[i]];
+      }
+      const int64_t gap = (int64_t)((intptr_t)r->k_out - (intptr_t)r->q_out) /
+                          (int64_t)size_of(r->dtype);
+      if (heads_meet(gap, stride, lo, hi, 3, r->d)) return BL_ERR_INVALID_ARG;
+    }
+  }
   if (r->positions_batch_stride != 0 &&
       r->positions_batch_stride != (int64_t)r->n * r->axes)
     return BL_ERR_INVALID_ARG;

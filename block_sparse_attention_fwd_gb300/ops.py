@@ -389,7 +389,8 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
     ``positions`` is int32 [B, n, axes], or [n, axes] for all batches alike;
     packed tensors [total, heads, d] take [total, axes].  ``inverse`` turns
     back: applied to the outputs' gradients it gives the inputs'.  Returns
-    (q, k) as new contiguous tensors, or with ``inplace`` the given ones."""
+    (q, k) as new contiguous tensors, or with ``inplace`` the given ones, which
+    must not share elements."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype not in _lib.DTYPES:
         raise TypeError("q must be a bf16, fp16 or fp32 CUDA tensor")
     if q.dim() == 3:

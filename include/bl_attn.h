@@ -381,12 +381,13 @@ bl_status bl_rms_norm_bwd(int64_t rows, int64_t cols, int dtype, const void* g_y
  * those of the inputs.
  *   q, q_out  [B, n, H, d] of dtype, k, k_out [B, n, Hk, d]; Hk = 0: no k.
  *             Element strides {batch, token, head}, the dim stride is 1.
- *             q_out may be q itself (with the same strides), likewise k_out.
+ *             q_out may be q itself (with the same strides), likewise k_out;
+ *             q_out and k_out must not share elements.
  *   positions [B, n, axes] int32, contiguous: positions_batch_stride is n * axes,
  *             or 0 for [n, axes] that all batches share.
  *   freqs     [pairs] uint64 on the device: round(f_p / (2 pi) * 2^64) modulo
  *             2^64, f_p in radians a position.
- * 1 <= pairs <= d / 2.  Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
+ * 1 <= pairs <= d / 2, (H + Hk) * d < 2^31.  Errors: BL_ERR_INVALID_ARG, BL_ERR_CUDA. */
 typedef struct {
   int B, n, H, Hk, d, pairs, axes;
   int sections[4];

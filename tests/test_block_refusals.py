@@ -95,7 +95,7 @@ def test_norm_backward_refuses(lib, kw, code):
 def _rope_args(**kw):
     a = _lib.RopeArgs()
     v = dict(B=2, n=5, H=4, Hk=2, d=64, pairs=32, axes=1, sections=(32,), interleaved=0, inverse=0,
-             dtype=0, q=OK, k=OK, q_out=2 * OK, k_out=2 * OK, q_strides=(1280, 256, 64),
+             dtype=0, q=OK, k=OK, q_out=2 * OK, k_out=3 * OK, q_strides=(1280, 256, 64),
              k_strides=(640, 128, 64), q_out_strides=(1280, 256, 64), k_out_strides=(640, 128, 64),
              positions=OK, positions_batch_stride=5, freqs=OK)
     v.update(kw)
@@ -118,6 +118,41 @@ def _rope_args(**kw):
     dict(q_out=OK, q_strides=(2560, 512, 64)), dict(positions_batch_stride=4)])
 def test_rope_refuses(lib, kw):
     assert lib.bl_rope(ctypes.byref(_rope_args(**kw)), None) == 1
+
+
+# one tensor [2, 5, 6 heads, 64] behind both, token stride 384, batch stride 1920
+_ONE = (1920, 384, 64)
+
+
+@pytest.mark.parametrize("at", [0, 64, 3 * 64, -64, 32, 384, -384 + 64, 1920, 1920 - 384 + 128])
+def test_rope_refuses_outputs_that_share_elements(lib, at):
+    """k begins `at` elements behind q: some head of k is (part of) one of q's."""
+    k = OK + 2 * at
+    args = _rope_args(q=OK, q_out=OK, k=k, k_out=k, q_strides=_ONE, q_out_strides=_ONE,
+                      k_strides=_ONE, k_out_strides=_ONE)
+    assert lib.bl_rope(ctypes.byref(args), None) == 1
+
+
+@pytest.mark.parametrize("strides", [(64, 384, 64), (0, 384, 64), (10 ** 9, 384, 64),
+                                     (7, 64, 320)])
+def test_rope_refuses_shared_elements_of_one_batch(lib, strides):
+    """One batch, whose stride says nothing; the last: heads before tokens."""
+    args = _rope_args(B=1, q=OK, q_out=OK, k=OK + 2 * strides[2], k_out=OK + 2 * strides[2],
+                      q_strides=strides, q_out_strides=strides, k_strides=strides,
+                      k_out_strides=strides)
+    assert lib.bl_rope(ctypes.byref(args), None) == 1
+
+
+def test_rope_refuses_one_tensor_in_two_forms(lib):
+    assert lib.bl_rope(ctypes.byref(_rope_args(q_out=2 * OK, k_out=2 * OK)), None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(H=65535, Hk=0, d=65536), dict(H=30000, Hk=2768, d=65536)])
+def test_rope_refuses_tokens_past_32_bits(lib, kw):
+    H, Hk, d = kw["H"], kw["Hk"], kw["d"]
+    q, k = (H * d, H * d, d), (max(Hk, 1) * d, max(Hk, 1) * d, d)
+    args = _rope_args(B=1, n=1, q_strides=q, q_out_strides=q, k_strides=k, k_out_strides=k, **kw)
+    assert lib.bl_rope(ctypes.byref(args), None) == 1
 
 
 def test_rope_arguments_are_laid_out_as_the_struct():

@@ -186,6 +186,8 @@ def test_rope_refusals(bl):
         (ValueError, lambda: bl.rope(q.transpose(2, 3).contiguous().transpose(2, 3), None, pos, plan)),
         (ValueError, lambda: bl.rope(q, None, pos, bl.RopePlan(128, (64,)))),
         (bl.BLError, lambda: bl.rope(q[:, :, :1].expand(2, 4, 2, 64), None, pos, plan, inplace=True)),
+        (bl.BLError, lambda: bl.rope(q, q, pos, plan, inplace=True)),
+        (bl.BLError, lambda: bl.rope(q, q[:, :, 1:], pos, plan, inplace=True)),
     ]
     for error, call in bad:
         with pytest.raises(error):
