@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(512, 1) bwd_tc_kernel(
         uint8_t* wstage = sm + C::OFF_DS + half * C::CHUNK + q4 * 32 * 128;   // 1024-aligned
         uint8_t* srow = wstage + lane * 128;
         const int row0 = ie.j * 128 + q4 * 32;
-if constexpr (PART) {
+        if constexpr (PART) {
 #pragma unroll
           for (int c32 = 0; c32 < D / 32; ++c32) {    // 32 fp32 columns = one 128-byte row
             if (c32 > 0) {
