@@ -28,9 +28,10 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Bytes of the scratch that lets the attention backward's work items be single
 // query heads, or 0 where it does not pay: without groups there is nothing to
-// split, and with an item for every SM the extra passes over fp32 tiles cost
-// more than the idle SMs do.
+// split, few tokens have their own kernel, and with an item for every SM the
+// extra passes over fp32 tiles cost more than the idle SMs do.
 size_t part_bytes(const bl::Shape& sh) {
+  if (sh.n <= bl::kFewTokens) return 0;
   if (sh.H == sh.Hk || sh.block_q != 128 || sh.block_k != 128) return 0;
   if ((int64_t)sh.T_c * sh.Hk * sh.B >= 152) return 0;
   return 2 * (size_t)sh.B * sh.n * sh.H * sh.d * sizeof(float);
@@ -256,6 +257,33 @@ bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_ac
   uint8_t* q = ws + up256(bl_bwd_workspace_bytes(shape));
   uint8_t* k = q + up256(tokens * sh.H);
   uint8_t* v = k + up256(tokens * sh.Hk);
+  int32_t* ws_status = reinterpret_cast<int32_t*>(ws + bl::ws_status_off(sh));
+  if (sh.n <= bl::kFewTokens) {
+    bl::BwdFew f{};
+    f.B = sh.B; f.n = sh.n; f.H = sh.H; f.Hk = sh.Hk;
+    f.causal = sh.causal; f.window = sh.window;
+    f.scale = scale;
+    f.q = static_cast<const uint8_t*>(q8->codes); f.q_scales = q8->scales;
+    f.k = static_cast<const uint8_t*>(k8->codes); f.k_scales = k8->scales;
+    f.v = static_cast<const uint8_t*>(v8->codes); f.v_scales = v8->scales;
+    f.o = static_cast<const __nv_bfloat16*>(o);
+    f.g_o = static_cast<const __nv_bfloat16*>(g_o);
+    if (o8) {
+      f.o_codes = static_cast<const uint8_t*>(o8->codes);
+      f.o_scales = o8->scales;
+    }
+    f.lse = lse;
+    if (lists) {
+      f.q_idx = lists->q_idx;
+      f.q_cnt = lists->q_cnt;
+    }
+    f.g_q = static_cast<__nv_bfloat16*>(g_q);
+    f.g_k = static_cast<__nv_bfloat16*>(g_k);
+    f.g_v = static_cast<__nv_bfloat16*>(g_v);
+    f.status = ws_status;
+    const cudaError_t e = bl::launch_bwd_few(sh.d, q8->format, f, (cudaStream_t)stream);
+    if (e != cudaErrorNotSupported) return cuda_status(e);
+  }
   float* part = part_bytes(sh) ? reinterpret_cast<float*>(v + up256(tokens * sh.Hk)) : nullptr;
   bl::Expand e{};
   uint8_t* out[3] = {q, k, v};
@@ -270,7 +298,6 @@ bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_ac
   float* ws_D = reinterpret_cast<float*>(ws);
   float* ws_dq = reinterpret_cast<float*>(ws + bl::ws_D_bytes(sh));
   int32_t* ws_sub = reinterpret_cast<int32_t*>(ws + bl::ws_D_bytes(sh) + bl::ws_dq_bytes(sh));
-  int32_t* ws_status = reinterpret_cast<int32_t*>(ws + bl::ws_status_off(sh));
   return cuda_status(bl::launch_bwd_act8(
       sh, q, k, v, o, o8 ? static_cast<const uint8_t*>(o8->codes) : nullptr,
       o8 ? o8->scales : nullptr, q8->format, g_o, lse, scale, lists ? lists->q_idx : nullptr,

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -134,6 +135,23 @@ cudaError_t launch_bwd_act8(const Shape& sh, const void* q, const void* k, const
                             const int32_t* q_idx, const int32_t* q_cnt, void* g_q, void* g_k,
                             void* g_v, float* ws_D, float* ws_dq, int32_t* ws_sub,
                             int32_t* ws_status, cudaStream_t st, float* part = nullptr);
+
+// The same for up to kFewTokens tokens (bwd_few.cu), from the codes; o either in
+// bf16 or (o null) as codes; q_idx/q_cnt [B,H] of one tile, or null;
+// status two int32.
+constexpr int kFewTokens = 64;
+struct BwdFew {
+  int B, n, H, Hk, causal, window;
+  float scale;
+  const uint8_t *q, *k, *v, *o_codes;
+  const float *q_scales, *k_scales, *v_scales, *o_scales;
+  const __nv_bfloat16 *o, *g_o;
+  const float* lse;
+  const int32_t *q_idx, *q_cnt;
+  __nv_bfloat16 *g_q, *g_k, *g_v;
+  int32_t* status;
+};
+cudaError_t launch_bwd_few(int d, int fmt, const BwdFew& a, cudaStream_t st);
 
 // Rotary positions (rope.cu).  Strides {batch, token, head} in elements.
 struct Rope {

@@ -408,6 +408,8 @@ bl_status bl_rope(const bl_rope_args* args, void* stream);
  * q8->scales [B,n,H]) and stand for their values rounded to bf16; o comes
  * either in bf16 (o) or as codes (o8), exactly one of both.  All codes have
  * the same format.  Contiguous tensors only (zero strides in the shape).
+ * Up to 64 tokens P and dS enter their products within 2^-16 of their values,
+ * beyond as bf16, as in bl_attn_bwd.
  * The workspace begins with bl_attn_bwd's, so bl_bwd_check_status reads it. */
 size_t bl_attn_bwd_act8_workspace_bytes(const bl_shape* shape);
 bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_act8* k8,

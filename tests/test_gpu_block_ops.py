@@ -584,6 +584,101 @@ def test_attention_backward_from_8_bits_of_kv_heads(bl, B, n, H, Hk, bq):
     assert U.rel_l2(U.cpu(got[0]), U.cpu(ref[0])) <= 1e-3
 
 
+FEW = [
+    # B, n, H, Hk, d, causal, window, tile, fmt, o in 8 bits, heads whose tile a mask drops (None: no lists)
+    (1, 1, 1, 1, 64, False, 0, 128, "int8", True, None),
+    (3, 1, 6, 2, 128, True, 0, 128, "e4m3", False, None),
+    (2, 2, 4, 1, 64, True, 1, 128, "int8", False, None),
+    (1, 15, 3, 3, 128, False, 0, 128, "int8", True, None),
+    (2, 16, 4, 2, 128, True, 0, 128, "e4m3", True, None),
+    (1, 17, 5, 1, 64, True, 0, 128, "int8", False, None),
+    (2, 33, 6, 2, 128, True, 16, 128, "int8", True, None),
+    (1, 48, 4, 4, 64, True, 17, 128, "e4m3", False, None),
+    (2, 63, 6, 3, 64, False, 0, 64, "int8", True, (0, 3, 7)),
+    (1, 64, 8, 2, 128, True, 0, 128, "int8", False, (0, 1, 2, 3)),
+    (1, 64, 2, 1, 128, True, 40, 128, "e4m3", True, (1,)),
+    (2, 64, 3, 1, 128, False, 0, 128, "int8", False, (0, 1, 2, 3, 4, 5)),
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: f"n{c[1]}d{c[4]}{c[8]}")
+def test_attention_backward_from_8_bits_of_few_tokens(bl, case):
+    """Up to 64 tokens, element by element: half a step of bf16 and what fp32 can lose.
+
+    A matrix instruction adds 16 exact products to an accumulator; with every of the 17
+    terms cut at 2^-23 of the largest it is off by 17 * 2^-23 of the sum of their sizes,
+    so d / 16 of them in a row by m * 2^-24, m = 2.125 d.  The sums over n G pairs take
+    two parts, 4.25 (n G + 15) * 2^-24, and three additions of warps' sums; the parts
+    leave 2^-16 of P and of dS.  P = 2^x with x = log2(e) (s S - LSE) is off, relative to
+    it, by the error of s S and by 2^-21 of |s S| + |LSE| + 4 (three roundings of x, the
+    constants', exp2's two units)."""
+    B, n, H, Hk, d, causal, window, tile, fmt, o_in8, dropped = case
+    scale, G, u = d ** -0.5, H // Hk, 2.0 ** -24
+    q, g_o = (_randn(B, n, H, d, dtype=torch.bfloat16, seed=s) for s in (41, 42))
+    k, v = (_randn(B, n, Hk, d, dtype=torch.bfloat16, seed=s) for s in (43, 44))
+    i, j = np.arange(n)[:, None], np.arange(n)[None]
+    attends = (j <= i if causal else np.ones((n, n), bool)) & (i - j < (window or n))
+    heads = lambda t: np.repeat(_f64(t).transpose(0, 2, 1, 3), G if t.shape[2] != H else 1, 1)  # noqa: E731
+    S = np.where(attends, scale * heads(q) @ heads(k).swapaxes(2, 3), -np.inf)
+    top = S.max(-1, keepdims=True)
+    e = np.exp(S - top)
+    o = (e / e.sum(-1, keepdims=True)) @ heads(v)
+    lse = torch.from_numpy((top + np.log(e.sum(-1, keepdims=True)))[..., 0]).float().cuda()
+    o = torch.from_numpy(o.transpose(0, 2, 1, 3)).to(torch.bfloat16).contiguous().cuda()
+    q8, k8, v8, o8 = (bl.act_save(t, fmt) for t in (q, k, v, o))
+    shape = bl.make_shape(B, n, H, Hk, d, tile, tile, int(causal), window)
+    lists, on = None, np.ones((B, H))
+    if dropped is not None:
+        on.reshape(-1)[list(dropped)] = 0
+        lists = bl.alloc_lists(shape, q.device)
+        for name, t in lists.items():
+            t.fill_(0)
+        lists["q_cnt"].copy_(torch.from_numpy(on).to(torch.int32)[..., None])
+        lists["q_idx"].masked_fill_(lists["q_cnt"][..., None] == 0, -7)        # never read
+    ws = torch.full((bl.attn_bwd_act8_workspace_bytes(shape),), 255, dtype=torch.uint8, device="cuda")
+    call = lambda: bl.attn_bwd_act8(shape, q8, k8, v8, o8 if o_in8 else o, g_o, lse, scale, lists,  # noqa: E731
+                                    workspace=ws)
+    got = call()
+    assert bl.bwd_check_status(shape, ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, call()))
+
+    Q, K, V = (heads(bl.act_load(t)) for t in (q8, k8, v8))
+    O = heads(o8.codes.float().double() * o8.scales.double()) if o_in8 else heads(o)
+    dO, L = heads(g_o), _f64(lse)[..., None]
+    use = attends * on[:, :, None, None]
+    T = lambda x: x.swapaxes(2, 3)  # noqa: E731
+    s = scale * Q @ T(K)
+    P = np.where(use > 0, np.exp(np.where(use > 0, s - L, 0)), 0)
+    D = (dO * O).sum(-1, keepdims=True)
+    dP = dO @ T(V)
+    dS = P * (dP - D)
+    m = 2.125 * d
+    eP = P * (scale * m * u * (abs(Q) @ T(abs(K))) + 2.0 ** -21 * (abs(s) + abs(L) + 4) + 2.0 ** -16)
+    eD = (d + 4) * u * (abs(dO) * abs(O)).sum(-1, keepdims=True)
+    edS = eP * abs(dP - D) + (P + eP) * (m * u * (abs(dO) @ T(abs(V))) + eD) + 2.0 ** -16 * abs(dS)
+    terms = 4.25 * (n * G + 15) + 3
+    sum_group = lambda x: x.reshape(B, Hk, G, n, d).sum(2)  # noqa: E731
+    want = [(scale * dS @ K, scale * (edS + terms * u * abs(dS)) @ abs(K)),
+            (sum_group(scale * T(dS) @ Q), sum_group(scale * T(edS + terms * u * abs(dS)) @ abs(Q))),
+            (sum_group(T(P) @ dO), sum_group(T(eP + terms * u * P) @ abs(dO)))]
+    for g, (ref, noise) in zip(got, want):
+        err = abs(_f64(g).transpose(0, 2, 1, 3) - ref)
+        assert np.all(err <= 2.0 ** -8 * (abs(ref) + noise) + noise + 2.0 ** -130)
+
+
+def test_attention_backward_from_8_bits_of_few_tokens_reports_bad_lists(bl):
+    shape, (q, k, v, o), g_o, lse, (q8, k8, v8, _) = _attn_case(bl, 1, 20, 3, 1, 64, False, "int8")
+    lists = bl.alloc_lists(shape, q.device)
+    for t in lists.values():
+        t.fill_(0)
+    lists["q_cnt"].copy_(torch.tensor([[[1], [2], [1]]], dtype=torch.int32))
+    lists["q_idx"].copy_(torch.tensor([0, 0, 5], dtype=torch.int32).view(1, 3, 1, 1))
+    ws = torch.empty(bl.attn_bwd_act8_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    got = bl.attn_bwd_act8(shape, q8, k8, v8, o, g_o, lse, 0.125, lists, workspace=ws)
+    assert bl.bwd_check_status(shape, ws) != 0
+    assert got[0][:, :, 0].any() and not got[0][:, :, 1:].any()       # only head 0's list stands
+
+
 def test_attention_backward_from_8_bits_refusals(bl):
     shape, (q, k, v, o), g_o, lse, (q8, k8, v8, o8) = _attn_case(bl, 1, 130, 2, 1, 64, False, "int8")
     s = 0.125
