@@ -23,8 +23,8 @@
 namespace bl {
 namespace norm {
 
-// A row is held by LPR lanes of a warp (8, 16 or 32, each with NV chunks: up to
-// 1024 columns) or by the whole block (LPR = 0).
+// A row is held by LPR lanes of a warp (8, 16 or 32, each with NV chunks) or by the
+// whole block (LPR = 0).
 template <int LPR>
 struct Rows {
   int here, mine, t, step;      // rows of the block, this thread's; its first chunk and their distance
@@ -42,6 +42,84 @@ struct Rows {
     }
   }
 };
+// The 8 elements of a row that a thread has in its unit k.  Chunks: 8 neighbours.
+// SPREAD: R.step apart, so that the lanes of an access have neighbouring elements:
+// for rows that start anywhere, where a chunk would take 8 accesses that each
+// touch a sector a lane.  fp32, 32760 x 2561: forward 45 -> 64% of the copy rate, 83%
+// with a residual; straight from global memory, as 4-byte copies to the ring wait
+// on their own number (54 and 52%).  Backward 63% on the ring, 33% without.
+template <bool SPREAD, int LPR>
+__device__ __forceinline__ int col_of(const Rows<LPR>& R, int k, int i) {
+  return SPREAD ? (k * 8 + i) * R.step + R.t : (R.t + k * R.step) * 8 + i;
+}
+template <typename T, bool VEC, bool SPREAD, int LPR>
+__device__ __forceinline__ Chunk<T> load_unit(const T* __restrict__ row, const Rows<LPR>& R, int k,
+                                              int cols) {
+  if constexpr (!SPREAD) {
+    const int col = col_of<false>(R, k, 0);
+    return load8<T, VEC>(row + col, cols - col);
+  } else {
+    Chunk<T> c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = col_of<true>(R, k, i);
+      c.e[i] = col < cols ? row[col] : from_f32<T>(0.f);
+    }
+    return c;
+  }
+}
+template <typename T, bool VEC, bool SPREAD, int LPR>
+__device__ __forceinline__ void store_unit(T* __restrict__ row, const Rows<LPR>& R, int k, int cols,
+                                           const float (&f)[8]) {
+  if constexpr (!SPREAD) {
+    const int col = col_of<false>(R, k, 0);
+    store8<T, VEC>(row + col, f, cols - col);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = col_of<true>(R, k, i);
+      if (col < cols) row[col] = from_f32<T>(f[i]);
+    }
+  }
+}
+template <typename T, bool VEC, bool SPREAD, int LPR>
+__device__ __forceinline__ void weight_unit(const void* w, bool f32, const Rows<LPR>& R, int k,
+                                            int cols, float (&f)[8]) {
+  if constexpr (!SPREAD) {
+    const int col = col_of<false>(R, k, 0);
+    load_weight8<T, VEC>(w, f32, col, cols - col, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = col_of<true>(R, k, i);
+      f[i] = !w            ? 1.f
+             : col >= cols ? 0.f
+             : f32         ? static_cast<const float*>(w)[col]
+                           : to_f32(static_cast<const T*>(w)[col]);
+    }
+  }
+}
+
+// The same through a plane of shared memory, fp32: element i of unit k lies
+// 4 bytes a thread apart from its neighbours', and those behind the row are zero.
+template <int LPR>
+__device__ __forceinline__ void copy_spread(uint8_t* plane, const float* row, const Rows<LPR>& R,
+                                            int k, int nt, int cols) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int col = col_of<true>(R, k, i);
+    copy_async<4>(plane + ((k * 8 + i) * nt + (int)threadIdx.x) * 4, row + (col < cols ? col : 0),
+                  col < cols ? 4 : 0);
+  }
+}
+__device__ __forceinline__ Chunk<float> chunk_spread(const uint8_t* plane, int k, int nt) {
+  Chunk<float> c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    c.e[i] = *reinterpret_cast<const float*>(plane + ((k * 8 + i) * nt + (int)threadIdx.x) * 4);
+  return c;
+}
+
 // Whether the lane in front (behind) of this one's holds the chunk in front
 // (behind): not across the ends of a warp or, with LPR, of a row's lanes.
 template <int LPR>
@@ -103,8 +181,9 @@ inline unsigned grid(int64_t rows, int here, int most) {
   return (unsigned)(blocks < most ? blocks : most);
 }
 
-// The ring kernels for rows of 16-bit types that start anywhere (norm_fwd_odd.cu,
-// norm_bwd_odd.cu); cudaErrorNotSupported where a row is too wide for them.
+// The ring kernels for rows that start anywhere (norm_fwd_odd.cu: 16-bit types;
+// norm_bwd_odd.cu: those, and fp32 that a block holds, without 8 bits);
+// cudaErrorNotSupported for others and where a row is too wide.
 cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st);
 cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 

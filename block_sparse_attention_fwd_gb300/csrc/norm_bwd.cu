@@ -11,6 +11,7 @@ template <typename T, int LPR, int NV, bool VEC, bool IN8>
 __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
   __shared__ float buf[2][32];
   __shared__ float part[LPR ? 256 * 8 * NV : 1];
+  constexpr bool SPREAD = !VEC && !IN8;
   const Rows<LPR> R;
   const int cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
@@ -20,12 +21,14 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
   int slot = 0;
-  auto load_unit = [&](int64_t row, int col, int valid, float rstd, float (&u)[8]) {
+  auto unit_of = [&](int64_t row, int k, int here, float rstd, float (&u)[8]) {
     if constexpr (!IN8) {
-      const Chunk<T> h = load8<T, VEC>(static_cast<const T*>(a.h) + row * cols + col, valid);
+      const Chunk<T> h =
+          load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.h) + row * cols, R, k, here);
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = to_f32(h.e[i]) * rstd;
     } else {
+      const int col = (R.t + k * R.step) * 8, valid = here - col;
       const Codes c = load_codes<VEC>(a.codes + row * cols + col, valid);
       const float s = valid > 0 ? a.scales[row * a.groups + (col >> a.shift)] : 0.f;
       decode8(a.fmt, c, u);
@@ -37,17 +40,16 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
        row0 += (int64_t)gridDim.x * R.here) {
     const int64_t row = row0 + R.mine;
     const bool in = row < a.rows;
+    const int here = in ? cols : 0;
     const float rstd = in ? a.rstd[row] : 0.f;
     Chunk<T> gy[NV];
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in ? cols - col : 0;
-      gy[k] = load8<T, VEC>(static_cast<const T*>(a.g_y) + row * cols + col, valid);
+      gy[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.g_y) + row * cols, R, k, here);
       float w[8], u[8];
-      load_unit(row, col, valid, rstd, u);
-      load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
+      unit_of(row, k, here, rstd, u);
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float g = to_f32(gy[k].e[i]);
@@ -58,22 +60,21 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
     const float c = row_sum<LPR>(dot, buf, slot) * inv_cols;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in ? cols - col : 0;
       float w[8], u[8], g[8];
-      load_unit(row, col, valid, rstd, u);             // from the caches
-      load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
+      unit_of(row, k, here, rstd, u);                  // from the caches
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = rstd * (to_f32(gy[k].e[i]) * w[i] - u[i] * c);
       if (a.g_h) {
-        const Chunk<T> e = load8<T, VEC>(static_cast<const T*>(a.g_h) + row * cols + col, valid);
+        const Chunk<T> e =
+            load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.g_h) + row * cols, R, k, here);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] += to_f32(e.e[i]);
       }
-      store8<T, VEC>(static_cast<T*>(a.g_x) + row * cols + col, g, valid);
+      store_unit<T, VEC, SPREAD>(static_cast<T*>(a.g_x) + row * cols, R, k, here, g);
     }
   }
-  if (a.partial) write_partial<LPR, NV, VEC>(a, R, acc, part);
+  if (a.partial) write_partial<LPR, NV, VEC, SPREAD>(a, R, acc, part);
 }
 
 // g_w[col] = sum of the blocks' partial sums, 32 columns a block, 32 slices of

@@ -11,7 +11,7 @@ namespace {
 
 // The end of a backward block: its threads' sums of g_w over the block's rows
 // go to the block's row of a.partial.
-template <int LPR, int NV, bool VEC>
+template <int LPR, int NV, bool VEC, bool SPREAD = false>
 __device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>& R,
                                               const float (&acc)[NV][8], float* part) {
   const int cols = (int)a.cols;
@@ -23,7 +23,7 @@ __device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>&
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        part[R.mine * (LPR * NV * 8) + (R.t + k * LPR) * 8 + i] = acc[k][i];
+        part[R.mine * (LPR * NV * 8) + col_of<SPREAD>(R, k, i)] = acc[k][i];
     __syncthreads();
     for (int col = threadIdx.x; col < cols; col += blockDim.x) {
       float s = 0.f;
@@ -32,15 +32,19 @@ __device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>&
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      store8<float, VEC>(out + col, acc[k], cols - col);
-    }
+    for (int k = 0; k < NV; ++k) store_unit<float, VEC, SPREAD>(out, R, k, cols, acc[k]);
   }
 }
 
 // Registers a thread of the backward may take (the launch counts on them).
-constexpr int bwd_regs(int lpr, int nv) { return nv >= 3 ? 128 : nv == 2 ? 96 : lpr ? 64 : 72; }
+// SPREAD, with an address an element, takes more.
+constexpr int bwd_regs(int lpr, int nv, bool spread = false) {
+  return nv >= 3  ? 128
+         : spread ? (nv == 1 ? 104 : 128)
+         : nv == 2 ? 96
+         : lpr     ? 64
+                   : 72;
+}
 
 // The backward of rows whose chunks are whole and aligned: one pass over the
 // rows.  A block takes rows gridDim.x apart and keeps its sums of g_w in
@@ -53,13 +57,15 @@ constexpr int bwd_regs(int lpr, int nv) { return nv >= 3 ? 128 : nv == 2 ? 96 : 
 // registers took 354 and 719 us; with the ring but scalar arithmetic on u = h
 // rstd, 245 instructions a chunk, 240 and 255 us.
 // ODD: rows of a 16-bit type that start anywhere, as in the forward (2561 columns:
-// 24% of the copy rate element by element, 51% so).
+// 24% of the copy rate element by element, 51% so), or of fp32, SPREAD.
 template <typename T, int LPR, int NV, int FMT, int S, bool ODD>
-__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV))
+__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV, ODD && sizeof(T) == 4))
     norm_bwd_ring_kernel(NormBwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   constexpr int HB = FMT ? 12 : CB;                  // of h's: codes and a scale
   constexpr bool KEEP_W = NV <= 2;                   // the weight stays in registers
+  constexpr bool SHIFT = ODD && CB == 16, SPREAD = ODD && CB != 16;
+  static_assert(!SPREAD || FMT == 0);
   __shared__ float buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Rows<LPR> R;
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
   const int plane = NV * nt * CB, stage_bytes = 2 * plane + NV * nt * HB;
   bool has[NV];                                      // whether the thread has a chunk k
 #pragma unroll
-  for (int k = 0; k < NV; ++k) has[k] = (R.t + k * R.step) * 8 < cols;
+  for (int k = 0; k < NV; ++k) has[k] = col_of<SPREAD>(R, k, 0) < cols;
 
   // `place`: the thread's first 16 bytes of a stage; its codes and scales lie
   // 8 and 12 bytes a thread less far
@@ -92,7 +98,12 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         uint8_t* p = place + k * nt * CB;
-        if constexpr (ODD) {
+        if constexpr (SPREAD) {
+          uint8_t* all = place - threadIdx.x * 16;
+          copy_spread(all, gy, R, k, nt, cols);
+          if (a.g_h) copy_spread(all + plane, gh, R, k, nt, cols);
+          copy_spread(all + 2 * plane, h, R, k, nt, cols);
+        } else if constexpr (SHIFT) {
           const int c = R.t + k * R.step;
           if (c * 8 >= cols + 8) continue;
           copy_odd(p, gy, c, cols);
@@ -121,10 +132,13 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
     }
     copy_commit();
   };
-  // a chunk out of place p, of a row of this tensor
-  auto chunk = [&](const uint8_t* p, const void* tensor, int64_t row) {
+  // chunk k out of the thread's place in a plane, of a row of this tensor
+  auto chunk = [&](const uint8_t* place, int k, const void* tensor, int64_t row) {
+    const uint8_t* p = place + k * nt * CB;
     Chunk<T> c;
-    if constexpr (ODD) {
+    if constexpr (SPREAD) {
+      c = chunk_spread(place - threadIdx.x * 16, k, nt);
+    } else if constexpr (SHIFT) {
       c = chunk_odd<T, LPR>(p, R.t, nt, static_cast<const T*>(tensor) + row * cols);
     } else {
 #pragma unroll
@@ -135,11 +149,11 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
   };
   auto load_h = [&](const uint8_t* place, int k, int64_t row, uint64_t (&h)[4]) {
     if constexpr (FMT == 0) {
-      unpack2(chunk(place + 2 * plane + k * nt * CB, a.h, row), h);
+      unpack2(chunk(place + 2 * plane, k, a.h, row), h);
     } else {
       const float s = *reinterpret_cast<const float*>(scale_at(place, k));
       Codes codes;
-      if constexpr (ODD) {
+      if constexpr (SHIFT) {
         codes = codes_odd<LPR>(codes_at(place, k), R.t, nt, a.codes + row * cols);
       } else {
         const uint2 raw = *reinterpret_cast<const uint2*>(codes_at(place, k));
@@ -154,8 +168,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
   };
   auto load_w = [&](int k, uint64_t (&w)[4]) {
     float f[8];
-    const int col = (R.t + k * R.step) * 8;
-    load_weight8<T, !ODD>(a.w, a.w_f32, col, cols - col, f);
+    weight_unit<T, !ODD, SPREAD>(a.w, a.w_f32, R, k, cols, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f2_pack(f[2 * i], f[2 * i + 1]);
   };
@@ -176,14 +189,14 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
   for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
     const int64_t row = row0 + R.mine;
     const bool in = LPR == 0 || row < a.rows;
-    if constexpr (ODD) {
+    if constexpr (SHIFT) {
       copy_wait<S - 2>();
       if constexpr (LPR) __syncwarp(); else __syncthreads();
     }
     fetch(mine + fill * stage_bytes, row + (S - 1) * stride);
     // behind the fetch: in front of it the copies waited for this load (153 -> 171 us)
     const float rstd_next = row + stride < a.rows ? a.rstd[row + stride] : 0.f;
-    if constexpr (!ODD) copy_wait<S - 1>();
+    if constexpr (!SHIFT) copy_wait<S - 1>();
     const uint8_t* place = mine + now * stage_bytes;
     uint64_t wv[NV][4], h[NV][4], dot = 0;
     const uint64_t rr = f2_pack(rstd, rstd);
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
     for (int k = 0; k < NV; ++k) {
       if (!in || !has[k]) continue;
       uint64_t g[4];
-      unpack2(chunk(place + k * nt * CB, a.g_y, row), g);
+      unpack2(chunk(place, k, a.g_y, row), g);
       load_h(place, k, row, h[k]);
       if constexpr (!KEEP_W) load_w(k, w[0]);
 #pragma unroll
@@ -217,16 +230,22 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
         for (int i = 0; i < 4; ++i) g[i] = ffma2(h[k][i], cc, wv[k][i]);
         if (a.g_h) {
           uint64_t e[4];
-          unpack2(chunk(place + plane + k * nt * CB, a.g_h, row), e);
+          unpack2(chunk(place + plane, k, a.g_h, row), e);
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[i] = fadd2(g[i], e[i]);
         }
-        if constexpr (ODD)
+        if constexpr (SPREAD) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f2_unpack(g[i], f[2 * i], f[2 * i + 1]);
+          store_unit<T, false, true>(out, R, k, cols, f);
+        } else if constexpr (SHIFT) {
           pack_words<T>(g, words);
-        else
+        } else {
           store8(out + k * R.step * 8, g);
+        }
       }
-      if constexpr (ODD) {
+      if constexpr (SHIFT) {
         const int c = R.t + k * R.step;
         store_anywhere<4>(reinterpret_cast<uint8_t*>(out), c,
                           in && has[k] ? min(cols - c * 8, 8) : 0, cols, lane_in_front(R),
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f2_unpack(acc[k][i], sum[k][2 * i], sum[k][2 * i + 1]);
-    write_partial<LPR, NV, !ODD>(a, R, sum, reinterpret_cast<float*>(ring));
+    write_partial<LPR, NV, !ODD, SPREAD>(a, R, sum, reinterpret_cast<float*>(ring));
   }
 }
 
@@ -251,33 +270,37 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV)
 // *blocks: its blocks, which are the rows of partial sums.
 template <typename T, int FMT, bool ODD>
 cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
-  const Plan p = plan(a.cols, 512, 96, ODD);
+  const Plan p = plan(a.cols, 512, 96, ODD && sizeof(T) == 2);
   cudaError_t e = cudaErrorNotSupported;
   if (p.threads > 512) return e;
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
     constexpr int CB = (int)sizeof(Chunk<T>);
-    const size_t stage = (size_t)N * p.threads * (2 * CB + (FMT ? 12 : CB));
-    auto ring = [&](auto stages) {
-      constexpr int S = decltype(stages)::value;
-      constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S, ODD>;
-      size_t smem = S * stage;
-      if constexpr (L != 0) {                          // the block's sums of g_w go there too
-        if (smem < (size_t)256 * 8 * N * 4) smem = (size_t)256 * 8 * N * 4;
+    // fp32 that a warp holds: 4-byte copies cost more than the ring gains (129
+    // columns: 72% of the copy rate straight from global memory, 29% so)
+    if constexpr (!(ODD && CB != 16 && L != 0)) {
+      const size_t stage = (size_t)N * p.threads * (2 * CB + (FMT ? 12 : CB));
+      auto ring = [&](auto stages) {
+        constexpr int S = decltype(stages)::value;
+        constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S, ODD>;
+        size_t smem = S * stage;
+        if constexpr (L != 0) {                          // the block's sums of g_w go there too
+          if (smem < (size_t)256 * 8 * N * 4) smem = (size_t)256 * 8 * N * 4;
+        }
+        *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N, ODD && CB != 16), smem));
+        e = allow_smem<k>();
+        if (e != cudaSuccess) return;
+        k<<<*blocks, p.threads, smem, st>>>(a);
+        e = cudaGetLastError();
+      };
+      constexpr int MOST = N == 4 ? 2 : 3;               // stages
+      if (MOST * stage <= kMaxSmem) {
+        ring(Int<MOST>());
+        return;
       }
-      *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N), smem));
-      e = allow_smem<k>();
-      if (e != cudaSuccess) return;
-      k<<<*blocks, p.threads, smem, st>>>(a);
-      e = cudaGetLastError();
-    };
-    constexpr int MOST = N == 4 ? 2 : 3;               // stages
-    if (MOST * stage <= kMaxSmem) {
-      ring(Int<MOST>());
-      return;
+      if constexpr (L == 0 && N == 2)
+        if (2 * stage <= kMaxSmem) ring(Int<2>());
     }
-    if constexpr (L == 0 && N == 2)
-      if (2 * stage <= kMaxSmem) ring(Int<2>());
   });
   return e;
 }

@@ -1,4 +1,4 @@
-// The backward's ring kernel on rows of 16-bit types that start anywhere.
+// The backward's ring kernel on rows that start anywhere.
 #include "norm_bwd.cuh"
 
 namespace bl {
@@ -6,7 +6,7 @@ namespace bl {
 namespace norm {
 
 cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st) {
-  if (dtype > 1) return cudaErrorNotSupported;       // fp32
+  if (dtype == 2) return a.codes ? cudaErrorNotSupported : bwd_ring<float, 0, true>(a, blocks, st);
   auto launch = [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     return !a.codes            ? bwd_ring<T, 0, true>(a, blocks, st)

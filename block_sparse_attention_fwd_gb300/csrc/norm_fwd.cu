@@ -5,10 +5,12 @@ namespace bl {
 
 namespace {
 
-// Any rows, straight from global memory.  OUT8: with the 8-bit output.
+// Any rows, straight from global memory.  OUT8: with the 8-bit output, whose
+// groups are neighbours, so those rows keep to chunks.
 template <typename T, int LPR, int NV, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
   __shared__ float buf[2][32];
+  constexpr bool SPREAD = !VEC && !OUT8;
   const Rows<LPR> R;
   const int cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
@@ -18,26 +20,24 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
        row0 += (int64_t)gridDim.x * R.here) {
     const int64_t row = row0 + R.mine;
     const bool in = row < a.rows;
+    const int here = in ? cols : 0;
     float h[NV][8];
     float s0 = 0.f, s1 = 0.f;                          // as the ring kernel sums them
     Chunk<T> x[NV], r[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in ? cols - col : 0;
-      x[k] = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col, valid);
-      if (a.r) r[k] = load8<T, VEC>(static_cast<const T*>(a.r) + row * a.r_stride + col, valid);
+      x[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.x) + row * a.x_stride, R, k, here);
+      if (a.r)
+        r[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.r) + row * a.r_stride, R, k, here);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in ? cols - col : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x[k].e[i]);
       if (a.r) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r[k].e[i]);
-        if (a.h) store8<T, VEC>(static_cast<T*>(a.h) + row * cols + col, h[k], valid);
+        if (a.h) store_unit<T, VEC, SPREAD>(static_cast<T*>(a.h) + row * cols, R, k, here, h[k]);
       }
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
@@ -51,14 +51,14 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int col = (R.t + k * R.step) * 8;
-      const int valid = in ? cols - col : 0;
       float w[8];
-      load_weight8<T, VEC>(a.w, a.w_f32, col, cols - col, w);
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[i];
-      if (a.y) store8<T, VEC>(static_cast<T*>(a.y) + row * cols + col, h[k], valid);
+      if (a.y) store_unit<T, VEC, SPREAD>(static_cast<T*>(a.y) + row * cols, R, k, here, h[k]);
       if constexpr (OUT8) {
+        const int col = (R.t + k * R.step) * 8;
+        const int valid = in ? cols - col : 0;
         float m = amax8(h[k]);
         if (a.group) {
           m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
