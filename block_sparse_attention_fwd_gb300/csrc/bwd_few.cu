@@ -12,23 +12,24 @@
 // two bf16 parts each, P = hi + lo within 2^-16 of P.
 //
 // A block has 16 rows of one kind ("mine") and walks tiles of 16 rows of the
-// other: a key item (batch, kv head, 16 keys) goes over the group's heads and
-// their queries and forms dK and dV, a query item (batch, head, 16 queries) over
-// the keys and forms dQ.  S and dP are formed twice for it, but no sum crosses
-// blocks.  Both kinds are the same four products,
-//   S = A1 B1^T, dP = A2 B2^T, acc1 += dS B1, acc2 += P B2
-// with (A1, A2) = (K, V) and (B1, B2) = (Q, dO), or the other way round without
-// acc2.  A warp takes every fourth tile by itself (no barriers) on
+// other.  A key item (batch, kv head, 16 keys) goes over the group's heads and
+// their queries and forms dK or dV, a query item (batch, head, 16 queries) over
+// the keys and forms dQ.  S is formed three times for it and dP twice, but no sum
+// crosses blocks, and a thread has one result's sums (dK and dV together: 242
+// registers, 8 warps an SM).  All kinds are the same products,
+//   S = A1 B1^T, dP = A2 B2^T, and acc += dS B1 (dQ, dK) or acc += P B2 (dV),
+// with (A1, A2) = (K, V) and (B1, B2) = (Q, dO) or the other way round.  A warp takes every fourth tile by itself (no barriers) on
 // mma.sync.m16n8k16, whose 16 rows fit where the 64 or 128 rows of a tcgen05
 // instruction would stay empty: the accumulators of S are, in place, the A
 // operand of the next product.  The warps' sums are added in their order at the
 // end, so results do not vary.
 //
 // Measured (device time; the tcgen05 path at 65 tokens beside it), d = 128: 8/2
-// heads causal, 1 token 4.9, 16 tokens 6.0, 64 tokens 14.6 us (19.3); 16 x 32/8
-// heads causal, 64 tokens 52 us (57).  Bound by latency: loads, one tile's chain
-// of products, the sums.  The same split on fp32 multiply-adds, bound by its
-// reads of shared memory, took 49 and 174 us at 64 tokens.  Beyond 64 tokens the
+// heads causal, 1 token 4.1, 16 tokens 4.8, 64 tokens 13.0 us (19.2); 16 x 32/8
+// heads causal, 64 tokens 44 us (57).  Bound by latency: loads, one tile's chain
+// of products, the sums (0.44 instructions a cycle and scheduler, DRAM 5% busy).
+// dK and dV in one item took 14.6 and 52 us; the same split on fp32
+// multiply-adds, bound by its reads of shared memory, 49 and 174 us.  Beyond 64 tokens the
 // pairs grow with n^2 and the tcgen05 path's one tile of 128 does not.
 #include "common.cuh"
 #include "kernels.h"
@@ -85,12 +86,15 @@ struct Smem {
   float lse[kWarps + 1][kRows], dd[kWarps + 1][kRows];
 };
 
-template <int D, int FMT, bool KEYS>
+enum Kind { kDQ, kDK, kDV };
+
+template <int D, int FMT, Kind KIND>
 __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item, int tiles) {
   constexpr int LANES = D / 16;                  // of a row when loading
   constexpr int ROWS = 32 / LANES;               // of a warp's pass
   constexpr int PASSES = kRows / ROWS;
   constexpr int NT = D / 8;                      // 8-column tiles of a result
+  constexpr bool KEYS = KIND != kDQ, DS = KIND != kDV;     // DS: needs dS
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.H / a.Hk, heads = KEYS ? a.Hk : a.H;
   const int mine = item % tiles, head = item / tiles % heads, b = item / tiles / heads;
@@ -103,8 +107,9 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
     if (r >= a.n) return;
     const int64_t at = ((int64_t)b * a.n + r) * a.Hk + hk;
     p.x = *reinterpret_cast<const uint4*>(a.k + at * D + c16);
-    p.y[0] = *reinterpret_cast<const uint4*>(a.v + at * D + c16);
     p.xs = a.k_scales[at];
+    if (!DS) return;
+    p.y[0] = *reinterpret_cast<const uint4*>(a.v + at * D + c16);
     p.ys = a.v_scales[at];
   };
   auto load_q = [&](int hq, int r, Part& p) {
@@ -116,6 +121,8 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
     const uint4* g = reinterpret_cast<const uint4*>(a.g_o + at * D + c16);
     p.y[0] = g[0];
     p.y[1] = g[1];
+    p.lse = a.lse[((int64_t)b * a.H + hq) * a.n + r];
+    if (!DS) return;
     if (a.o) {
       const uint4* o = reinterpret_cast<const uint4*>(a.o + at * D + c16);
       p.o[0] = o[0];
@@ -124,7 +131,6 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
       p.o[0] = *reinterpret_cast<const uint4*>(a.o_codes + at * D + c16);
       p.os = a.o_scales[at];
     }
-    p.lse = a.lse[((int64_t)b * a.H + hq) * a.n + r];
   };
   // 16 values of a checkpoint: they stand for bf16
   auto put_codes = [&](__nv_bfloat16* dst, const uint4& c, float scale) {
@@ -140,7 +146,7 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
   };
   auto put_kv = [&](typename Smem<D>::Tile (&to)[2], int row, const Part& p) {
     put_codes(&to[0][row][c16], p.x, p.xs);
-    put_codes(&to[1][row][c16], p.y[0], p.ys);
+    if (DS) put_codes(&to[1][row][c16], p.y[0], p.ys);
   };
   auto put_q = [&](typename Smem<D>::Tile (&to)[2], int row, const Part& p, int slot) {
     put_codes(&to[0][row][c16], p.x, p.xs);
@@ -149,6 +155,7 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       reinterpret_cast<uint4*>(&to[1][row][c16])[v] = p.y[v];
+      if (!DS) continue;
       const uint32_t gw[4] = {p.y[v].x, p.y[v].y, p.y[v].z, p.y[v].w};
       const uint32_t ow[4] = {p.o[v].x, p.o[v].y, p.o[v].z, p.o[v].w};
       float o[8];
@@ -167,7 +174,7 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
         dot = fmaf(__uint_as_float(gw[i] & 0xffff0000u), o[2 * i + 1], dot);
       }
     }
-    dot = lanes_sum(dot, LANES);
+    if (DS) dot = lanes_sum(dot, LANES);
     if (c16 == 0) {
       sm.dd[slot][row] = a.o ? dot : dot * p.os;
       sm.lse[slot][row] = p.lse;
@@ -203,7 +210,7 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
   // rows that a lane points at: of A (and of B as [k][n], transposed), of B as [n][k]
   const uint32_t at_a = (lane & 15) * ROW + (lane >> 4) * 16;
   const uint32_t at_b = ((lane & 7) + (lane >> 4) * 8) * ROW + (lane >> 3 & 1) * 16;
-  float acc1[NT][4] = {}, acc2[KEYS ? NT : 1][4] = {};
+  float acc[NT][4] = {};
   const int g4 = lane >> 2, t4 = lane & 3;
   for (int u = warp; u < units; u += kWarps) {
     const int h = KEYS ? head * G + u / per_head : head, o0 = (first + u % per_head) * kRows;
@@ -234,18 +241,20 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
       ldm(fb, sB + at_b + k * 32);
       mma16(s[0], fa, fb[0], fb[1]);
       mma16(s[1], fa, fb[2], fb[3]);
-      ldm(fa, sA + TILE + at_a + k * 32);
-      ldm(fb, sB + TILE + at_b + k * 32);
-      mma16(dp[0], fa, fb[0], fb[1]);
-      mma16(dp[1], fa, fb[2], fb[3]);
+      if constexpr (DS) {
+        ldm(fa, sA + TILE + at_a + k * 32);
+        ldm(fb, sB + TILE + at_b + k * 32);
+        mma16(dp[0], fa, fb[0], fb[1]);
+        mma16(dp[1], fa, fb[2], fb[3]);
+      }
     }
-    // P and dS, in two parts, where the next products take them
-    uint32_t p_hi[4], p_lo[4], s_hi[4], s_lo[4];
+    // P or dS, in two parts, where the next product takes them
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float e[2], ds[2];
+        float e[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int m = g4 + 8 * r, o = 8 * t + 2 * t4 + j, c = 2 * r + j;
@@ -254,63 +263,52 @@ __device__ __forceinline__ void few_item(const BwdFew& a, Smem<D>& sm, int item,
           const bool on = key < a.n && query < a.n && (!a.causal || query >= key) &&
                           (!a.window || query - key < a.window);
           e[j] = on ? exp2f(fmaf(s[t][c], a.scale * kLog2e, -(sm.lse[slot][ql] * kLog2e))) : 0.f;
-          ds[j] = on ? e[j] * (dp[t][c] - sm.dd[slot][ql]) : 0.f;
+          if (DS) e[j] = on ? e[j] * (dp[t][c] - sm.dd[slot][ql]) : 0.f;
         }
-        split(e[0], e[1], p_hi[2 * t + r], p_lo[2 * t + r]);
-        split(ds[0], ds[1], s_hi[2 * t + r], s_lo[2 * t + r]);
+        split(e[0], e[1], hi[2 * t + r], lo[2 * t + r]);
       }
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       uint32_t fb[4];
-      ldm_t(fb, sB + at_a + x * 32);
+      ldm_t(fb, sB + (DS ? 0 : TILE) + at_a + x * 32);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        mma16(acc1[2 * x + t], s_hi, fb[2 * t], fb[2 * t + 1]);
-        mma16(acc1[2 * x + t], s_lo, fb[2 * t], fb[2 * t + 1]);
-      }
-      if constexpr (KEYS) {
-        ldm_t(fb, sB + TILE + at_a + x * 32);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          mma16(acc2[2 * x + t], p_hi, fb[2 * t], fb[2 * t + 1]);
-          mma16(acc2[2 * x + t], p_lo, fb[2 * t], fb[2 * t + 1]);
-        }
+        mma16(acc[2 * x + t], hi, fb[2 * t], fb[2 * t + 1]);
+        mma16(acc[2 * x + t], lo, fb[2 * t], fb[2 * t + 1]);
       }
     }
   }
 
   // the warps' sums, added in their order
-  auto finish = [&](const float (*acc)[4], __nv_bfloat16* to, float by) {
-    __syncthreads();                                       // what was there has been read
+  __nv_bfloat16* to = KIND == kDQ ? a.g_q : KIND == kDK ? a.g_k : a.g_v;
+  const float by = DS ? a.scale : 1.f;
+  __syncwarp();                                            // the warp's tiles have been read
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
+  for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        *reinterpret_cast<float2*>(&sm.w[warp].sum[g4 + 8 * r][8 * x + 2 * t4]) =
-            make_float2(acc[x][2 * r], acc[x][2 * r + 1]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * D / 4; i += kWarps * 32) {
-      const int row = i / (D / 4), c = i % (D / 4) * 4, r = m0 + row;
-      if (r >= a.n) continue;
-      float4 f = *reinterpret_cast<const float4*>(&sm.w[0].sum[row][c]);
+    for (int r = 0; r < 2; ++r)
+      *reinterpret_cast<float2*>(&sm.w[warp].sum[g4 + 8 * r][8 * x + 2 * t4]) =
+          make_float2(acc[x][2 * r], acc[x][2 * r + 1]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * D / 4; i += kWarps * 32) {
+    const int row = i / (D / 4), c = i % (D / 4) * 4, r = m0 + row;
+    if (r >= a.n) continue;
+    float4 f = *reinterpret_cast<const float4*>(&sm.w[0].sum[row][c]);
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 g = *reinterpret_cast<const float4*>(&sm.w[w].sum[row][c]);
-        f.x += g.x;
-        f.y += g.y;
-        f.z += g.z;
-        f.w += g.w;
-      }
-      *reinterpret_cast<uint2*>(to + (((int64_t)b * a.n + r) * heads + head) * D + c) =
-          make_uint2(pack_bf16(f.x * by, f.y * by), pack_bf16(f.z * by, f.w * by));
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 g = *reinterpret_cast<const float4*>(&sm.w[w].sum[row][c]);
+      f.x += g.x;
+      f.y += g.y;
+      f.z += g.z;
+      f.w += g.w;
     }
-  };
-  finish(acc1, KEYS ? a.g_k : a.g_q, a.scale);
-  if constexpr (KEYS) finish(acc2, a.g_v, 1.f);
+    *reinterpret_cast<uint2*>(to + (((int64_t)b * a.n + r) * heads + head) * D + c) =
+        make_uint2(pack_bf16(f.x * by, f.y * by), pack_bf16(f.z * by, f.w * by));
+  }
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) bwd_few_kernel(BwdFew a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) bwd_few_kernel(BwdFew a) {
   __shared__ Smem<D> sm;
   if (blockIdx.x == 0) {
     bool bad = false;
@@ -328,16 +326,18 @@ __global__ void __launch_bounds__(kWarps * 32) bwd_few_kernel(BwdFew a) {
   const int tiles = (a.n + kRows - 1) / kRows;
   const int key_items = a.B * a.Hk * tiles, item = (int)blockIdx.x;
   if (item < key_items)
-    few_item<D, FMT, true>(a, sm, item, tiles);
+    few_item<D, FMT, kDK>(a, sm, item, tiles);
+  else if (item < 2 * key_items)
+    few_item<D, FMT, kDV>(a, sm, item - key_items, tiles);
   else
-    few_item<D, FMT, false>(a, sm, item - key_items, tiles);
+    few_item<D, FMT, kDQ>(a, sm, item - 2 * key_items, tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_few(int d, int fmt, const BwdFew& a, cudaStream_t st) {
   const int tiles = (a.n + kRows - 1) / kRows;
-  const int64_t items = (int64_t)a.B * ((int64_t)a.Hk + a.H) * tiles;
+  const int64_t items = (int64_t)a.B * (2 * (int64_t)a.Hk + a.H) * tiles;
   if (items > INT32_MAX) return cudaErrorNotSupported;
   const unsigned g = (unsigned)items;
   if (d == 64)
