@@ -50,12 +50,17 @@ constexpr int bwd_regs(int lpr, int nv, bool spread = false) {
 // rows.  A block takes rows gridDim.x apart and keeps its sums of g_w in
 // registers; g_y, h (or its codes and scales) and g_h of the next S - 1 rows are
 // on their way to shared memory meanwhile, each thread's chunks into places of
-// its own.  With v = g_y rstd the formulas need the fewest operations,
-//   g_w += v h,  d = sum of (w v) h,  g_x = w v - (rstd^2 d / cols) h + g_h,
-// on packed pairs of fp32.  Bound by HBM: 32760 x 5120 bf16 with g_h in 192 us
-// (7.0 TB/s), h from int8 in 179 us (6.6 TB/s).  The same pass with loads into
-// registers took 354 and 719 us; with the ring but scalar arithmetic on u = h
-// rstd, 245 instructions a chunk, 240 and 255 us.
+// its own.  With u = h rstd (of 8 bits: the codes by the product of scale and
+// rstd),
+//   g_w += g_y u,  c = mean of (w g_y) u,  g_x = rstd (w g_y - c u) + g_h,
+// on packed pairs of fp32.  No product on the way is much larger or smaller than
+// a result, so rows and gradients of any size stay within fp32's range; rstd^2
+// does not (rows below 5e-20).  Bound by HBM: 32760 x 5120 bf16 with g_h in 192
+// us (7.0 TB/s), h from int8 in 180 us (6.6 TB/s).  The same pass with loads into
+// registers took 354 and 719 us; with the ring but scalar arithmetic, 245
+// instructions a chunk, 240 and 255 us.  The weight that does not stay in
+// registers is loaded in front of the row's chunks (fp32, 75000 x 640: 129 us, 140
+// behind them).
 // ODD: rows of a 16-bit type that start anywhere, as in the forward (2561 columns:
 // 24% of the copy rate element by element, 51% so), or of fp32, SPREAD.
 template <typename T, int LPR, int NV, int FMT, int S, bool ODD>
@@ -147,11 +152,14 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
     }
     return c;
   };
-  auto load_h = [&](const uint8_t* place, int k, int64_t row, uint64_t (&h)[4]) {
+  auto load_u = [&](const uint8_t* place, int k, int64_t row, float rstd, uint64_t (&u)[4]) {
     if constexpr (FMT == 0) {
-      unpack2(chunk(place + 2 * plane, k, a.h, row), h);
+      const uint64_t rr = f2_pack(rstd, rstd);
+      unpack2(chunk(place + 2 * plane, k, a.h, row), u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = fmul2(u[i], rr);
     } else {
-      const float s = *reinterpret_cast<const float*>(scale_at(place, k));
+      const float s = *reinterpret_cast<const float*>(scale_at(place, k)) * rstd;
       Codes codes;
       if constexpr (SHIFT) {
         codes = codes_odd<LPR>(codes_at(place, k), R.t, nt, a.codes + row * cols);
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
       decode8<FMT>(codes, f);
       const uint64_t ss = f2_pack(s, s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = fmul2(f2_pack(f[2 * i], f[2 * i + 1]), ss);
+      for (int i = 0; i < 4; ++i) u[i] = fmul2(f2_pack(f[2 * i], f[2 * i + 1]), ss);
     }
   };
   auto load_w = [&](int k, uint64_t (&w)[4]) {
@@ -198,28 +206,25 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
     const float rstd_next = row + stride < a.rows ? a.rstd[row + stride] : 0.f;
     if constexpr (!SHIFT) copy_wait<S - 1>();
     const uint8_t* place = mine + now * stage_bytes;
-    uint64_t wv[NV][4], h[NV][4], dot = 0;
-    const uint64_t rr = f2_pack(rstd, rstd);
+    uint64_t wg[NV][4], u[NV][4], dot = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in || !has[k]) continue;
+      if constexpr (!KEEP_W) load_w(k, w[0]);
       uint64_t g[4];
       unpack2(chunk(place, k, a.g_y, row), g);
-      load_h(place, k, row, h[k]);
-      if constexpr (!KEEP_W) load_w(k, w[0]);
+      load_u(place, k, row, rstd, u[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t v = fmul2(g[i], rr);
-        acc[k][i] = ffma2(v, h[k][i], acc[k][i]);
-        wv[k][i] = fmul2(v, w[KEEP_W ? k : 0][i]);
-        dot = ffma2(wv[k][i], h[k][i], dot);
+        acc[k][i] = ffma2(g[i], u[k][i], acc[k][i]);
+        wg[k][i] = fmul2(g[i], w[KEEP_W ? k : 0][i]);
+        dot = ffma2(wg[k][i], u[k][i], dot);
       }
     }
     float d0, d1;
     f2_unpack(dot, d0, d1);
-    const float d = row_sum<LPR>(d0 + d1, buf, slot);
-    const float c = -(d * inv_cols) * (rstd * rstd);
-    const uint64_t cc = f2_pack(c, c);
+    const float c = -(row_sum<LPR>(d0 + d1, buf, slot) * inv_cols);
+    const uint64_t cc = f2_pack(c, c), rr = f2_pack(rstd, rstd);
     T* out = static_cast<T*>(a.g_x) + row * cols + (ODD ? 0 : R.t * 8);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -227,12 +232,15 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
       if (in && has[k]) {
         uint64_t g[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = ffma2(h[k][i], cc, wv[k][i]);
+        for (int i = 0; i < 4; ++i) g[i] = ffma2(u[k][i], cc, wg[k][i]);
         if (a.g_h) {
           uint64_t e[4];
           unpack2(chunk(place + plane, k, a.g_h, row), e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g[i] = fadd2(g[i], e[i]);
+          for (int i = 0; i < 4; ++i) g[i] = ffma2(g[i], rr, e[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[i] = fmul2(g[i], rr);
         }
         if constexpr (SPREAD) {
           float f[8];

@@ -284,6 +284,33 @@ def test_norm_backward(bl, rows, cols, dtype, saved):
         assert none is None and torch.equal(only, g_x)
 
 
+@pytest.mark.parametrize("saved", ["same", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(9, 8), (13, 64), (7, 129), (5, 264), (300, 1001), (6, 1024), (4, 4096),
+                                       (3, 5123), (2, 10000)])
+def test_norm_backward_of_rows_of_any_size(bl, rows, cols, dtype, saved):
+    """Rows around 1e-20, 1 and 1e18 beside each other, with gradients whose g_x has a place in
+    the type: rstd^2 alone would leave fp32's range on either side."""
+    t = TYPES[dtype]
+    size = torch.tensor([1e-20, 1.0, 1e18], device="cuda")[torch.arange(rows, device="cuda") % 3][:, None]
+    grad = torch.tensor([1.0, 1.0, 1e-12], device="cuda")[torch.arange(rows, device="cuda") % 3][:, None]
+    h = (_randn(rows, cols, dtype=torch.float32, seed=rows) * size).to(t)
+    g_y = (_randn(rows, cols, dtype=torch.float32, seed=rows + 1) * grad).to(t)
+    w = 1 + 0.3 * _randn(cols, dtype=torch.float32, seed=cols)
+    rstd = (1 / torch.sqrt((h.double() ** 2).mean(-1))).float()
+    h8, value = h, _f64(h)
+    if saved != "same":
+        h8 = bl.act_save(h, saved, 64)
+        value = OB.load8(h8.codes.cpu().numpy(), h8.scales.cpu().numpy(), 64)
+    ref_x, ref_w = OB.rms_norm_backward(g_y, value, rstd, w)
+    g_x, g_w = bl.rms_norm_bwd(g_y, h8, rstd, w)
+    u = np.abs(value * _f64(rstd)[:, None])
+    gw = np.abs(_f64(g_y)) * np.abs(_f64(w))
+    mag = _f64(rstd)[:, None] * (gw + u * (gw * u).mean(axis=1, keepdims=True))
+    _close(g_x, ref_x, 64 * F * mag, t)
+    _close(g_w, ref_w, (rows + 64) * F * (np.abs(_f64(g_y)) * u).sum(axis=0), torch.float32)
+
+
 def test_norm_takes_views(bl):
     """Row strides, leading dims, unaligned bases: the contiguous call's values."""
     big = _randn(6, 10, 384, dtype=torch.bfloat16, seed=9)
