@@ -174,17 +174,17 @@ class _BLAttnVarlenFn(torch.autograd.Function):
 
 class _RopeFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, plan):
-        ctx.save_for_backward(positions)
+    def forward(ctx, q, k, positions, fixed, plan):
+        ctx.save_for_backward(positions, fixed)
         ctx.plan = plan
-        return ops.rope(q, k, positions, plan)
+        return ops.rope_with(q, k, positions, plan, fixed)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_q, g_k):
-        positions, = ctx.saved_tensors
+        positions, fixed = ctx.saved_tensors
         g_q, g_k = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (g_q, g_k))
-        return (*ops.rope(g_q, g_k, positions, ctx.plan, inverse=True), None, None)
+        return (*ops.rope_with(g_q, g_k, positions, ctx.plan, fixed, inverse=True), None, None, None)
 
 
 class Rotary(torch.nn.Module):
@@ -198,12 +198,12 @@ class Rotary(torch.nn.Module):
         if device is None:
             device = "cuda" if torch.cuda.is_available() else "cpu"
         self.plan = ops.RopePlan(head_dim, sections, theta, layout, shared, freqs, device)
-        # a buffer, so that the module moves between devices
+        # a buffer, so that the module moves between devices; the plan, which replicas
+        # of the module share, keeps its own
         self.register_buffer("fixed", self.plan.fixed, persistent=False)
 
     def forward(self, q, k, positions):
-        self.plan.fixed = self.fixed
-        return _RopeFn.apply(q, k, positions, self.plan)
+        return _RopeFn.apply(q, k, positions, self.fixed, self.plan)
 
 
 class _RMSNormFn(torch.autograd.Function):

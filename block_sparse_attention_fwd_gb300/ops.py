@@ -391,10 +391,16 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
     back: applied to the outputs' gradients it gives the inputs'.  Returns
     (q, k) as new contiguous tensors, or with ``inplace`` the given ones, which
     must not share elements."""
+    return rope_with(q, k, positions, plan, plan.fixed, inverse, inplace)
+
+
+def rope_with(q, k, positions, plan, fixed, inverse=False, inplace=False):
+    """``rope`` with the plan's frequencies in ``fixed``, a tensor on q's device."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype not in _lib.DTYPES:
         raise TypeError("q must be a bf16, fp16 or fp32 CUDA tensor")
     if q.dim() == 3:
-        out = rope(q[None], None if k is None else k[None], positions, plan, inverse, inplace)
+        out = rope_with(q[None], None if k is None else k[None], positions, plan, fixed, inverse,
+                        inplace)
         return (q, k) if inplace else (out[0][0], None if k is None else out[1][0])
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k are [B, n, heads, d] or packed [total, heads, d]")
@@ -404,7 +410,7 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
     if H < 1:
         raise ValueError("q needs at least one head")
     dev, dtype = q.device, q.dtype
-    _tensor(plan.fixed, "plan", dev)
+    _tensor(fixed, "plan", dev, torch.int64, (plan.pairs,))
     axes = len(plan.sections)
     batched = positions.dim() == 3
     _tensor(positions, "positions", dev, torch.int32, (B, n, axes) if batched else (n, axes))
@@ -428,7 +434,7 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
         B, n, H, Hk, d, plan.pairs, axes, *plan.padded_sections, plan.layout == "interleaved",
         bool(inverse), _lib.DTYPES[dtype], q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr,
         *q_in, *k_in, *q_st, *k_st, positions.data_ptr(), n * axes if batched else 0,
-        plan.fixed.data_ptr())
+        fixed.data_ptr())
     _launch("bl_rope", dev, args)
     return q_out, k_out
 

@@ -288,3 +288,36 @@ def test_row_strides():
     assert ops.row_stride(x[:1, :1].expand(4, 6, 32)) is None
     assert ops.row_stride(x[:, :, :1]) == 32
     assert ops.row_stride(x[2:2]) == 32
+
+
+# --- replicas ------------------------------------------------------------------------
+
+def test_rotary_replicas_keep_their_own_frequencies(monkeypatch):
+    """Replicas of a module share its plan; each call, and the backward behind it, reads the
+    frequencies of its own replica's buffer, whichever replica was called last."""
+    read = []
+
+    def turn(q, k, positions, plan, fixed, inverse=False):
+        read.append((fixed, inverse))
+        return q * 1, k * 1
+
+    monkeypatch.setattr(ops, "rope_with", turn, raising=False)
+    rot = api.Rotary(64, (32,), device="cpu")
+    replicas = []
+    for _ in range(2):
+        r = rot._replicate_for_data_parallel()
+        r._buffers["fixed"] = rot.fixed.clone()          # as a copy on a device of its own
+        replicas.append(r)
+    assert replicas[0].plan is replicas[1].plan
+    own = rot.plan.fixed
+    pos = torch.zeros(4, 1, dtype=torch.int32)
+    outs = []
+    for r in replicas:
+        q = torch.zeros(1, 4, 2, 64, requires_grad=True)
+        outs.append(r(q, q, pos)[0])
+    for o in outs:
+        o.sum().backward()
+    assert rot.plan.fixed is own
+    assert [i for _, i in read] == [False, False, True, True]
+    for j, r in enumerate(replicas):
+        assert read[j][0].data_ptr() == r.fixed.data_ptr() == read[2 + j][0].data_ptr()

@@ -168,6 +168,22 @@ def test_rotary_module_without_a_key(bl):
         assert _rel(got.view_as(ref), ref) <= 2e-6
 
 
+def test_rotary_backward_after_its_module_moved(bl):
+    """The backward reads the frequencies that its forward read, wherever the module is by then."""
+    rot = bl.Rotary(64, (32,))
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")[:, None]
+    q = _randn(1, 9, 2, 64, seed=90).requires_grad_()
+    g = _randn(1, 9, 2, 64, seed=91)
+    want, = torch.autograd.grad(rot(q, None, pos)[0], [q], [g])
+    a, _ = rot(q, None, pos)
+    rot.cpu()
+    with pytest.raises((TypeError, ValueError)):
+        rot(q.detach(), None, pos)                       # its table is on the CPU now
+    got, = torch.autograd.grad(a, [q], [g])
+    assert torch.equal(got, want)
+    assert torch.equal(rot.cuda()(q.detach(), None, pos)[0], a)
+
+
 # --- a block of them --------------------------------------------------------------------
 
 def _block(bl, causal, checkpoint, d=128, H=4, Hk=2, seed=15):
