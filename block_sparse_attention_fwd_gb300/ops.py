@@ -4,8 +4,9 @@ activations held in 8 bits until the backward.
 
 Each function checks its arguments, allocates its outputs and makes one call
 of the C ABI in ``include/bl_attn.h`` on the current stream of the tensors'
-device; all arithmetic runs in libbl_attn.so.  ``api.py`` builds the autograd
-modules from them.
+device; all arithmetic runs in libbl_attn.so.  They stand outside autograd:
+their outputs carry no gradients.  ``api.py`` builds the autograd modules from
+them.
 """
 from __future__ import annotations
 
@@ -390,7 +391,7 @@ def rope(q, k, positions, plan, inverse=False, inplace=False):
     packed tensors [total, heads, d] take [total, axes].  ``inverse`` turns
     back: applied to the outputs' gradients it gives the inputs'.  Returns
     (q, k) as new contiguous tensors, or with ``inplace`` the given ones, which
-    must not share elements."""
+    must not share elements and, in grad mode, not require gradients."""
     return rope_with(q, k, positions, plan, plan.fixed, inverse, inplace)
 
 
@@ -414,6 +415,9 @@ def rope_with(q, k, positions, plan, fixed, inverse=False, inplace=False):
     axes = len(plan.sections)
     batched = positions.dim() == 3
     _tensor(positions, "positions", dev, torch.int32, (B, n, axes) if batched else (n, axes))
+    if inplace and torch.is_grad_enabled() and \
+            (q.requires_grad or (k is not None and k.requires_grad)):
+        raise ValueError("in place, the rotation would be missing from the gradients: use Rotary")
     none = (0, 0, 0)
     q_in, q_out = _rope_strides(q, "q", dtype, B, n, d), q
     if not inplace:
@@ -436,6 +440,8 @@ def rope_with(q, k, positions, plan, fixed, inverse=False, inplace=False):
         *q_in, *k_in, *q_st, *k_st, positions.data_ptr(), n * axes if batched else 0,
         fixed.data_ptr())
     _launch("bl_rope", dev, args)
+    if inplace:                            # what autograd holds of them is stale now
+        torch.autograd.graph.increment_version(q if k is None else (q, k))
     return q_out, k_out
 
 

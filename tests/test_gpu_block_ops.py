@@ -194,6 +194,38 @@ def test_rope_refusals(bl):
             call()
 
 
+def test_rope_in_place_and_autograd(bl):
+    """In place, the rotation would be missing from the gradients of a tensor that wants them:
+    refused. What autograd holds of a tensor that is then turned counts as changed."""
+    plan = bl.RopePlan(64, (32,))
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")[:, None]
+    q, k = (_randn(1, 4, 2, 64, dtype=torch.float32, seed=s) for s in (50, 51))
+    before = q.clone()
+    wants = q.clone().requires_grad_()
+    for args in ((wants, k), (k, wants), (wants * 1, None), (wants[0], None)):
+        with pytest.raises(ValueError):
+            bl.rope(*args, pos, plan, inplace=True)
+    assert torch.equal(wants.detach(), before)
+    a = torch.ones_like(q).requires_grad_()
+    product = a * q                                      # holds q for a's gradient
+    bl.rope(q, k, pos, plan, inplace=True)
+    assert torch.equal(q, bl.rope(before, None, pos, plan)[0])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        product.sum().backward()
+    flat = before[0].clone()
+    product = a[0] * flat                                # packed tensors too
+    bl.rope(flat, None, pos, plan, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        product.sum().backward()
+    with torch.no_grad():                                # as torch's own operations allow
+        bl.rope(wants, None, pos, plan, inplace=True)
+    assert torch.equal(wants.detach(), q)
+    with torch.inference_mode():
+        x = before.clone()
+        bl.rope(x, None, pos, plan, inplace=True)
+        assert torch.equal(x, q)
+
+
 # --- norm -----------------------------------------------------------------------
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (1000, 64), (517, 128), (33, 129), (5, 256), (9, 264), (7, 1000),
