@@ -37,10 +37,37 @@ size_t part_bytes(const bl::Shape& sh) {
   return 2 * (size_t)sh.B * sh.n * sh.H * sh.d * sizeof(float);
 }
 
+// Dims from the largest stride to the smallest.
+void order_by_stride(const int64_t* stride, int* order) {
+  for (int i = 0; i < 3; ++i) order[i] = i;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[order[j]] < stride[order[j + 1]]) {
+        const int s = order[j];
+        order[j] = order[j + 1];
+        order[j + 1] = s;
+      }
+}
+// Whether each stride of a tensor of heads of d spans the dims behind it, so that
+// no two heads meet.  Every view that slices, steps over or permutes the dims of
+// a dense tensor is such.
+bool spans(const int64_t* stride, const int64_t* size, int64_t d) {
+  int order[3];
+  order_by_stride(stride, order);
+  int64_t extent = d;
+  for (int i = 2; i >= 0; --i) {
+    const int64_t s = stride[order[i]], m = size[order[i]];
+    if (m == 1) continue;
+    if (s < extent || s > ((int64_t)1 << 60) / m) return false;
+    extent += (m - 1) * s;
+  }
+  return true;
+}
+
 // Whether some head of k lies on elements of one of q's, where both have the
 // same strides: `gap` elements between their first ones, t[i] in [lo[i], hi[i]]
 // the distance of a head of k and one of q along dim i, dims from the largest
-// stride to the smallest.  Exact where each stride spans the dims behind it.
+// stride to the smallest.  Exact where each stride spans the dims behind it (spans).
 bool heads_meet(int64_t gap, const int64_t* stride, const int64_t* lo, const int64_t* hi, int dims,
                 int64_t d) {
   if (dims == 0) return gap > -d && gap < d;
@@ -49,6 +76,32 @@ bool heads_meet(int64_t gap, const int64_t* stride, const int64_t* lo, const int
     const int64_t t = s < lo[0] ? lo[0] : s > hi[0] ? hi[0] : s;
     if (heads_meet(gap + t * stride[0], stride + 1, lo + 1, hi + 1, dims - 1, d)) return true;
   }
+  return false;
+}
+
+// Whether k_out shares elements with q_out (each spans its dims), as far as their
+// batches and tokens have the same strides.
+bool outputs_meet(const bl_rope_args* r, const int64_t* q, const int64_t* k) {
+  // the stride of a dim of one element says nothing
+  const int64_t batch = r->B > 1 ? q[0] : 0, token = r->n > 1 ? q[1] : 0;
+  if ((r->B > 1 && k[0] != batch) || (r->n > 1 && k[1] != token)) return false;
+  const int64_t q_head = r->H > 1 ? q[2] : 0, k_head = r->Hk > 1 ? k[2] : 0;
+  const int64_t gap =
+      (int64_t)((intptr_t)r->k_out - (intptr_t)r->q_out) / (int64_t)size_of(r->dtype);
+  // heads a step of their own apart: q's one by one
+  const bool one_step = r->H == 1 || r->Hk == 1 || q_head == k_head;
+  const int64_t at[3] = {batch, token, one_step && r->Hk == 1 ? q_head : k_head};
+  int order[3];
+  order_by_stride(at, order);
+  int64_t stride[3], lo[3], hi[3];
+  for (int i = 0; i < 3; ++i) {
+    const int64_t span = order[i] == 0 ? r->B - 1 : r->n - 1;
+    stride[i] = at[order[i]];
+    lo[i] = order[i] == 2 ? (one_step ? 1 - (int64_t)r->H : 0) : -span;
+    hi[i] = order[i] == 2 ? r->Hk - 1 : span;
+  }
+  for (int64_t h = 0; h < (one_step ? 1 : r->H); ++h)
+    if (heads_meet(gap - h * q_head, stride, lo, hi, 3, r->d)) return true;
   return false;
 }
 
@@ -178,35 +231,11 @@ bl_status bl_rope(const bl_rope_args* r, void* stream) {
     if (q_same && a.qs[i] != a.qos[i]) return BL_ERR_INVALID_ARG;
     if (k_same && a.ks[i] != a.kos[i]) return BL_ERR_INVALID_ARG;
   }
-  if ((r->H > 1 && a.qos[2] < r->d) || (r->Hk > 1 && a.kos[2] < r->d)) return BL_ERR_INVALID_ARG;
-  if ((r->n > 1 && a.qos[1] < r->d) || (r->Hk && r->n > 1 && a.kos[1] < r->d))
-    return BL_ERR_INVALID_ARG;
-  if ((r->B > 1 && a.qos[0] < r->d) || (r->Hk && r->B > 1 && a.kos[0] < r->d))
+  const int64_t q_size[3] = {r->B, r->n, r->H}, k_size[3] = {r->B, r->n, r->Hk};
+  if (!spans(a.qos, q_size, r->d) || (r->Hk && !spans(a.kos, k_size, r->d)))
     return BL_ERR_INVALID_ARG;
   // nor those of k on those of q, where both are views of one tensor
-  if (r->Hk) {
-    if (r->q_out == r->k_out) return BL_ERR_INVALID_ARG;
-    if (a.qos[0] == a.kos[0] && a.qos[1] == a.kos[1] && a.qos[2] == a.kos[2]) {
-      const int64_t span[3] = {r->B - 1, r->n - 1, 0};
-      int order[3] = {0, 1, 2};
-      for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-          if (a.qos[order[j]] < a.qos[order[j + 1]]) {
-            const int s = order[j];
-            order[j] = order[j + 1];
-            order[j + 1] = s;
-          }
-      int64_t stride[3], lo[3], hi[3];
-      for (int i = 0; i < 3; ++i) {
-        stride[i] = a.qos[order[i]];
-        lo[i] = order[i] == 2 ? -(int64_t)(r->H - 1) : -span[order[i]];
-        hi[i] = order[i] == 2 ? r->Hk - 1 : span[order[i]];
-      }
-      const int64_t gap = (int64_t)((intptr_t)r->k_out - (intptr_t)r->q_out) /
-                          (int64_t)size_of(r->dtype);
-      if (heads_meet(gap, stride, lo, hi, 3, r->d)) return BL_ERR_INVALID_ARG;
-    }
-  }
+  if (r->Hk && (r->q_out == r->k_out || outputs_meet(r, a.qos, a.kos))) return BL_ERR_INVALID_ARG;
   if (r->positions_batch_stride != 0 &&
       r->positions_batch_stride != (int64_t)r->n * r->axes)
     return BL_ERR_INVALID_ARG;

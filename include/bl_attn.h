@@ -381,8 +381,11 @@ bl_status bl_rms_norm_bwd(int64_t rows, int64_t cols, int dtype, const void* g_y
  * those of the inputs.
  *   q, q_out  [B, n, H, d] of dtype, k, k_out [B, n, Hk, d]; Hk = 0: no k.
  *             Element strides {batch, token, head}, the dim stride is 1.
- *             q_out may be q itself (with the same strides), likewise k_out;
- *             q_out and k_out must not share elements.
+ *             q_out may be q itself (with the same strides), likewise k_out.
+ *             q_out's strides, sorted, each span the dims behind (as those of any
+ *             slice or permutation of a dense tensor do), likewise k_out's;
+ *             q_out and k_out must not share elements: refused where their
+ *             batch and token strides are alike, else up to the caller.
  *   positions [B, n, axes] int32, contiguous: positions_batch_stride is n * axes,
  *             or 0 for [n, axes] that all batches share.
  *   freqs     [pairs] uint64 on the device: round(f_p / (2 pi) * 2^64) modulo

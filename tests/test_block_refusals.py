@@ -143,6 +143,38 @@ def test_rope_refuses_shared_elements_of_one_batch(lib, strides):
     assert lib.bl_rope(ctypes.byref(args), None) == 1
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=1, strides=(64, 64, 64)),                     # the same elements as batch and token
+    dict(H=1, strides=(128, 64, 64)),                    # batches that begin within one another
+    dict(H=4, strides=(1216, 256, 64)),                  # by one head
+    dict(H=4, strides=(1280, 64, 64)),                   # tokens and heads
+    dict(H=4, strides=(1280, 192, 64)),
+    dict(H=4, strides=(256, 512, 64), B=3),              # batches within tokens: three of 256 in 512
+    dict(H=4, strides=(64, 512, 128), B=3),
+    dict(H=4, strides=(2 ** 62, 256, 64))])              # past any memory
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_rope_refuses_an_output_that_meets_itself(lib, which, kw):
+    kw = dict(kw)
+    H, st = kw.pop("H"), kw.pop("strides")
+    at = {"q": dict(H=H, q=OK, q_out=OK, q_strides=st, q_out_strides=st),
+          "k": dict(Hk=H, k=OK, k_out=OK, k_strides=st, k_out_strides=st)}[which]
+    assert lib.bl_rope(ctypes.byref(_rope_args(**at, **kw)), None) == 1
+
+
+@pytest.mark.parametrize("H,Hk,step_q,step_k,at", [
+    (3, 2, 2, 1, 1),        # heads 0, 2, 4 and 1, 2
+    (6, 2, 1, 3, 2),        # all and 2, 5
+    (2, 3, 3, 2, 1),        # 0, 3 and 1, 3, 5
+    (1, 6, 5, 1, 0), (3, 1, 2, 9, 4)])
+def test_rope_refuses_heads_of_other_steps_that_meet(lib, H, Hk, step_q, step_k, at):
+    """q takes every step_q-th of a tensor's six heads, k every step_k-th from `at`."""
+    q, k = (1920, 384, 64 * step_q), (1920, 384, 64 * step_k)
+    k_at = OK + 128 * at if at else OK + 2               # or one element behind q
+    args = _rope_args(H=H, Hk=Hk, q=OK, q_out=OK, k=k_at, k_out=k_at, q_strides=q,
+                      q_out_strides=q, k_strides=k, k_out_strides=k)
+    assert lib.bl_rope(ctypes.byref(args), None) == 1
+
+
 def test_rope_refuses_one_tensor_in_two_forms(lib):
     assert lib.bl_rope(ctypes.byref(_rope_args(q_out=2 * OK, k_out=2 * OK)), None) == 1
 

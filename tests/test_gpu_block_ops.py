@@ -226,6 +226,25 @@ def test_rope_in_place_and_autograd(bl):
         assert torch.equal(x, q)
 
 
+def test_rope_in_place_on_views_beside_each_other(bl):
+    """q and k as other heads of one tensor, at steps of their own, batches inside the tokens,
+    heads before them: the values of the call on copies, and nothing else changes."""
+    plan = bl.RopePlan(64, (32,))
+    pos = torch.randint(0, 500, (7, 1), dtype=torch.int32, device="cuda")
+    views = [lambda x: (x[:, :, 0::2], x[:, :, 1::2]), lambda x: (x[:, :, 0:4:2], x[:, :, 4:]),
+             lambda x: (x[:, :, 5:], x[:, :, 1:5:3]), lambda x: (x[:, :, :4], x[:, :, 4:5])]
+    layouts = [(lambda t: t, (2, 7, 6, 64)), (lambda t: t.transpose(0, 1), (7, 2, 6, 64)),
+               (lambda t: t.permute(0, 2, 1, 3), (2, 6, 7, 64)), (lambda t: t.permute(2, 1, 0, 3), (6, 7, 2, 64))]
+    for i, view in enumerate(views):
+        for layout, shape in layouts:
+            x = _randn(*shape, dtype=torch.bfloat16, seed=60 + i)
+            want = layout(x.clone())
+            for t, turned in zip(view(want), bl.rope(*(t.contiguous() for t in view(want)), pos, plan)):
+                t.copy_(turned)
+            bl.rope(*view(layout(x)), pos, plan, inplace=True)
+            assert torch.equal(layout(x), want)
+
+
 # --- norm -----------------------------------------------------------------------
 
 SHAPES = [(1, 1), (1, 64), (3, 7), (1000, 64), (517, 128), (33, 129), (5, 256), (9, 264), (7, 1000),
