@@ -258,7 +258,13 @@ class BLRMSNorm(torch.nn.Module):
             raise ValueError(f"rows of {x.shape[-1]} elements, the norm has {self.cols}")
         x, residual = (t if t is None or ops.row_stride(t) is not None else t.contiguous()
                        for t in (x, residual))
-        return _RMSNormFn.apply(x, self.weight, residual, self.eps, self.checkpoint, self.group)
+        checkpoint = self.checkpoint if _wants_backward(x, self.weight, residual) else None
+        return _RMSNormFn.apply(x, self.weight, residual, self.eps, checkpoint, self.group)
+
+
+def _wants_backward(*tensors):
+    """Whether a backward can follow.  (Within an autograd function the grad mode is off.)"""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def _check_checkpoint(checkpoint):
@@ -316,6 +322,14 @@ class BLAttention(torch.nn.Module):
             query, key = self.rotary(query, key, positions)
         return query, key
 
+    def _checkpoints(self, *qkv):
+        """(checkpoint, checkpoint_out, checkpoint_in_forward) of a call: nothing is kept
+        where no backward can follow, but the forward still reads rounded tensors."""
+        if _wants_backward(*qkv):
+            return self.checkpoint, self.checkpoint_out, self.checkpoint_in_forward
+        return self.checkpoint if self.checkpoint_in_forward else None, False, \
+            self.checkpoint_in_forward
+
     def forward(self, query, key, value, scale=None, return_softmax_lse=False, tile_stats=None,
                 positions=None):
         query, key = self._before(query, key, positions)
@@ -327,8 +341,7 @@ class BLAttention(torch.nn.Module):
         bk = self.block_k or bk
         q, k, v = (t.contiguous() for t in (query, key, value))
         o, lse = _BLAttnFn.apply(q, k, v, float(scale), self.negl_prob, bq, bk, tile_stats,
-                                 int(self.causal), self.window, self.checkpoint,
-                                 self.checkpoint_out, self.checkpoint_in_forward)
+                                 int(self.causal), self.window, *self._checkpoints(q, k, v))
         return (o, lse) if return_softmax_lse else o
 
     def varlen(self, query, key, value, cu_seqlens, scale=None, return_softmax_lse=False,
@@ -348,8 +361,8 @@ class BLAttention(torch.nn.Module):
         if vl.total != total:
             raise ValueError(f"cu_seqlens covers {vl.total} tokens, query has {total}")
         q, k, v = (t.contiguous() for t in (query, key, value))
-        o, lse = _BLAttnVarlenFn.apply(q, k, v, vl, float(scale), self.negl_prob, self.checkpoint,
-                                       self.checkpoint_out, self.checkpoint_in_forward)
+        o, lse = _BLAttnVarlenFn.apply(q, k, v, vl, float(scale), self.negl_prob,
+                                       *self._checkpoints(q, k, v))
         return (o, lse) if return_softmax_lse else o
 
 

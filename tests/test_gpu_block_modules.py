@@ -336,6 +336,43 @@ def test_calibration_counts_the_checkpoint(bl):
     assert worst["int8", True] < worst["e4m3", True]
 
 
+@pytest.mark.parametrize("varlen", [False, True])
+def test_nothing_is_saved_without_a_backward(bl, varlen, monkeypatch):
+    """A forward that no backward can follow forms no checkpoint; its outputs stay the same."""
+    from block_sparse_attention_fwd_gb300 import ops
+    saves, save = [], ops.act_save
+    monkeypatch.setattr(ops, "act_save", lambda x, *a: saves.append(tuple(x.shape)) or save(x, *a))
+    norm = bl.BLRMSNorm(128, checkpoint="int8", device="cuda", dtype=torch.bfloat16)
+    q, k, v = (_randn(1, 200, 2, 64, dtype=torch.bfloat16, seed=s) for s in (100, 101, 102))
+    x, r = q.flatten(-2), k.flatten(-2)
+
+    def attend(*qkv, in_forward=False):
+        attn = bl.BLAttention(0.05, checkpoint="int8", checkpoint_out=True, checkpoint_in_forward=in_forward)
+        return attn.varlen(*(t[0] for t in qkv), [0, 80, 200]) if varlen else attn(*qkv)
+
+    grad = [t.clone().requires_grad_() for t in (q, k, v)]
+    runs = [(lambda *t: attend(*t), grad, 4, 0), (lambda *t: attend(*t, in_forward=True), grad, 4, 3),
+            (lambda *t: norm(t[0].flatten(-2), t[1].flatten(-2))[0], grad, 1, 0)]
+    for run, leaves, with_grad, without in runs:
+        saves.clear()
+        want = run(*leaves)
+        assert want.requires_grad and len(saves) == with_grad
+        saves.clear()
+        with torch.no_grad():
+            assert torch.equal(run(*leaves), want)
+        assert len(saves) == without
+        norm.requires_grad_(False)                       # every tensor frozen
+        saves.clear()
+        assert torch.equal(run(*(t.detach() for t in leaves)), want)
+        assert len(saves) == without
+        saves.clear()                                    # one tensor is enough
+        some = run(leaves[0], *(t.detach() for t in leaves[1:]))
+        assert torch.equal(some, want) and some.requires_grad and len(saves) == with_grad
+        norm.requires_grad_(True)
+    saves.clear()
+    assert norm(x, r)[0].requires_grad and len(saves) == 1     # the weight alone
+
+
 # --- streams and graphs ------------------------------------------------------------------
 
 def test_another_stream(bl):
