@@ -190,7 +190,8 @@ class _RopeFn(torch.autograd.Function):
 class Rotary(torch.nn.Module):
     """Rotary positions with one to four axes: ``rotary(q, k, positions)``.  The
     arguments are those of ``ops.RopePlan``; ``positions`` as in ``ops.rope``
-    (``ops.grid_positions(T, Y, X)`` gives a video grid's)."""
+    (``ops.grid_positions(T, Y, X)`` gives a video grid's).  q and k may have any
+    strides; without a contiguous last dim they are copied first."""
 
     def __init__(self, head_dim, sections, theta: float = 10000.0, layout: str = "half",
                  shared: bool = False, freqs=None, device=None):
@@ -203,6 +204,7 @@ class Rotary(torch.nn.Module):
         self.register_buffer("fixed", self.plan.fixed, persistent=False)
 
     def forward(self, q, k, positions):
+        q, k = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (q, k))
         return _RopeFn.apply(q, k, positions, self.fixed, self.plan)
 
 

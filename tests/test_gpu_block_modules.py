@@ -184,6 +184,24 @@ def test_rotary_backward_after_its_module_moved(bl):
     assert torch.equal(rot.cuda()(q.detach(), None, pos)[0], a)
 
 
+def test_rotary_module_takes_any_strides(bl):
+    """As the attention without it does: heads or tokens last, broadcast elements."""
+    rot = bl.Rotary(64, (32,))
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")[:, None]
+    for x in (_randn(1, 64, 9, 2, seed=92).permute(0, 2, 3, 1), _randn(1, 9, 2, 1, seed=93).expand(1, 9, 2, 64)):
+        leaf = x.detach().requires_grad_()
+        g = _randn(1, 9, 2, 64, seed=94)
+        a, b = rot(leaf, leaf, pos)
+        want = rot(x.contiguous(), None, pos)[0]
+        assert torch.equal(a, want) and torch.equal(b, want)
+        got, = torch.autograd.grad(a, [leaf], [g])
+        plain = x.contiguous().requires_grad_()
+        assert torch.equal(got, torch.autograd.grad(rot(plain, None, pos)[0], [plain], [g])[0])
+    attn = bl.BLAttention(0.0, rotary=bl.Rotary(64, (32,)))
+    q, k, v = (_randn(1, 64, 9, 2, dtype=torch.bfloat16, seed=s).permute(0, 2, 3, 1) for s in (95, 96, 97))
+    assert torch.equal(attn(q, k, v, positions=pos), attn(*(t.contiguous() for t in (q, k, v)), positions=pos))
+
+
 # --- a block of them --------------------------------------------------------------------
 
 def _block(bl, causal, checkpoint, d=128, H=4, Hk=2, seed=15):
