@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(256) act_save_groups_kernel(ActSave a) {
 
 // One scale a row: a warp (BLOCK: a block) goes over its row twice, for the
 // maximum and for the codes; the second reading comes from the caches.  For rows
-// that the row kernels of norm_fwd.cu do not take (odd widths, more than 16384
-// columns).
+// that the row kernels of norm_fwd.cu do not take: fp32 that starts anywhere, and
+// more than 16384 columns (16376 of 16-bit rows that start anywhere).
 template <typename T, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(256) act_save_rows_kernel(ActSave a) {
   __shared__ float buf[2][32];
@@ -312,12 +312,12 @@ cudaError_t launch_act_save(int dtype, const ActSave& in, cudaStream_t st) {
         act_save_groups_kernel<T, true><<<blocks_for(units), 256, 0, st>>>(a);
       else
         act_save_groups_kernel<T, false><<<blocks_for(units), 256, 0, st>>>(a);
-    } else if (a.cols <= 1024) {
-      if (vec)
-        act_save_rows_kernel<T, true, false><<<blocks_for((a.rows + 7) / 8), 256, 0, st>>>(a);
-      else
-        act_save_rows_kernel<T, false, false><<<blocks_for((a.rows + 7) / 8), 256, 0, st>>>(a);
     } else {
+      if constexpr (sizeof(T) == 4)
+        if (a.cols <= 1024) {
+          act_save_rows_kernel<T, false, false><<<blocks_for((a.rows + 7) / 8), 256, 0, st>>>(a);
+          return cudaGetLastError();
+        }
       if (vec)
         act_save_rows_kernel<T, true, true><<<blocks_for(a.rows), 256, 0, st>>>(a);
       else

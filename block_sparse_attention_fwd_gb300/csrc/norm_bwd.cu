@@ -5,8 +5,9 @@ namespace bl {
 
 namespace {
 
-// The backward of any other rows, straight from global memory.  IN8: h comes in
-// 8 bits.
+// The backward of rows that the ring does not take, straight from global memory: fp32
+// that starts anywhere and is held by a warp or comes in 8 bits (IN8) or is too wide,
+// and 16-bit rows that start anywhere of more than 16376 columns.
 template <typename T, int LPR, int NV, bool VEC, bool IN8>
 __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
   __shared__ float buf[2][32];
@@ -104,20 +105,23 @@ __global__ void __launch_bounds__(1024) norm_gw_kernel(const float* __restrict__
 
 template <typename T, int FMT>
 cudaError_t bwd(int dtype, const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
-  const cudaError_t e =
+  cudaError_t e =
       vec ? bwd_ring<T, FMT, false>(a, blocks, st) : bwd_odd(dtype, a, blocks, st);
   if (e != cudaErrorNotSupported) return e;
   const Plan p = plan(a.cols, 512, 96);
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 4;     // too wide for the ring
-    *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N), 0));
-    if (vec && WIDE)
-      norm_bwd_kernel<T, L, N, WIDE, FMT != 0><<<*blocks, p.threads, 0, st>>>(a);
-    else
-      norm_bwd_kernel<T, L, N, false, FMT != 0><<<*blocks, p.threads, 0, st>>>(a);
+    if constexpr ((L == 0 && N == 4) || (sizeof(T) == 4 && (FMT != 0 || L != 0))) {
+      constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 4;     // too wide for the ring
+      *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N), 0));
+      if (vec && WIDE)
+        norm_bwd_kernel<T, L, N, WIDE, FMT != 0><<<*blocks, p.threads, 0, st>>>(a);
+      else
+        norm_bwd_kernel<T, L, N, false, FMT != 0><<<*blocks, p.threads, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
   });
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace

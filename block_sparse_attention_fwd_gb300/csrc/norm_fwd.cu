@@ -5,7 +5,9 @@ namespace bl {
 
 namespace {
 
-// Any rows, straight from global memory.  OUT8: with the 8-bit output, whose
+// Rows that the ring does not take, straight from global memory: fp32 that starts
+// anywhere or is too wide, and 16-bit rows that start anywhere of more than 16376
+// columns.  OUT8: with the 8-bit output, whose
 // groups are neighbours, so those rows keep to chunks.
 template <typename T, int LPR, int NV, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
@@ -100,15 +102,16 @@ cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
   const unsigned g = grid(a.rows, p.here, kSMs * 32);
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    if constexpr (N <= 2) {
+    if constexpr (N <= 2 && (sizeof(T) == 4 || (L == 0 && N == 2))) {
       constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 2;     // too wide for the ring
       if (vec && WIDE)
         norm_fwd_kernel<T, L, N, WIDE, FMT8 != 0><<<g, p.threads, 0, st>>>(a);
       else
         norm_fwd_kernel<T, L, N, false, FMT8 != 0><<<g, p.threads, 0, st>>>(a);
+      e = cudaGetLastError();
     }
   });
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
