@@ -303,6 +303,39 @@ def test_norm_forward_in_8_bits(bl, rows, cols, group, fmt):
     assert (np.abs(back - ry) <= step * (1 + 1e-4) + 70 * F * np.abs(ry)).all()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (257, 64), (33, 136), (9, 264), (4, 1001), (900, 777),
+                                       (500, 1024), (700, 2563), (3, 5120), (2, 8192), (2, 16380), (2, 16384)])
+@pytest.mark.parametrize("dtype,w32", [("fp16", False), ("fp16", True), ("fp32", True)])
+def test_norm_forward_of_other_types_in_8_bits(bl, rows, cols, group, fmt, dtype, w32):
+    """The bf16 test's bounds for fp16 and fp32, with a residual and without: aligned rows, rows too
+    wide for the ring and rows that start anywhere."""
+    t = TYPES[dtype]
+    x, r, w = _norm_inputs(rows, cols, t, torch.float32 if w32 else t)
+    for residual in (r, None):
+        ry, _, _ = OB.rms_norm(x, w, 1e-6, residual)
+        y, y8, h, rstd = bl.rms_norm_fwd_8bit(x, w, 1e-6, residual=residual, fmt=fmt, group=group, with_y=True)
+        plain = bl.rms_norm_fwd(x, w, 1e-6, residual=residual)
+        # fp32 rows that start anywhere: without 8 bits another order of the sum
+        for a, b in zip((y, rstd), (plain[0], plain[2])):
+            assert torch.equal(a, b) or (dtype == "fp32" and U.rel_l2(U.cpu(a), U.cpu(b)) <= 64 * F)
+        _close(y, ry, 64 * F * np.abs(ry), t)
+        assert torch.equal(h, plain[1])
+        only, h2, _ = bl.rms_norm_fwd_8bit(x, w, 1e-6, residual=residual, fmt=fmt, group=group)
+        assert torch.equal(only.codes.view(torch.uint8), y8.codes.view(torch.uint8))
+        assert torch.equal(only.scales, y8.scales) and torch.equal(h2, h)
+        codes, scales = _codes_np(y8), y8.scales.cpu().numpy()
+        size = group or cols
+        want = np.stack([np.abs(ry[:, j:j + size]).max(axis=1) for j in range(0, cols, size)], 1) / \
+            (127.0 if fmt == "int8" else 448.0)
+        assert np.abs(scales / want - 1).max() <= 66 * F
+        s = np.repeat(scales, size, axis=1)[:, :cols].astype(np.float64)
+        step = 0.5 * s if fmt == "int8" else np.maximum(np.abs(ry) / 16, s * 2.0 ** -10)
+        back = OB.load8(codes, scales, group)
+        assert (np.abs(back - ry) <= step * (1 + 1e-4) + 70 * F * np.abs(ry)).all()
+
+
 @pytest.mark.parametrize("saved", ["same", "int8", "e4m3"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows,cols", SHAPES + [(2500, 128), (700, 5120)])
