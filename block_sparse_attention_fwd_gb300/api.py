@@ -269,9 +269,11 @@ def _wants_backward(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
-def _check_checkpoint(checkpoint):
+def _check_checkpoint(checkpoint, out=False, in_forward=False):
     if checkpoint not in (None, "int8", "e4m3"):
         raise ValueError(f'checkpoint must be None, "int8" or "e4m3", got {checkpoint!r}')
+    if (out or in_forward) and checkpoint is None:
+        raise ValueError("checkpoint_out and checkpoint_in_forward need a checkpoint format")
 
 
 class BLAttention(torch.nn.Module):
@@ -297,9 +299,7 @@ class BLAttention(torch.nn.Module):
                  rotary: Rotary | None = None, checkpoint: str | None = None,
                  checkpoint_out: bool = False, checkpoint_in_forward: bool = False):
         super().__init__()
-        _check_checkpoint(checkpoint)
-        if (checkpoint_out or checkpoint_in_forward) and checkpoint is None:
-            raise ValueError("checkpoint_out and checkpoint_in_forward need a checkpoint format")
+        _check_checkpoint(checkpoint, checkpoint_out, checkpoint_in_forward)
         if not (0.0 <= negl_prob < 1.0):
             raise ValueError("negl_prob must lie in [0, 1)")
         if window < 0 or (window and not causal):

@@ -23,6 +23,7 @@ import dataclasses
 import torch
 
 from . import _lib, ops
+from .api import _check_checkpoint
 
 
 @dataclasses.dataclass
@@ -57,6 +58,7 @@ def calibrate_negl_prob(q, k, v, g_o, *, candidates=(0.005, 0.01, 0.02, 0.05, 0.
                         checkpoint_in_forward: bool = False):
     """Returns (negl_prob, trials) for bf16 device tensors q, g_o [B,n,H,d] and
     k, v [B,n,Hk,d]."""
+    _check_checkpoint(checkpoint, checkpoint_out, checkpoint_in_forward)
     B, n, H, d = q.shape
     Hk = k.shape[2]
     if scale is None:

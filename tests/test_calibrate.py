@@ -1,4 +1,6 @@
 """Host logic of negl_prob calibration (CPU only): the selection rule."""
+import pytest
+
 from block_sparse_attention_fwd_gb300.calibrate import Trial, select_negl
 
 
@@ -29,3 +31,12 @@ def test_worst_gradient_decides():
               {"G_Q": 1.0, "G_K": 1.0, "G_V": 0.98})
     assert t.worst_rel_l2 == 0.2 and t.worst_cos == 0.98
     assert select_negl([t], 0.1, 0.9) == 0.0
+
+
+@pytest.mark.parametrize("kw", [dict(checkpoint_out=True), dict(checkpoint_in_forward=True),
+                                dict(checkpoint="int4")])
+def test_checkpoint_arguments_are_checked_as_the_attentions(kw):
+    """As in BLAttention: without a format, what they ask for would silently not be measured."""
+    from block_sparse_attention_fwd_gb300.calibrate import calibrate_negl_prob
+    with pytest.raises(ValueError, match="checkpoint"):
+        calibrate_negl_prob(None, None, None, None, **kw)
