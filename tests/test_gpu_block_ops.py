@@ -114,6 +114,16 @@ def test_rope_and_its_inverse(bl, case, dtype):
             assert torch.equal(y[..., 2 * P:], x[..., 2 * P:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("case", [
+    (2, 37, 4, 2, 80, (20,), "half"),                    # halves of 20 pairs: off 16-bit vectors, on fp32's
+    (1, 37, 4, 2, 80, (40,), "half"),
+    (1, 37, 4, 2, 80, (20,), "interleaved"),
+    (3, 5, 6, 1, 96, (9, 10, 11), "half")], ids=lambda c: f"d{c[4]}p{sum(c[5])}{c[6]}")
+def test_rope_of_a_part_of_other_heads(bl, case, dtype):
+    test_rope_and_its_inverse(bl, case, dtype)
+
+
 def test_rope_takes_views_and_works_in_place(bl):
     """Heads of a fused projection, rows that start anywhere, shared positions."""
     fused = _randn(2, 50, 3 * 4, 64, dtype=torch.bfloat16, seed=4)
