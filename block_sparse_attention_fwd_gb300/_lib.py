@@ -28,7 +28,10 @@ EXPORTS = ("bl_tile_stats_elems", "bl_lists_elems", "bl_bwd_workspace_bytes", "b
            "bl_attn_bwd_varlen",
            "bl_varlen_bwd_check_status", "bl_set_wait_limit",
            "bl_act_save", "bl_act_load", "bl_rms_norm_fwd", "bl_rms_norm_bwd_workspace_bytes",
-           "bl_rms_norm_bwd", "bl_rope", "bl_attn_bwd_act8_workspace_bytes", "bl_attn_bwd_act8")
+           "bl_rms_norm_bwd", "bl_rope", "bl_attn_bwd_act8_workspace_bytes", "bl_attn_bwd_act8",
+           "bl_tile8_save", "bl_tile8_load", "bl_matmul8_workspace_bytes", "bl_matmul8",
+           "bl_layer_norm_fwd", "bl_layer_norm_bwd_workspace_bytes", "bl_layer_norm_bwd",
+           "bl_dropout", "bl_dropout_next")
 
 # bl_dtype, bl_format8
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -169,6 +172,18 @@ def load():
     lib.bl_attn_bwd_act8_workspace_bytes.restype = Z
     lib.bl_attn_bwd_act8.argtypes = [S, A, A, A, P, A, P, P, F, ctypes.POINTER(Lists), P, P, P, P,
                                      Z, P]
+    # the argument structures by reference, or their bytes
+    lib.bl_tile8_save.argtypes = [P, P]
+    lib.bl_tile8_load.argtypes = [L, L, I, P, L, P, I, P, P]
+    lib.bl_matmul8_workspace_bytes.argtypes = [P]
+    lib.bl_matmul8_workspace_bytes.restype = Z
+    lib.bl_matmul8.argtypes = [P, P]
+    lib.bl_layer_norm_fwd.argtypes = [P, P]
+    lib.bl_layer_norm_bwd_workspace_bytes.argtypes = [L, L]
+    lib.bl_layer_norm_bwd_workspace_bytes.restype = Z
+    lib.bl_layer_norm_bwd.argtypes = [P, P]
+    lib.bl_dropout.argtypes = [L, L, I, P, L, P, L, D, P, P, P]
+    lib.bl_dropout_next.argtypes = [P, P, P]
     lib.bl_status_string.argtypes = [ctypes.c_int]
     lib.bl_status_string.restype = ctypes.c_char_p
     _lib = lib

@@ -70,26 +70,28 @@ cudaError_t launch_grad_error(const void* a, const void* b, int64_t n, double* o
 cudaError_t launch_combine(int parts, int B, int n, int H, int d, const void* o_parts,
                            const float* lse_parts, void* o, float* lse, cudaStream_t st);
 
-// Rows of a root-mean-square norm (norm.cuh).  Strides in elements; y, h, g_y,
+// Rows of a root-mean-square or layer norm (norm.cuh).  Strides in elements; y, h, g_y,
 // g_x, g_h and codes are contiguous [rows, cols].
 struct NormFwd {
   int64_t rows, cols, x_stride, r_stride, groups;
   const void *x, *r, *w;          // r: residual or null; w: weight or null (ones)
+  const void* b;                  // layer norm: bias or null (zeros)
   void *y, *h;                    // y or codes may be null; h only with r
-  float* rstd;
+  float *mean, *rstd;             // mean: layer norm
   uint8_t* codes;                 // 8-bit output, with scales [rows, groups]
   float* scales;
   float eps;
   int group, fmt, shift;          // shift: from a column to its group, set by the launch
-  bool w_f32;                     // the weight is fp32, whatever x is
+  bool w_f32;                     // the weight (and bias) is fp32, whatever x is
 };
 struct NormBwd {
   int64_t rows, cols, groups;
   const void *g_y, *h, *w, *g_h;  // h null: codes and scales
   const uint8_t* codes;
-  const float *scales, *rstd;
+  const float *scales, *rstd, *mean;  // mean: layer norm
   void* g_x;
-  float* partial;                 // [norm_bwd_parts, cols], or null without g_w
+  float* partial;                 // [norm_bwd_parts, cols], or null without g_w; layer norm:
+                                  // [2 * layer_norm_bwd_parts, cols], or null without both
   int group, fmt, shift;
   bool w_f32;
 };
@@ -97,6 +99,12 @@ cudaError_t launch_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st);
 // Partial rows of g_w that the backward writes.
 int norm_bwd_parts(int64_t rows, int64_t cols);
 cudaError_t launch_norm_bwd(int dtype, const NormBwd& a, void* g_w, cudaStream_t st);
+
+cudaError_t launch_layer_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st);
+int layer_norm_bwd_parts(int64_t rows, int64_t cols);
+// g_w, g_b: either may be null.
+cudaError_t launch_layer_norm_bwd(int dtype, const NormBwd& a, void* g_w, void* g_b,
+                                  cudaStream_t st);
 
 // 8-bit activations (act8.cu).
 struct ActSave {
@@ -126,6 +134,63 @@ struct Expand {
   int64_t rows[3], blocks[3];
 };
 cudaError_t launch_expand(int d, int fmt, const Expand& a, cudaStream_t st);
+
+// e4m3 codes of x [rows, cols] with a scale for 128 elements of a row (row_*, scales
+// [rows, ceil(cols / 128)]), of a column (col_*, [ceil(rows / 128), cols]) or for 128 x 128
+// (block_*, [ceil(rows / 128), ceil(cols / 128)]); null codes: not wanted.  block_* and
+// col_* do not go together.
+struct TileSave {
+  int64_t rows, cols, x_stride, row_stride, col_stride, block_stride;
+  const void* x;
+  uint8_t *row_codes, *col_codes, *block_codes;
+  float *row_scales, *col_scales, *block_scales;
+};
+cudaError_t launch_tile_save(int dtype, const TileSave& a, cudaStream_t st);
+struct TileLoad {
+  int64_t rows, cols, stride, groups;   // groups: scales of 128 rows
+  const uint8_t* codes;
+  const float* scales;
+  void* x;
+  int shift;                            // from a column to its scale: 0 or 7
+};
+cudaError_t launch_tile_load(int dtype, const TileLoad& a, cudaStream_t st);
+
+// Products of e4m3 codes with a scale for each block of 128 of the summed dim
+// (gemm8.cu): out[i, j] = sum_b sa(i, b) sb(j, b) sum_{k in b} A[i, k] B[j, k].
+struct Gemm8 {
+  int m, n, k;
+  const uint8_t *a, *b;           // 16-byte aligned
+  int64_t a_pitch, b_pitch;       // bytes between rows, multiples of 16
+  bool a_mn, b_mn;                // rows of k codes of i (j), or rows of i (j) a k
+  const float *sa, *sb;           // at [(i >> shift) * s_i + b * s_b]
+  int64_t sa_i, sa_b, sb_i, sb_b;
+  int sa_shift, sb_shift;         // 0, or 7: 128 share a scale
+  void* out;                      // at [i * out_i + j * out_j], one of them 1
+  int64_t out_i, out_j;
+  int splits;                     // set by the launch, like:
+  bool wide;                      // 32-byte stores
+};
+cudaError_t launch_gemm8(int dtype, const Gemm8& g, cudaStream_t st);
+// 2-D TMA map of codes: `rows` rows of `inner` bytes, `pitch` bytes apart; box of 128
+// bytes x `box` rows, 128-byte swizzle, out-of-range reads 0.
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t pitch,
+                    int box);
+// `rows` rows of `cols` codes to rows `pitch` bytes apart.
+cudaError_t launch_repitch(const uint8_t* from, int64_t from_pitch, uint8_t* to, int64_t pitch,
+                           int64_t rows, int64_t cols, cudaStream_t st);
+
+// Dropout (dropout.cu).  state: seed and offset, on the device.
+struct Dropout {
+  int64_t rows, cols, x_stride, r_stride;
+  const void *x, *r;              // r: residual or null
+  void* y;
+  const int64_t* state;
+  uint32_t threshold;             // words below are dropped
+  bool all;                       // p = 1
+  float scale;
+};
+cudaError_t launch_dropout(int dtype, const Dropout& a, cudaStream_t st);
+cudaError_t launch_dropout_next(int64_t* state, int64_t* used, cudaStream_t st);
 
 // The backward whose q, k and v have been expanded into bf16 and whose o is
 // either bf16 (o_codes null) or codes with one scale a (token, head).

@@ -1,4 +1,4 @@
-// Root-mean-square norm of rows, with the residual's addition in front, an
+// Norms of rows: the root-mean-square norm, with the residual's addition in front, an
 // output in 8 bits and the backward pass:
 //
 //   h = x + r,  rstd = 1 / sqrt(mean(h^2) + eps),  y = (h rstd) w
@@ -6,6 +6,13 @@
 // and, for the gradients g_y of y and g_h of h (the residual stream's own),
 //   u = h rstd,  c = mean(w g_y u),
 //   g_x = g_r = rstd (w g_y - u c) + g_h,   g_w = sum over rows of g_y u.
+//
+// Layer norm:
+//
+//   h = x + r,  m = mean(h),  rstd = 1 / sqrt(mean((h - m)^2) + eps),
+//   y = (h - m) rstd w + b,  and with u = (h - m) rstd, c = mean(w g_y u),
+//   g_x = g_r = rstd (w g_y - mean(w g_y) - u c) + g_h,
+//   g_w = sum over rows of g_y u,  g_b = sum over rows of g_y.
 //
 // Sums run in fp32; y comes from the unrounded h, so it is rounded once.
 // The passes are bound by HBM: each input read once, each output written once.
@@ -139,6 +146,26 @@ __device__ __forceinline__ float row_sum(float v, float (*buf)[32], int& slot) {
   return v;
 }
 
+// Two sums at once (32 + 32 partial sums a slot of buf).
+template <int LPR>
+__device__ __forceinline__ float2 row_sum2(float2 v, float (*buf)[64], int& slot) {
+  v.x = lanes_sum(v.x, LPR ? LPR : 32);
+  v.y = lanes_sum(v.y, LPR ? LPR : 32);
+  if constexpr (LPR == 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float* b = buf[slot];
+    if (lane == 0) {
+      b[warp] = v.x;
+      b[32 + warp] = v.y;
+    }
+    __syncthreads();
+    v.x = lanes_sum(lane < warps ? b[lane] : 0.f, 32);
+    v.y = lanes_sum(lane < warps ? b[32 + lane] : 0.f, 32);
+    slot ^= 1;
+  }
+  return v;
+}
+
 // Lanes a row (0: the block), chunks a thread and threads of a launch over rows
 // of `cols` columns.  Up to warp_chunks chunks a warp holds whole rows and needs
 // no barrier; beyond, a block of as few threads as hold the row with two chunks
@@ -186,6 +213,9 @@ inline unsigned grid(int64_t rows, int here, int most) {
 // cudaErrorNotSupported for others and where a row is too wide.
 cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st);
 cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
+// The layer norm's.
+cudaError_t layer_fwd_odd(int dtype, const NormFwd& a, cudaStream_t st);
+cudaError_t layer_bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 
 // Calls f(lanes a row, chunks a thread) as compile-time constants.
 template <int N> struct Int { static constexpr int value = N; };

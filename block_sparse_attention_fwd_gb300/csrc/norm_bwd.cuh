@@ -1,4 +1,4 @@
-// Kernels of the root-mean-square norm's backward (norm.cuh).
+// Kernels of the norms' backward (norm.cuh).
 #pragma once
 
 #include "norm.cuh"
@@ -9,13 +9,13 @@ using namespace norm;
 
 namespace {
 
-// The end of a backward block: its threads' sums of g_w over the block's rows
-// go to the block's row of a.partial.
+// The end of a backward block: its threads' sums of g_w (g_b) over the block's rows
+// go to the block's row of `partial`.
 template <int LPR, int NV, bool VEC, bool SPREAD = false>
-__device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>& R,
+__device__ __forceinline__ void write_partial(const NormBwd& a, float* partial, const Rows<LPR>& R,
                                               const float (&acc)[NV][8], float* part) {
   const int cols = (int)a.cols;
-  float* out = a.partial + (int64_t)blockIdx.x * cols;
+  float* out = partial + (int64_t)blockIdx.x * cols;
   if constexpr (LPR != 0) {
     // the block's row slots are added in their order
     __syncthreads();
@@ -37,9 +37,11 @@ __device__ __forceinline__ void write_partial(const NormBwd& a, const Rows<LPR>&
 }
 
 // Registers a thread of the backward may take (the launch counts on them).
-// SPREAD, with an address an element, takes more.
-constexpr int bwd_regs(int lpr, int nv, bool spread = false) {
-  return nv >= 3  ? 128
+// SPREAD, with an address an element, takes more, and so does the layer norm, with
+// the sums of g_b.
+constexpr int bwd_regs(int lpr, int nv, bool spread = false, bool layer = false) {
+  return layer    ? (nv >= 2 || spread ? 128 : 88)
+         : nv >= 3  ? 128
          : spread ? (nv == 1 ? 104 : 128)
          : nv == 2 ? 96
          : lpr     ? 64
@@ -63,15 +65,20 @@ constexpr int bwd_regs(int lpr, int nv, bool spread = false) {
 // behind them).
 // ODD: rows of a 16-bit type that start anywhere, as in the forward (2561 columns:
 // 24% of the copy rate element by element, 51% so), or of fp32, SPREAD.
-template <typename T, int LPR, int NV, int FMT, int S, bool ODD>
-__global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV, ODD && sizeof(T) == 4))
+// LN: the layer norm's, u = (h - mean) rstd and g_x = rstd (w g_y - mean of w g_y - c u)
+// + g_h, with g_b beside g_w.  With three chunks a thread and more, u and w g_y do not
+// stay in registers over the row's sum but are formed again from the ring (RELOAD).
+template <typename T, int LPR, int NV, int FMT, int S, bool ODD, bool LN>
+__global__ void __launch_bounds__(LPR ? 256 : 512)
+    __maxnreg__(bwd_regs(LPR, NV, ODD && sizeof(T) == 4, LN))
     norm_bwd_ring_kernel(NormBwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   constexpr int HB = FMT ? 12 : CB;                  // of h's: codes and a scale
   constexpr bool KEEP_W = NV <= 2;                   // the weight stays in registers
   constexpr bool SHIFT = ODD && CB == 16, SPREAD = ODD && CB != 16;
+  constexpr bool RELOAD = LN && (NV >= 3 || (SPREAD && NV == 2));
   static_assert(!SPREAD || FMT == 0);
-  __shared__ float buf[2][32];
+  __shared__ float buf[2][LN ? 64 : 32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Rows<LPR> R;
   const int cols = (int)a.cols;
@@ -152,14 +159,15 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
     }
     return c;
   };
-  auto load_u = [&](const uint8_t* place, int k, int64_t row, float rstd, uint64_t (&u)[4]) {
+  auto load_u = [&](const uint8_t* place, int k, int64_t row, float mean, float rstd,
+                    uint64_t (&u)[4]) {
+    const uint64_t rr = f2_pack(rstd, rstd), mm = f2_pack(-mean, -mean);
     if constexpr (FMT == 0) {
-      const uint64_t rr = f2_pack(rstd, rstd);
       unpack2(chunk(place + 2 * plane, k, a.h, row), u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = fmul2(u[i], rr);
+      for (int i = 0; i < 4; ++i) u[i] = fmul2(LN ? fadd2(u[i], mm) : u[i], rr);
     } else {
-      const float s = *reinterpret_cast<const float*>(scale_at(place, k)) * rstd;
+      const float s = *reinterpret_cast<const float*>(scale_at(place, k)) * (LN ? 1.f : rstd);
       Codes codes;
       if constexpr (SHIFT) {
         codes = codes_odd<LPR>(codes_at(place, k), R.t, nt, a.codes + row * cols);
@@ -171,7 +179,10 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
       decode8<FMT>(codes, f);
       const uint64_t ss = f2_pack(s, s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = fmul2(f2_pack(f[2 * i], f[2 * i + 1]), ss);
+      for (int i = 0; i < 4; ++i) {
+        u[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+        u[i] = LN ? fmul2(ffma2(u[i], ss, mm), rr) : fmul2(u[i], ss);
+      }
     }
   };
   auto load_w = [&](int k, uint64_t (&w)[4]) {
@@ -185,15 +196,16 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
   const int64_t first = (int64_t)blockIdx.x * R.here;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(mine + s * stage_bytes, first + s * stride + R.mine);
-  uint64_t acc[NV][4], w[KEEP_W ? NV : 1][4];
+  uint64_t acc[NV][4], acc_b[LN ? NV : 1][4], w[KEEP_W ? NV : 1][4];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[k][i] = 0;
+    for (int i = 0; i < 4; ++i) acc[k][i] = acc_b[LN ? k : 0][i] = 0;
     if constexpr (KEEP_W) load_w(k, w[k]);
   }
   int slot = 0, now = 0, fill = S - 1;
   float rstd = first + R.mine < a.rows ? a.rstd[first + R.mine] : 0.f;
+  float mean = LN && first + R.mine < a.rows ? a.mean[first + R.mine] : 0.f;
   for (int64_t row0 = first; row0 < a.rows; row0 += stride) {
     const int64_t row = row0 + R.mine;
     const bool in = LPR == 0 || row < a.rows;
@@ -204,35 +216,58 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
     fetch(mine + fill * stage_bytes, row + (S - 1) * stride);
     // behind the fetch: in front of it the copies waited for this load (153 -> 171 us)
     const float rstd_next = row + stride < a.rows ? a.rstd[row + stride] : 0.f;
+    const float mean_next = LN && row + stride < a.rows ? a.mean[row + stride] : 0.f;
     if constexpr (!SHIFT) copy_wait<S - 1>();
     const uint8_t* place = mine + now * stage_bytes;
-    uint64_t wg[NV][4], u[NV][4], dot = 0;
+    uint64_t wg[RELOAD ? 1 : NV][4], u[RELOAD ? 1 : NV][4], dot = 0, all = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in || !has[k]) continue;
+      constexpr auto at = [](int k) { return RELOAD ? 0 : k; };
       if constexpr (!KEEP_W) load_w(k, w[0]);
       uint64_t g[4];
       unpack2(chunk(place, k, a.g_y, row), g);
-      load_u(place, k, row, rstd, u[k]);
+      load_u(place, k, row, mean, rstd, u[at(k)]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[k][i] = ffma2(g[i], u[k][i], acc[k][i]);
-        wg[k][i] = fmul2(g[i], w[KEEP_W ? k : 0][i]);
-        dot = ffma2(wg[k][i], u[k][i], dot);
+        acc[k][i] = ffma2(g[i], u[at(k)][i], acc[k][i]);
+        if constexpr (LN) acc_b[k][i] = fadd2(g[i], acc_b[k][i]);
+        wg[at(k)][i] = fmul2(g[i], w[KEEP_W ? k : 0][i]);
+        dot = ffma2(wg[at(k)][i], u[at(k)][i], dot);
+        if constexpr (LN) all = fadd2(wg[at(k)][i], all);
       }
     }
     float d0, d1;
     f2_unpack(dot, d0, d1);
-    const float c = -(row_sum<LPR>(d0 + d1, buf, slot) * inv_cols);
-    const uint64_t cc = f2_pack(c, c), rr = f2_pack(rstd, rstd);
+    float c, flat = 0.f;
+    if constexpr (LN) {
+      float a0, a1;
+      f2_unpack(all, a0, a1);
+      const float2 sums = row_sum2<LPR>(make_float2(d0 + d1, a0 + a1), buf, slot);
+      c = -(sums.x * inv_cols);
+      flat = -(sums.y * inv_cols);
+    } else {
+      c = -(row_sum<LPR>(d0 + d1, buf, slot) * inv_cols);
+    }
+    const uint64_t cc = f2_pack(c, c), rr = f2_pack(rstd, rstd), ff = f2_pack(flat, flat);
     T* out = static_cast<T*>(a.g_x) + row * cols + (ODD ? 0 : R.t * 8);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       uint32_t words[4] = {0, 0, 0, 0};
       if (in && has[k]) {
         uint64_t g[4];
+        if constexpr (RELOAD) {
+          if constexpr (!KEEP_W) load_w(k, w[0]);
+          unpack2(chunk(place, k, a.g_y, row), g);
+          load_u(place, k, row, mean, rstd, u[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = ffma2(u[k][i], cc, wg[k][i]);
+          for (int i = 0; i < 4; ++i) wg[0][i] = fmul2(g[i], w[KEEP_W ? k : 0][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[i] = ffma2(u[RELOAD ? 0 : k][i], cc, wg[RELOAD ? 0 : k][i]);
+          if constexpr (LN) g[i] = fadd2(g[i], ff);
+        }
         if (a.g_h) {
           uint64_t e[4];
           unpack2(chunk(place + plane, k, a.g_h, row), e);
@@ -261,6 +296,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
       }
     }
     rstd = rstd_next;
+    mean = mean_next;
     now = now == S - 1 ? 0 : now + 1;
     fill = fill == S - 1 ? 0 : fill + 1;
   }
@@ -270,13 +306,21 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) __maxnreg__(bwd_regs(LPR, NV,
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f2_unpack(acc[k][i], sum[k][2 * i], sum[k][2 * i + 1]);
-    write_partial<LPR, NV, !ODD, SPREAD>(a, R, sum, reinterpret_cast<float*>(ring));
+    write_partial<LPR, NV, !ODD, SPREAD>(a, a.partial, R, sum, reinterpret_cast<float*>(ring));
+    if constexpr (LN) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(acc_b[k][i], sum[k][2 * i], sum[k][2 * i + 1]);
+      write_partial<LPR, NV, !ODD, SPREAD>(a, a.partial + (int64_t)gridDim.x * cols, R, sum,
+                                           reinterpret_cast<float*>(ring));
+    }
   }
 }
 
 // Launches the ring kernel on rows that it takes, else cudaErrorNotSupported.
 // *blocks: its blocks, which are the rows of partial sums.
-template <typename T, int FMT, bool ODD>
+template <typename T, int FMT, bool ODD, bool LN>
 cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
   const Plan p = plan(a.cols, 512, 96, ODD && sizeof(T) == 2);
   cudaError_t e = cudaErrorNotSupported;
@@ -290,12 +334,13 @@ cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
       const size_t stage = (size_t)N * p.threads * (2 * CB + (FMT ? 12 : CB));
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
-        constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S, ODD>;
+        constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S, ODD, LN>;
         size_t smem = S * stage;
         if constexpr (L != 0) {                          // the block's sums of g_w go there too
           if (smem < (size_t)256 * 8 * N * 4) smem = (size_t)256 * 8 * N * 4;
         }
-        *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N, ODD && CB != 16), smem));
+        *blocks = (int)grid(a.rows, p.here,
+                            resident(p.threads, bwd_regs(L, N, ODD && CB != 16, LN), smem));
         e = allow_smem<k>();
         if (e != cudaSuccess) return;
         k<<<*blocks, p.threads, smem, st>>>(a);
@@ -311,6 +356,193 @@ cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
     }
   });
   return e;
+}
+
+// The backward of rows that the ring does not take, straight from global memory: fp32
+// that starts anywhere and is held by a warp or comes in 8 bits (IN8) or is too wide,
+// and 16-bit rows that start anywhere of more than 16376 columns.
+template <typename T, int LPR, int NV, bool VEC, bool IN8, bool LN>
+__global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
+  __shared__ float buf[2][LN ? 64 : 32];
+  __shared__ float part[LPR ? 256 * 8 * NV : 1];
+  constexpr bool SPREAD = !VEC && !IN8;
+  const Rows<LPR> R;
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.f / (float)cols;
+  float acc[NV][8], acc_b[LN ? NV : 1][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[k][i] = acc_b[LN ? k : 0][i] = 0.f;
+  int slot = 0;
+  auto unit_of = [&](int64_t row, int k, int here, float mean, float rstd, float (&u)[8]) {
+    if constexpr (!IN8) {
+      const Chunk<T> h =
+          load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.h) + row * cols, R, k, here);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = (LN ? to_f32(h.e[i]) - mean : to_f32(h.e[i])) * rstd;
+    } else {
+      const int col = (R.t + k * R.step) * 8, valid = here - col;
+      const Codes c = load_codes<VEC>(a.codes + row * cols + col, valid);
+      const float s = valid > 0 ? a.scales[row * a.groups + (col >> a.shift)] : 0.f;
+      decode8(a.fmt, c, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = (LN ? u[i] * s - mean : u[i] * s) * rstd;
+    }
+  };
+  for (int64_t row0 = (int64_t)blockIdx.x * R.here; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * R.here) {
+    const int64_t row = row0 + R.mine;
+    const bool in = row < a.rows;
+    const int here = in ? cols : 0;
+    const float rstd = in ? a.rstd[row] : 0.f;
+    const float mean = LN && in ? a.mean[row] : 0.f;
+    Chunk<T> gy[NV];
+    float dot = 0.f, all = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      gy[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.g_y) + row * cols, R, k, here);
+      float w[8], u[8];
+      unit_of(row, k, here, mean, rstd, u);
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = to_f32(gy[k].e[i]);
+        acc[k][i] = fmaf(g, u[i], acc[k][i]);
+        dot = fmaf(g * w[i], u[i], dot);
+        if constexpr (LN) {
+          acc_b[k][i] += g;
+          all = fmaf(g, w[i], all);
+        }
+      }
+    }
+    float c, flat = 0.f;
+    if constexpr (LN) {
+      const float2 sums = row_sum2<LPR>(make_float2(dot, all), buf, slot);
+      c = sums.x * inv_cols;
+      flat = sums.y * inv_cols;
+    } else {
+      c = row_sum<LPR>(dot, buf, slot) * inv_cols;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float w[8], u[8], g[8];
+      unit_of(row, k, here, mean, rstd, u);                  // from the caches
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = to_f32(gy[k].e[i]) * w[i] - u[i] * c;
+        g[i] = rstd * (LN ? g[i] - flat : g[i]);
+      }
+      if (a.g_h) {
+        const Chunk<T> e =
+            load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.g_h) + row * cols, R, k, here);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += to_f32(e.e[i]);
+      }
+      store_unit<T, VEC, SPREAD>(static_cast<T*>(a.g_x) + row * cols, R, k, here, g);
+    }
+  }
+  if (a.partial) {
+    write_partial<LPR, NV, VEC, SPREAD>(a, a.partial, R, acc, part);
+    if constexpr (LN)
+      write_partial<LPR, NV, VEC, SPREAD>(a, a.partial + (int64_t)gridDim.x * cols, R, acc_b, part);
+  }
+}
+
+// g_w[col] (of the second row of blocks, g_b) = sum of the blocks' partial sums, 32 columns a block, 32 slices of
+// the partial rows side by side and then added in their order: no atomics, so
+// the result does not vary.  4 us at 4096 columns, most of it the launch.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_gw_kernel(const float* __restrict__ partial, int parts,
+                                                       int cols, void* g_w, void* g_b, bool f32) {
+  __shared__ float s[32][33];
+  if (blockIdx.y) {
+    partial += (int64_t)parts * cols;
+    g_w = g_b;
+  }
+  if (!g_w) return;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + x;
+  float v = 0.f;
+  if (col < cols)
+    for (int p = y; p < parts; p += 32) v += partial[(int64_t)p * cols + col];
+  s[y][x] = v;
+  __syncthreads();
+  if (y == 0 && col < cols) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[i][x];
+    if (f32)
+      static_cast<float*>(g_w)[col] = sum;
+    else
+      static_cast<T*>(g_w)[col] = from_f32<T>(sum);
+  }
+}
+
+template <typename T, int FMT, bool LN>
+cudaError_t bwd(int dtype, const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
+  cudaError_t e =
+      vec  ? bwd_ring<T, FMT, false, LN>(a, blocks, st)
+      : LN ? layer_bwd_odd(dtype, a, blocks, st)
+           : bwd_odd(dtype, a, blocks, st);
+  if (e != cudaErrorNotSupported) return e;
+  const Plan p = plan(a.cols, 512, 96);
+  with_plan(p, [&](auto lpr, auto nv) {
+    constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
+    if constexpr ((L == 0 && N == 4) || (sizeof(T) == 4 && (FMT != 0 || L != 0))) {
+      constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 4;     // too wide for the ring
+      *blocks = (int)grid(a.rows, p.here, resident(p.threads, bwd_regs(L, N, false, LN), 0));
+      if (vec && WIDE)
+        norm_bwd_kernel<T, L, N, WIDE, FMT != 0, LN><<<*blocks, p.threads, 0, st>>>(a);
+      else
+        norm_bwd_kernel<T, L, N, false, FMT != 0, LN><<<*blocks, p.threads, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+  });
+  return e;
+}
+
+// Rows of partial sums that the backward writes at most.
+template <bool LN>
+int bwd_parts_of(int64_t rows, int64_t cols) {
+  // of either way to lay out the rows
+  int most = 0;
+  for (bool odd : {false, true}) {
+    const Plan p = plan(cols, 512, 96, odd);
+    const int blocks =
+        (int)grid(rows, p.here, resident(p.threads, bwd_regs(p.lpr, p.nv, false, LN), 0));
+    if (blocks > most) most = blocks;
+  }
+  return most;
+}
+
+// The backward's launch on rows of any kind.
+template <bool LN>
+cudaError_t launch_bwd_of(int dtype, const NormBwd& in, void* g_w, void* g_b, cudaStream_t st) {
+  NormBwd a = in;
+  a.shift = group_shift(a.group);
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const size_t al = chunk_align(dtype);
+    const bool vec = a.cols % 8 == 0 && aligned_to(a.g_y, al) && aligned_to(a.h, al) &&
+                     aligned_to(a.g_h, al) && aligned_to(a.g_x, al) &&
+                     aligned_to(a.w, a.w_f32 ? 32 : 16) && aligned_to(a.codes, 8) &&
+                     aligned_to(a.partial, 32);
+    int blocks = 0;
+    if (a.rows > 0) {
+      const cudaError_t e = !a.codes              ? bwd<T, 0, LN>(dtype, a, vec, &blocks, st)
+                            : a.fmt == kFmtInt8   ? bwd<T, kFmtInt8, LN>(dtype, a, vec, &blocks, st)
+                                                  : bwd<T, kFmtE4m3, LN>(dtype, a, vec, &blocks, st);
+      if (e != cudaSuccess) return e;
+    }
+    if (g_w || g_b) {
+      norm_gw_kernel<T><<<dim3((unsigned)((a.cols + 31) / 32), g_b ? 2 : 1), 1024, 0, st>>>(
+          a.partial, blocks, (int)a.cols, g_w, g_b, a.w_f32);
+      return cudaGetLastError();
+    }
+    return cudaSuccess;
+  });
 }
 
 }  // namespace

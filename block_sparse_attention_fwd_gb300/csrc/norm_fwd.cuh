@@ -1,5 +1,4 @@
-// Kernels of the root-mean-square norm's forward (norm.cuh), which also save rows
-// in 8 bits.
+// Kernels of the norms' forward (norm.cuh), which also save rows in 8 bits.
 #pragma once
 
 #include "norm.cuh"
@@ -17,15 +16,17 @@ namespace {
 // Bound by HBM: 32760 x 5120 bf16 in 100 us, with the residual in 196 us
 // (6.8 TB/s), with the residual to e4m3 in 175 us (6.7 TB/s; issue slots are 74%
 // busy there).  FMT8: 0 without the 8-bit output, else its format.  NORM = false
-// only saves x in 8 bits: the same walk without the norm.
+// only saves x in 8 bits: the same walk without the norm.  LN: the layer norm, whose
+// squares are summed of the centred row, which is a second reduction.
 // ODD: rows of a 16-bit type that start anywhere.  Their aligned vectors go to
 // the ring, and a chunk is shifted out of its own and the next thread's vector:
 // one barrier more, and some 40 instructions a chunk and tensor (2561 columns: 23%
 // of the copy rate element by element, 50% so, 63% with a residual).
-template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD>
+template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
+  static_assert(NORM || !LN);
   __shared__ float buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Rows<LPR> R;
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
   const int64_t first = (int64_t)blockIdx.x * R.here;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s, first + s * stride + R.mine);
-  uint64_t w[NV][4];                                 // pairs of fp32, like h
+  uint64_t w[NV][4], b[LN ? NV : 1][4];              // pairs of fp32, like h
   if constexpr (NORM) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -84,6 +85,11 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
       load_weight8<T, !ODD>(a.w, a.w_f32, col, cols - col, f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[k][i] = f2_pack(f[2 * i], f[2 * i + 1]);
+      if constexpr (LN) {
+        load_bias8<T, !ODD>(a.b, a.w_f32, col, cols - col, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[k][i] = f2_pack(f[2 * i], f[2 * i + 1]);
+      }
     }
   }
   int slot = 0, now = 0, fill = S - 1;
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
         }
         if constexpr (NORM) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ss = ffma2(h[k][i], h[k][i], ss);
+          for (int i = 0; i < 4; ++i)
+            ss = LN ? fadd2(h[k][i], ss) : ffma2(h[k][i], h[k][i], ss);
         }
       } else {
 #pragma unroll
@@ -148,7 +155,32 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
     if constexpr (NORM) {
       float s0, s1;
       f2_unpack(ss, s0, s1);
-      const float sum = row_sum<LPR>(s0 + s1, buf, slot);
+      float sum = row_sum<LPR>(s0 + s1, buf, slot);
+      if constexpr (LN) {
+        const float mean = sum * inv_cols;
+        if (R.t == 0 && in && a.mean) a.mean[row] = mean;
+        const uint64_t mm = f2_pack(-mean, -mean);
+        ss = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int valid = in ? cols - (R.t + k * R.step) * 8 : 0;
+          if (valid <= 0) continue;                  // h stays 0 there
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[k][i] = fadd2(h[k][i], mm);
+          if constexpr (ODD) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float lo, hi;
+              f2_unpack(h[k][i], lo, hi);
+              h[k][i] = f2_pack(2 * i < valid ? lo : 0.f, 2 * i + 1 < valid ? hi : 0.f);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = ffma2(h[k][i], h[k][i], ss);
+        }
+        f2_unpack(ss, s0, s1);
+        sum = row_sum<LPR>(s0 + s1, buf, slot);
+      }
       const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
       if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
       const uint64_t rr = f2_pack(rstd, rstd);
@@ -156,7 +188,9 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
       for (int k = 0; k < NV; ++k) {
         const bool has = in && (R.t + k * R.step) * 8 < cols;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[k][i] = fmul2(fmul2(h[k][i], rr), w[k][i]);
+        for (int i = 0; i < 4; ++i)
+          h[k][i] = LN ? ffma2(fmul2(h[k][i], rr), w[k][i], b[LN ? k : 0][i])
+                       : fmul2(fmul2(h[k][i], rr), w[k][i]);
         if (a.y) write(a.y, k, h[k], has);
       }
     }
@@ -217,7 +251,7 @@ int fwd_blocks(int64_t rows, const Plan& p, int regs, size_t smem) {
 }
 
 // Launches the ring kernel on rows that it takes, else cudaErrorNotSupported.
-template <typename T, int FMT8, bool NORM, bool ODD>
+template <typename T, int FMT8, bool NORM, bool ODD, bool LN>
 cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
   const Plan p = plan(a.cols, 1024, 64, ODD);
   cudaError_t e = cudaErrorNotSupported;
@@ -228,11 +262,11 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
       const size_t stage = (size_t)N * p.threads * (NORM ? 2 : 1) * sizeof(Chunk<T>);
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
-        constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM, ODD>;
+        constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM, ODD, LN>;
         const size_t smem = S * stage;
         e = allow_smem<k>();
         if (e != cudaSuccess) return;
-        k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, NORM ? 64 : 48, smem)), p.threads, smem,
+        k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, LN ? 80 : NORM ? 64 : 48, smem)), p.threads, smem,
             st>>>(a);
         e = cudaGetLastError();
       };
@@ -244,6 +278,159 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
     }
   });
   return e;
+}
+
+// Rows that the ring does not take, straight from global memory: fp32 that starts
+// anywhere or is too wide, and 16-bit rows that start anywhere of more than 16376
+// columns.  OUT8: with the 8-bit output, whose
+// groups are neighbours, so those rows keep to chunks.
+template <typename T, int LPR, int NV, bool VEC, bool OUT8, bool LN>
+__global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
+  __shared__ float buf[2][32];
+  constexpr bool SPREAD = !VEC && !OUT8;
+  const Rows<LPR> R;
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.f / (float)cols;
+  int slot = 0;
+  // the loop is uniform over the block (lanes past the last row work on zeros)
+  for (int64_t row0 = (int64_t)blockIdx.x * R.here; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * R.here) {
+    const int64_t row = row0 + R.mine;
+    const bool in = row < a.rows;
+    const int here = in ? cols : 0;
+    float h[NV][8];
+    float s0 = 0.f, s1 = 0.f;                          // as the ring kernel sums them
+    Chunk<T> x[NV], r[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      x[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.x) + row * a.x_stride, R, k, here);
+      if (a.r)
+        r[k] = load_unit<T, VEC, SPREAD>(static_cast<const T*>(a.r) + row * a.r_stride, R, k, here);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] = to_f32(x[k].e[i]);
+      if (a.r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] += to_f32(r[k].e[i]);
+        if (a.h) store_unit<T, VEC, SPREAD>(static_cast<T*>(a.h) + row * cols, R, k, here, h[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        s0 = LN ? s0 + h[k][i] : fmaf(h[k][i], h[k][i], s0);
+        s1 = LN ? s1 + h[k][i + 1] : fmaf(h[k][i + 1], h[k][i + 1], s1);
+      }
+    }
+    float ss = row_sum<LPR>(s0 + s1, buf, slot);
+    if constexpr (LN) {
+      const float mean = ss * inv_cols;
+      if (R.t == 0 && in && a.mean) a.mean[row] = mean;
+      s0 = s1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          h[k][i] = col_of<SPREAD>(R, k, i) < here ? h[k][i] - mean : 0.f;
+          h[k][i + 1] = col_of<SPREAD>(R, k, i + 1) < here ? h[k][i + 1] - mean : 0.f;
+          s0 = fmaf(h[k][i], h[k][i], s0);
+          s1 = fmaf(h[k][i + 1], h[k][i + 1], s1);
+        }
+      ss = row_sum<LPR>(s0 + s1, buf, slot);
+    }
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, a.eps));
+    if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float w[8];
+      weight_unit<T, VEC, SPREAD>(a.w, a.w_f32, R, k, cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rstd * w[i];
+      if constexpr (LN) {
+        if (a.b) {
+          weight_unit<T, VEC, SPREAD>(a.b, a.w_f32, R, k, cols, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] += w[i];
+        }
+      }
+      if (a.y) store_unit<T, VEC, SPREAD>(static_cast<T*>(a.y) + row * cols, R, k, here, h[k]);
+      if constexpr (OUT8) {
+        const int col = (R.t + k * R.step) * 8;
+        const int valid = in ? cols - col : 0;
+        float m = amax8(h[k]);
+        if (a.group) {
+          m = lanes_amax(m, min(a.group / 8, LPR ? LPR : 32));
+          const float scale = scale_of(m, a.fmt);
+          store_codes<VEC>(a.codes + row * cols + col, encode8(a.fmt, h[k], scale), valid);
+          if (valid > 0 && (col & (a.group - 1)) == 0)
+            a.scales[row * a.groups + (col >> a.shift)] = scale;
+        } else {
+          top = amax2(top, m);
+        }
+      }
+    }
+    if constexpr (OUT8) {
+      if (!a.group) {
+        if constexpr (LPR != 0) {
+          top = lanes_amax(top, LPR);
+        } else {
+          top = block_amax(top, buf, slot);
+          slot ^= 1;
+        }
+        const float scale = scale_of(top, a.fmt);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int col = (R.t + k * R.step) * 8;
+          const int valid = in ? cols - col : 0;
+          store_codes<VEC>(a.codes + row * cols + col, encode8(a.fmt, h[k], scale), valid);
+        }
+        if (R.t == 0 && in) a.scales[row] = scale;
+      }
+    }
+  }
+}
+
+template <typename T, int FMT8, bool LN>
+cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
+  cudaError_t e = vec  ? fwd_ring<T, FMT8, true, false, LN>(a, st)
+                  : LN ? layer_fwd_odd(dtype, a, st)
+                       : fwd_odd(dtype, true, a, st);
+  if (e != cudaErrorNotSupported) return e;
+  const Plan p = plan(a.cols, 1024, 64);
+  const unsigned g = grid(a.rows, p.here, kSMs * 32);
+  with_plan(p, [&](auto lpr, auto nv) {
+    constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
+    if constexpr (N <= 2 && (sizeof(T) == 4 || (L == 0 && N == 2))) {
+      constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 2;     // too wide for the ring
+      if (vec && WIDE)
+        norm_fwd_kernel<T, L, N, WIDE, FMT8 != 0, LN><<<g, p.threads, 0, st>>>(a);
+      else
+        norm_fwd_kernel<T, L, N, false, FMT8 != 0, LN><<<g, p.threads, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+  });
+  return e;
+}
+
+// The forward's launch on rows of any kind.
+template <bool LN>
+cudaError_t launch_fwd_of(int dtype, const NormFwd& in, cudaStream_t st) {
+  NormFwd a = in;
+  if (a.rows == 0) return cudaSuccess;
+  a.shift = group_shift(a.group);
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const size_t al = chunk_align(dtype);
+    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
+                     aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.h, al) &&
+                     aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) && aligned_to(a.b, a.w_f32 ? 32 : 16) &&
+                     aligned_to(a.codes, 8);
+    const int fmt = a.codes ? a.fmt : 0;
+    return fmt == 0          ? fwd<T, 0, LN>(dtype, a, vec, st)
+           : fmt == kFmtInt8 ? fwd<T, kFmtInt8, LN>(dtype, a, vec, st)
+                             : fwd<T, kFmtE4m3, LN>(dtype, a, vec, st);
+  });
 }
 
 }  // namespace

@@ -11,11 +11,11 @@ cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st) {
   auto launch = [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     if (!norm)
-      return fmt == kFmtInt8 ? fwd_ring<T, kFmtInt8, false, true>(a, st)
-                             : fwd_ring<T, kFmtE4m3, false, true>(a, st);
-    return fmt == 0          ? fwd_ring<T, 0, true, true>(a, st)
-           : fmt == kFmtInt8 ? fwd_ring<T, kFmtInt8, true, true>(a, st)
-                             : fwd_ring<T, kFmtE4m3, true, true>(a, st);
+      return fmt == kFmtInt8 ? fwd_ring<T, kFmtInt8, false, true, false>(a, st)
+                             : fwd_ring<T, kFmtE4m3, false, true, false>(a, st);
+    return fmt == 0          ? fwd_ring<T, 0, true, true, false>(a, st)
+           : fmt == kFmtInt8 ? fwd_ring<T, kFmtInt8, true, true, false>(a, st)
+                             : fwd_ring<T, kFmtE4m3, true, true, false>(a, st);
   };
   return dtype == 0 ? launch((__nv_bfloat16*)nullptr) : launch((__half*)nullptr);
 }

@@ -491,6 +491,18 @@ __device__ __forceinline__ void load_weight8(const void* w, bool f32, int64_t co
   }
 }
 
+// A bias row likewise (or none: zeros).
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_bias8(const void* b, bool f32, int64_t col, int valid,
+                                           float (&f)[8]) {
+  if (b) {
+    load_weight8<T, VEC>(b, f32, col, valid, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  }
+}
+
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }

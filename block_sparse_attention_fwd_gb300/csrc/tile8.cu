@@ -1,0 +1,208 @@
+// Saving in e4m3 for products in 8 bits (gemm8.cu): of a tensor [rows, cols], in one
+// reading, with one scale for every
+//   128 elements of a row        the codes that products over the columns read
+//   128 elements of a column     those of products over the rows
+//   128 x 128 elements           a weight's, which both kinds of product read
+// in the format of rows.cuh.  And the loading of the last two.
+//
+// A block takes a tile of 128 x 128: a thread holds a chunk of 8 columns of 8 rows, 16
+// apart, in registers, so a row lies in 16 neighbouring lanes and a column in 16 threads
+// of 8 warps.  Bound by HBM: x once in, a byte an element and kind out.
+#include <type_traits>
+
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace bl {
+
+namespace {
+
+// 8 codes to a row of codes of which `valid` exist; WIDE: 8-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ void put_codes(uint8_t* p, const Codes& c, int valid) {
+  if (WIDE && valid >= 8)
+    store_codes<true>(p, c, 8);
+  else
+    store_codes<false>(p, c, valid);
+}
+
+template <typename T, bool VEC, bool WIDE>
+__global__ void __launch_bounds__(256) tile_save_kernel(TileSave a) {
+  __shared__ float part[8][128];
+  __shared__ __align__(16) float col_scale[128];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t tiles_x = (a.cols + 127) / 128;
+  const int64_t bx = blockIdx.x % tiles_x, by = blockIdx.x / tiles_x;
+  const int64_t row0 = by * 128, col0 = bx * 128, col = col0 + tx * 8;
+  const int valid = (int)min(max(a.cols - col, (int64_t)0), (int64_t)8);
+  Chunk<T> c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = row0 + ty + 16 * k;
+    c[k] = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col,
+                         row < a.rows ? valid : 0);
+  }
+  if (a.row_codes) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = row0 + ty + 16 * k;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(c[k].e[i]);
+      const float scale = scale_of(lanes_amax(amax8(f), 16), kFmtE4m3);
+      if (row < a.rows) {
+        put_codes<WIDE>(a.row_codes + row * a.row_stride + col, encode8<kFmtE4m3>(f, scale), valid);
+        if (tx == 0) a.row_scales[row * tiles_x + bx] = scale;
+      }
+    }
+  }
+  if (!a.col_codes && !a.block_codes) return;
+  float top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top[i] = to_f32(c[0].e[i]);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) top[i] = amax2(top[i], to_f32(c[k].e[i]));
+  }
+  if (a.block_codes) {
+    const float m = lanes_amax(amax8(top), 32);
+    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = m;
+    __syncthreads();
+    const float scale = scale_of(lanes_amax(part[0][threadIdx.x & 7], 8), kFmtE4m3);
+    if (threadIdx.x == 0) a.block_scales[by * tiles_x + bx] = scale;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = row0 + ty + 16 * k;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(c[k].e[i]);
+      if (row < a.rows)
+        put_codes<WIDE>(a.block_codes + row * a.block_stride + col, encode8<kFmtE4m3>(f, scale),
+                        valid);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top[i] = amax2(top[i], __shfl_xor_sync(0xffffffffu, top[i], 16));
+    if ((threadIdx.x & 16) == 0) part[threadIdx.x >> 5][tx * 8 + i] = top[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float m = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = amax2(m, part[w][threadIdx.x]);
+    const float scale = scale_of(m, kFmtE4m3);
+    col_scale[threadIdx.x] = scale;
+    if (col0 + threadIdx.x < a.cols) a.col_scales[by * a.cols + col0 + threadIdx.x] = scale;
+  }
+  __syncthreads();
+  float inv[8];
+  uint32_t keep[2] = {0u, 0u};                       // codes 0 under a scale that is NaN
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float scale = col_scale[tx * 8 + i];
+    inv[i] = __frcp_rn(scale);
+    if (!isnan(scale)) keep[i / 4] |= 0xffu << (8 * (i % 4));
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = row0 + ty + 16 * k;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(to_f32(c[k].e[i]), inv[i]);
+    Codes codes = encode8<kFmtE4m3>(f, 1.f);
+    codes.w[0] &= keep[0];
+    codes.w[1] &= keep[1];
+    if (row < a.rows) put_codes<WIDE>(a.col_codes + row * a.col_stride + col, codes, valid);
+  }
+}
+
+// Values of codes [rows, cols] whose scale lies at scales[(row / 128) * s_row + (col >> shift)
+// * s_col]: columns' groups (shift 0) or blocks (7).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) tile_load_kernel(TileLoad a) {
+  const int64_t per_row = (a.cols + 7) / 8, total = a.rows * per_row;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += step) {
+    const int64_t row = x / per_row, col = (x - row * per_row) * 8;
+    const int valid = (int)min(a.cols - col, (int64_t)8);
+    const Codes c = load_codes<VEC>(a.codes + row * a.stride + col, valid);
+    const float* s = a.scales + (row >> 7) * a.groups;
+    float f[8];
+    decode8<kFmtE4m3>(c, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) f[i] *= s[(col + i) >> a.shift];
+    store8<T, VEC>(static_cast<T*>(a.x) + row * a.cols + col, f, valid);
+  }
+}
+
+// Rows of codes that start anywhere to rows `pitch` bytes apart (16-byte aligned), 16 bytes
+// a thread out of the aligned words that cover them.
+__global__ void __launch_bounds__(256) repitch_kernel(const uint8_t* __restrict__ from,
+                                                      int64_t from_pitch, uint8_t* __restrict__ to,
+                                                      int64_t pitch, int64_t rows, int64_t cols) {
+  const int64_t per_row = (cols + 15) / 16, total = rows * per_row;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += step) {
+    const int64_t row = x / per_row, col = (x - row * per_row) * 16;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(from + row * from_pitch + col);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(from + row * from_pitch + cols);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+    uint32_t w[5], out[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = reinterpret_cast<uintptr_t>(p + i) < end ? __ldg(p + i) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (int)(at & 3) * 8);
+    *reinterpret_cast<uint4*>(to + row * pitch + col) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_repitch(const uint8_t* from, int64_t from_pitch, uint8_t* to, int64_t pitch,
+                           int64_t rows, int64_t cols, cudaStream_t st) {
+  const int64_t blocks = (rows * ((cols + 15) / 16) + 255) / 256;
+  repitch_kernel<<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, st>>>(
+      from, from_pitch, to, pitch, rows, cols);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tile_save(int dtype, const TileSave& a, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, chunk_align(dtype));
+    const bool wide = a.row_stride % 8 == 0 && a.col_stride % 8 == 0 && a.block_stride % 8 == 0 &&
+                      aligned_to(a.row_codes, 8) && aligned_to(a.col_codes, 8) &&
+                      aligned_to(a.block_codes, 8);
+    const unsigned g = (unsigned)tiles;
+    if (vec && wide)
+      tile_save_kernel<T, true, true><<<g, 256, 0, st>>>(a);
+    else if (wide)
+      tile_save_kernel<T, false, true><<<g, 256, 0, st>>>(a);
+    else
+      tile_save_kernel<T, false, false><<<g, 256, 0, st>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_tile_load(int dtype, const TileLoad& a, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  return with_type(dtype, [&](auto* z) {
+    using T = std::remove_pointer_t<decltype(z)>;
+    const int64_t blocks = (a.rows * ((a.cols + 7) / 8) + 255) / 256;
+    const unsigned g = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
+    if (a.cols % 8 == 0 && a.stride % 8 == 0 && aligned_to(a.codes, 8) &&
+        aligned_to(a.x, chunk_align(dtype)))
+      tile_load_kernel<T, true><<<g, 256, 0, st>>>(a);
+    else
+      tile_load_kernel<T, false><<<g, 256, 0, st>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace bl

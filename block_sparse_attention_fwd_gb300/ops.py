@@ -164,8 +164,11 @@ def act_save(x, fmt="int8", group=0) -> Act8:
     return a
 
 
-def act_load(a: Act8):
-    """The tensor an Act8 stands for, in the type it was saved from."""
+def act_load(a):
+    """The tensor an Act8 (or a Weight8 or Cols8) stands for, in the type it was saved
+    from."""
+    if not isinstance(a, Act8):
+        return a.load()
     x = torch.empty(a.codes.shape, dtype=a.dtype, device=a.codes.device)
     cols = x.shape[-1]
     _launch("bl_act_load", x.device, x.numel() // cols, cols, _lib.DTYPES[a.dtype],

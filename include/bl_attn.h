@@ -422,6 +422,140 @@ bl_status bl_attn_bwd_act8(const bl_shape* shape, const bl_act8* q8, const bl_ac
                            void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The linear layers around the attention: products of e4m3 codes with a scale
+ * for each block of 128, the layer norm, and dropout whose mask is never stored.
+ * (These too have no counterpart in the BackLite pages.)  Rows, strides and
+ * alignment as above.
+ * ------------------------------------------------------------------------- */
+
+/* x [rows, cols] (dtype, row stride x_stride) in e4m3, in one reading, with the
+ * format of bl_act8 and one scale for every
+ *   128 elements of a row      row_codes,   row_scales [rows, ceil(cols / 128)]
+ *                              (what bl_act_save gives with group 128)
+ *   128 elements of a column   col_codes,   col_scales [ceil(rows / 128), cols]
+ *   128 x 128 elements         block_codes, block_scales [ceil(rows / 128), ceil(cols / 128)]
+ * (groups at the ends may be cut).  Codes are [rows, cols] with the row strides
+ * given; NULL codes are not wanted.  At least one of the three, and not both
+ * columns and blocks.  Bytes behind the columns stay as they were.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED (2^31 tiles of 128 x 128 and more),
+ * BL_ERR_CUDA. */
+typedef struct {
+  int64_t rows, cols, x_stride, row_stride, col_stride, block_stride;
+  const void* x;
+  void* row_codes;
+  float* row_scales;
+  void* col_codes;
+  float* col_scales;
+  void* block_codes;
+  float* block_scales;
+  int dtype;
+} bl_tile8_args;
+bl_status bl_tile8_save(const bl_tile8_args* args, void* stream);
+
+/* The values of codes [rows, cols] (row stride `stride`) with scales for 128
+ * elements of a column (blocks = 0) or for 128 x 128 (blocks = 1), rounded to
+ * dtype, into x [rows, cols] (contiguous). */
+bl_status bl_tile8_load(int64_t rows, int64_t cols, int dtype, const void* codes, int64_t stride,
+                        const float* scales, int blocks, void* x, void* stream);
+
+/* The products of a linear layer y = x w^T, x [tokens, in], w [out, in], of values
+ * held as e4m3 codes:
+ *   form            a                           b                       out
+ *   BL_MATMUL8_Y    x   scales of rows          w  scales of blocks     y   [tokens, out]
+ *   BL_MATMUL8_G_X  g_y scales of rows          w  scales of blocks     g_x [tokens, in]  = g_y w
+ *   BL_MATMUL8_G_W  g_y scales of columns       x  scales of columns    g_w [out, in]     = g_y^T x
+ * Scales are laid out as bl_tile8_save's, contiguous; codes have row strides.
+ * Products of codes are summed in fp32 over blocks of 128 of the summed dim, and
+ * the blocks' sums, times the product of their two scales, in fp32 in the blocks'
+ * order (in a few parts of it, each in order, where few tiles share a sum); the
+ * result is rounded once, to out_dtype.  The product of two scales is an fp32
+ * number: below 2^-126 it loses bits, beyond 2^128 it is infinite.  A block
+ * whose scale is NaN makes what it reaches NaN.  tokens = 0 gives g_w = 0.
+ * Where a code tensor's rows are not 16-byte aligned, the call copies it to the
+ * workspace first (bl_matmul8_workspace_bytes, which reads everything but `out`
+ * and the workspace; 16-byte aligned).  When a device-side wait gives up
+ * (bl_set_wait_limit), the tiles that it left are NaN.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED, BL_ERR_WORKSPACE, BL_ERR_CUDA. */
+typedef enum { BL_MATMUL8_Y = 0, BL_MATMUL8_G_X = 1, BL_MATMUL8_G_W = 2 } bl_matmul8_form;
+typedef struct {
+  int64_t tokens, out_features, in_features;
+  const void* a_codes;
+  const float* a_scales;
+  int64_t a_stride;
+  const void* b_codes;
+  const float* b_scales;
+  int64_t b_stride;
+  void* out;                 /* contiguous */
+  void* workspace;
+  size_t workspace_bytes;
+  int form, out_dtype;
+} bl_matmul8_args;
+size_t bl_matmul8_workspace_bytes(const bl_matmul8_args* args);
+bl_status bl_matmul8(const bl_matmul8_args* args, void* stream);
+
+/* Layer norm: h = x + residual (h = x without one), m = mean(h),
+ * rstd = 1 / sqrt(mean((h - m)^2) + eps), y = (h - m) rstd weight + bias, row by
+ * row.  Arguments as bl_rms_norm_fwd's; weight and bias [cols] have the same type,
+ * either may be NULL (ones, zeros); mean and rstd [rows] fp32 for the backward may
+ * be NULL.  The squares are summed of the centred row. */
+typedef struct {
+  int64_t rows, cols, x_stride, residual_stride;
+  const void* x;
+  const void* residual;
+  const void* weight;
+  const void* bias;
+  void* y;
+  void* h;
+  float* mean;
+  float* rstd;
+  const bl_act8* y8;
+  float eps;
+  int dtype, weight_dtype;
+} bl_layer_norm_args;
+bl_status bl_layer_norm_fwd(const bl_layer_norm_args* args, void* stream);
+
+/* Its gradients.  With u = (h - m) rstd and c = mean(weight g_y u):
+ *   g_x = rstd (weight g_y - mean(weight g_y) - u c) + g_h
+ *   g_w = sum over the rows of g_y u,  g_b = sum over the rows of g_y
+ * (in a fixed order: reproducible).  Arguments as bl_rms_norm_bwd's; g_w and g_b
+ * have weight_dtype, either may be NULL, and without both no workspace is needed. */
+size_t bl_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+typedef struct {
+  int64_t rows, cols;
+  const void* g_y;
+  const void* h;
+  const bl_act8* h8;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  const void* g_h;
+  void* g_x;
+  void* g_w;
+  void* g_b;
+  void* workspace;
+  size_t workspace_bytes;
+  int dtype, weight_dtype;
+} bl_layer_norm_bwd_args;
+bl_status bl_layer_norm_bwd(const bl_layer_norm_bwd_args* args, void* stream);
+
+/* Dropout: y = x / (1 - p) where an element is kept, else 0, plus the residual
+ * (may be NULL).  Element i = row * cols + col, whatever the strides, is kept iff
+ * word i mod 4 of Philox4x32-10 of the counter (i / 4, offset), two 64-bit numbers,
+ * lower words first, and the key `seed` is at least round(p * 2^32); with p = 1 none is.
+ *   state  {seed, offset}, two int64 on the device, read when the kernel runs
+ *   y      [rows, cols] of dtype, contiguous; may be x or residual where that is too
+ * What is dropped gives 0 whatever x is, infinities and NaN too.  The gradient is
+ * the same call on g_y, without a residual.  rows * cols up to 2^42. */
+bl_status bl_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t x_stride,
+                     const void* residual, int64_t residual_stride, double p,
+                     const int64_t* state, void* y, void* stream);
+
+/* used = state, and then state's offset one on: the generator's next call, in stream
+ * order, so that a captured graph draws anew with every replay.  Calls that share a
+ * state must not overlap. */
+bl_status bl_dropout_next(int64_t* state, int64_t* used, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Packed variable-length batches.
  *
  * nseq sequences of lengths n_s = cu_seqlens[s+1] - cu_seqlens[s] are packed
