@@ -8,9 +8,9 @@
 //
 // A CTA has a tile of 128 x BN.  Warp roles:
 //   warp 0      TMA producer: codes of A and B, 128 of the summed dim a stage.
-//   warp 1      MMA issuer (one thread), TMEM owner: a block's product into one of NB
-//               accumulators.
-//   warps 2, 3  scales of the tile's rows and columns into a ring of shared memory.
+//   warps 1, 2  MMA issuers (one thread each, turn by turn), warp 1 the TMEM's owner: a
+//               block's product into one of NB accumulators.
+//   warp 3      scales of the tile's rows and columns into a ring of shared memory.
 //   warps 4-    accumulate: a thread has a row of up to 128 columns of the tile in
 //               registers, reads the block's product from TMEM and adds it, scaled.
 // Either operand may have the summed dim contiguous (K-major) or the other one
@@ -33,33 +33,33 @@ using namespace tc;
 
 constexpr int kSMs = 152;
 
-template <int BN>
+template <int BN, bool COL>
 struct GCfg {
   static constexpr int NB = BN <= 64 ? 4 : 2;           // accumulators in TMEM
   static constexpr int COLS = NB * BN < 32 ? 32 : NB * BN;
-  static constexpr int EPI = BN == 256 ? 8 : 4;         // accumulating warps
+  static constexpr int EPI = BN != 256 ? 4 : COL ? 8 : 16; // accumulating warps
   static constexpr int THREADS = 128 + EPI * 32;
   static constexpr int CTAS = BN == 256 ? 1 : 2;        // on an SM
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+  static constexpr int GROUP = 16;           // see tile_at
   static constexpr int NSC = 8;                         // stages of scales
   static constexpr int SC_FLOATS = 128 + BN;
   static constexpr int SMEM = NS * STAGE + NSC * SC_FLOATS * 4 + 1024;
   static constexpr int PER = BN / (EPI / 4);            // columns of a thread
 };
 
-template <int BN>
+template <typename C>
 struct GBars {
-  using C = GCfg<BN>;
   uint64_t full[C::NS], empty[C::NS], t_full[C::NB], t_empty[C::NB], s_full[C::NSC],
       s_empty[C::NSC];
 };
 
-// kind::f8f6f4 with e4m3 A and B (formats 0), fp32 accumulate, M = 128.
-__device__ __forceinline__ uint32_t idesc_e4m3(int N, bool a_mn, bool b_mn) {
+// kind::f8f6f4 with e4m3 A and B (formats 0), fp32 accumulate.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -89,19 +89,143 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr, int rank) {
   return v;
 }
 
-// Tiles in groups of kGroup along i, j by j: a group's rows of A stay in L2 while B
+// A bounded wait, which also ends when another role has given up.  Reading the global
+// timer takes longer than most waits do, so it starts only behind a few looks, each of
+// which suspends the thread for a while.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                             const int* given_up) {
+  auto look = [&]() { return mbar_try(bar, parity); };
+  if (look()) return true;
+  if (limit_ns >= kSuspendHintNs)
+    for (int i = 0; i < 4; ++i)
+      if (look()) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    if (look()) return true;
+    if (*(const volatile int*)given_up || globaltimer() - t0 > limit_ns) return false;
+  }
+}
+
+__device__ __forceinline__ uint4 ld_cluster4(uint32_t addr, int rank) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+      " ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [a];\n}\n"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// 16 lanes x 32 columns: thread t gets, of group g of 8 columns, columns 2 (t % 4) and the
+// next of lane t / 4 in x[4 g], x[4 g + 1], and of lane t / 4 + 8 in x[4 g + 2], x[4 g + 3].
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+        "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+        "=r"(x[14]), "=r"(x[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&x)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+        "=r"(x[7])
+      : "r"(taddr));
+}
+
+// A warp's 32 rows x PER columns of the tile, pairs of columns.  With a scale a row and one
+// for all columns a thread has a row; with a scale a column too, four rows (r / 4 and 8, 16,
+// 24 on) of every fourth pair, so that it needs a quarter of the columns' scales: the
+// shared memory that a thread would read them from is what feeds the MMAs (8192^3: 1250
+// TFLOP/s with a row a thread).
+template <int PER, bool COL>
+struct Acc {
+  uint64_t v[PER / 2];
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int c = 0; c < PER / 2; ++c) v[c] = f2_pack(x, x);
+  }
+  // += the product in TMEM, scaled
+  __device__ __forceinline__ void add(uint32_t taddr, const float* sa, const float* sb, int lane) {
+    if constexpr (!COL) {
+      const float s = sa[lane] * sb[0];
+      const uint64_t ss = f2_pack(s, s);
+#pragma unroll
+      for (int c = 0; c < PER; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(taddr + c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          v[(c + e) / 2] = ffma2(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ss,
+                                 v[(c + e) / 2]);
+      }
+    } else {
+      constexpr int CH = PER < 32 ? 16 : 32;             // columns at a time
+      uint64_t rows[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float s = sa[(lane >> 2) + 8 * u];
+        rows[u] = f2_pack(s, s);
+      }
+#pragma unroll
+      for (int c = 0; c < PER; c += CH) {
+        uint64_t cols[CH / 8];
+#pragma unroll
+        for (int k = 0; k < CH / 8; ++k)
+          cols[k] = *reinterpret_cast<const uint64_t*>(sb + c + k * 8 + (lane & 3) * 2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[CH / 2];
+          if constexpr (CH == 32)
+            tmem_ld_16x32(taddr + ((uint32_t)(16 * h) << 16) + c, x);
+          else
+            tmem_ld_16x16(taddr + ((uint32_t)(16 * h) << 16) + c, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < CH / 8; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint64_t& to = v[(c / 8 + k) * 4 + 2 * h + u];
+              to = ffma2(f2_pack(__uint_as_float(x[4 * k + 2 * u]),
+                                 __uint_as_float(x[4 * k + 2 * u + 1])),
+                         fmul2(cols[k], rows[2 * h + u]), to);
+            }
+        }
+      }
+    }
+  }
+  // f(row, column, value, value of the next column) of the thread's pairs
+  template <typename F>
+  __device__ __forceinline__ void each(int lane, F&& f) const {
+#pragma unroll
+    for (int c = 0; c < PER / 2; ++c) {
+      float lo, hi;
+      f2_unpack(v[c], lo, hi);
+      if constexpr (COL)
+        f((lane >> 2) + 8 * (c & 3), (c >> 2) * 8 + (lane & 3) * 2, lo, hi);
+      else
+        f(lane, 2 * c, lo, hi);
+    }
+  }
+};
+
+// Tiles in groups of GROUP along i, j by j: a group's rows of A stay in L2 while B
 // passes by.
-constexpr int kGroup = 16;
+template <int GROUP>
 __device__ __forceinline__ void tile_at(int t, int ti, int tj, int& i, int& j) {
-  const int per = kGroup * tj, g = t / per, r = t - g * per;
-  const int h = min(kGroup, ti - g * kGroup);
+  const int per = GROUP * tj, g = t / per, r = t - g * per;
+  const int h = min(GROUP, ti - g * GROUP);
   j = r / h;
-  i = g * kGroup + (r - j * h);
+  i = g * GROUP + (r - j * h);
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row(T* p, const uint64_t* acc, int n, bool wide) {
-  if (wide && n >= 16) {
+__device__ __forceinline__ void store_row(T* p, const uint64_t* acc, int n) {
+  if (n >= 16) {
     float f[2][8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) f2_unpack(acc[c], f[c / 4][2 * (c % 4)], f[c / 4][2 * (c % 4) + 1]);
@@ -118,27 +242,25 @@ __device__ __forceinline__ void store_row(T* p, const uint64_t* acc, int n, bool
 
 // COL: every column has a scale of its own; else every 128 share one.
 template <int BN, bool COL, typename T>
-__global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
+__global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
     gemm8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  Gemm8 g, uint64_t wait_ns) {
-  using C = GCfg<BN>;
+  using C = GCfg<BN, COL>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   float* sc = reinterpret_cast<float*>(sm + C::NS * C::STAGE);
-  __shared__ __align__(8) GBars<BN> bars;
+  __shared__ __align__(8) GBars<C> bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail, s_loads;
-  __shared__ uint64_t s_wait;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ti = (g.m + 127) / 128, tj = (g.n + BN - 1) / BN, tiles = ti * tj;
   const int nkb = (g.k + 127) / 128;
   // with splits, a cluster shares a tile: each CTA has a part of the summed dim
-  const int rank = BN <= 128 ? blockIdx.x % g.splits : 0;
-  const int first = BN <= 128 ? blockIdx.x / g.splits : blockIdx.x;
-  const int step = BN <= 128 ? gridDim.x / g.splits : gridDim.x;
-  const int kb0 = BN <= 128 ? (int)((int64_t)nkb * rank / g.splits) : 0;
-  const int kb1 = BN <= 128 ? (int)((int64_t)nkb * (rank + 1) / g.splits) : nkb;
+  const int share = BN <= 128 ? g.splits : 1;
+  const int rank = blockIdx.x % share, first = blockIdx.x / share, step = gridDim.x / share;
+  const int kb0 = (int)((int64_t)nkb * rank / share);
+  const int kb1 = (int)((int64_t)nkb * (rank + 1) / share);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -150,12 +272,11 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
       mbar_init(&bars.t_empty[s], C::EPI);
     }
     for (int s = 0; s < C::NSC; ++s) {
-      mbar_init(&bars.s_full[s], 64);
+      mbar_init(&bars.s_full[s], 32);
       mbar_init(&bars.s_empty[s], C::EPI);
     }
     s_fail = 0;
     s_loads = 0;
-    s_wait = wait_ns;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&s_tmem, C::COLS);
@@ -164,15 +285,16 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
   fence_after_sync();
   const uint32_t tmem = s_tmem;
   auto wait = [&](uint64_t* bar, int use, int ring) {   // for the phase of use `use` of a slot
-    return mbar_wait_limited(bar, (use / ring) & 1, &s_wait);
+    return wait_bounded(saddr(bar), (use / ring) & 1, wait_ns, &s_fail);
   };
   auto failed = [&]() { return *(volatile int*)&s_fail != 0; };
   auto fail = [&]() { atomicOr(&s_fail, 1); };
 
-  // the accumulating warps need registers, the others few; the shares add up to the
-  // launch's (384 x 168, 256 x 128)
+  // The accumulating warps need registers, the others few; the shares stay within the
+  // launch's 640 x 96, 384 x 168 or 256 x 128.  (A share that makes the compiler spill a
+  // few registers costs a third of the rate: the spills land in the loop over the blocks.)
   if (warp < 4) {
-  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if constexpr (BN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
   if (warp == 0) {
     if (lane == 0) {
@@ -182,72 +304,74 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
       bool ok = true;
       for (int t = first; ok && t < tiles; t += step) {
         int i, j;
-        tile_at(t, ti, tj, i, j);
+        tile_at<C::GROUP>(t, ti, tj, i, j);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % C::NS;
-          ok = !failed() && (it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS));
+          ok = (it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS));
           if (!ok) break;
           uint8_t* a = sm + s * C::STAGE;
           mbar_expect_tx(&bars.full[s], C::STAGE);
-          tma_load_2d(a, &tm_a, &bars.full[s], g.a_mn ? i * 128 : kb * 128,
-                      g.a_mn ? kb * 128 : i * 128);
+          const int row = i * 128, col = j * BN;
+          tma_load_2d(a, &tm_a, &bars.full[s], g.a_mn ? row : kb * 128, g.a_mn ? kb * 128 : row);
 #pragma unroll
           for (int h = 0; h < (BN + 127) / 128; ++h)
             tma_load_2d(a + C::A_BYTES + h * 16384, &tm_b, &bars.full[s],
-                        g.b_mn ? j * BN + h * 128 : kb * 128, g.b_mn ? kb * 128 : j * BN + h * 128);
+                        g.b_mn ? col + h * 128 : kb * 128, g.b_mn ? kb * 128 : col + h * 128);
           s_loads = it + 1;
         }
       }
       if (!ok) fail();
     }
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
+    // Two issuers take turns: a look at a barrier behind MMAs returns only when those have
+    // been taken up, some 100 clocks in which one issuer alone would leave the tensor core
+    // idle (with two looks a block, 930 clocks a block of 512).
+    const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
     if (lane == 0) {
-      const uint32_t id = idesc_e4m3(BN, g.a_mn, g.b_mn);
+      const uint32_t id = idesc_e4m3(128, BN, g.a_mn, g.b_mn);
       const uint32_t step_a = g.a_mn ? 4096 : 32, step_b = g.b_mn ? 4096 : 32;
-      int it = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += step)
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % C::NS, b = it % C::NB;
-          ok = !failed() && (it < C::NB || wait(&bars.t_empty[b], it - C::NB, C::NB)) &&
-               wait(&bars.full[s], it, C::NS);
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t a = saddr(sm + s * C::STAGE);
+      int it = warp - 1;
+      for (; it < total; it += 2) {
+        const int s = it % C::NS, b = it % C::NB;
+        if (!((it < C::NB || wait(&bars.t_empty[b], it - C::NB, C::NB)) &&
+              wait(&bars.full[s], it, C::NS)))
+          break;
+        fence_after_sync();
+        const uint32_t a = saddr(sm + s * C::STAGE);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8(tmem + b * BN, sdesc_sw128(a + kk * step_a, 16384, 1024),
-                   sdesc_sw128(a + C::A_BYTES + kk * step_b, 16384, 1024), id, kk > 0);
-          mma_commit(&bars.empty[s]);
-          mma_commit(&bars.t_full[b]);
-        }
-      if (!ok) {
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8(tmem + b * BN, sdesc_sw128(a + kk * step_a, 16384, 1024),
+                       sdesc_sw128(a + C::A_BYTES + kk * step_b, 16384, 1024), id, kk > 0);
+        mma_commit(&bars.empty[s]);
+        mma_commit(&bars.t_full[b]);
+      }
+      if (it < total) {
         fail();
         // nothing may be in flight when the CTA ends: its MMAs, and then the copies
-        if (it > 0) mbar_wait_poll(&bars.t_full[(it - 1) % C::NB], ((it - 1) / C::NB) & 1);
+        if (it >= 2) mbar_wait_poll(&bars.t_full[(it - 2) % C::NB], ((it - 2) / C::NB) & 1);
       }
     }
   } else {
-    const int t0 = threadIdx.x - 64;
+    const int t0 = lane;
     int it = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
       int i, j;
-      tile_at(t, ti, tj, i, j);
+      tile_at<C::GROUP>(t, ti, tj, i, j);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const int s = it % C::NSC;
-        ok = __all_sync(0xffffffffu, !failed() && (it < C::NSC ||
-                                                   wait(&bars.s_empty[s], it - C::NSC, C::NSC)));
+        ok = __all_sync(0xffffffffu,
+                        it < C::NSC || wait(&bars.s_empty[s], it - C::NSC, C::NSC));
         if (!ok) break;
         float* a = sc + s * C::SC_FLOATS;
 #pragma unroll
-        for (int e = t0; e < 128; e += 64) {
+        for (int e = t0; e < 128; e += 32) {
           const int row = min(i * 128 + e, g.m - 1);
           copy_async<4>(a + e, g.sa + (int64_t)(row >> g.sa_shift) * g.sa_i + kb * g.sa_b);
         }
         if constexpr (COL) {
-#pragma unroll
-          for (int e = t0; e < BN; e += 64) {
+#pragma unroll 2
+          for (int e = t0; e < BN; e += 32) {
             const int col = min(j * BN + e, g.n - 1);
             copy_async<4>(a + 128 + e, g.sb + (int64_t)(col >> g.sb_shift) * g.sb_i + kb * g.sb_b);
           }
@@ -262,47 +386,26 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
-  if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  if constexpr (BN == 256 && !COL) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+  if constexpr (BN == 256 && COL) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
   if constexpr (BN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const int r = q * 32 + lane, c0 = half * C::PER;
+    const int q = warp & 3, c0 = ((warp - 4) >> 2) * C::PER;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + c0;
-    constexpr int CH = C::PER < 32 ? 16 : 32;            // columns at a time
     int it = 0;
     bool ok = true;
     for (int t = first; t < tiles; t += step) {
       int i, j;
-      tile_at(t, ti, tj, i, j);
-      uint64_t acc[C::PER / 2];
-#pragma unroll
-      for (int c = 0; c < C::PER / 2; ++c) acc[c] = 0;
+      tile_at<C::GROUP>(t, ti, tj, i, j);
+      Acc<C::PER, COL> acc;
+      acc.fill(0.f);
       for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
         const int b = it % C::NB, s = it % C::NSC;
-        ok = __all_sync(0xffffffffu, !failed() && wait(&bars.s_full[s], it, C::NSC) &&
-                                         wait(&bars.t_full[b], it, C::NB));
+        ok = __all_sync(0xffffffffu,
+                        wait(&bars.s_full[s], it, C::NSC) && wait(&bars.t_full[b], it, C::NB));
         if (!ok) break;
         fence_after_sync();
         const float* a = sc + s * C::SC_FLOATS;
-        const float sa = a[r];
-        const uint64_t one = COL ? 0 : f2_pack(sa * a[128 + half], sa * a[128 + half]);
-        const uint64_t sa2 = f2_pack(sa, sa);
-#pragma unroll
-        for (int c = 0; c < C::PER; c += CH) {
-          uint32_t x[CH];
-          if constexpr (CH == 32)
-            tmem_ld32(lanes + b * BN + c, x);
-          else
-            tmem_ld16(lanes + b * BN + c, x);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < CH; e += 2) {
-            const uint64_t p = f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            uint64_t w = one;
-            if constexpr (COL)
-              w = fmul2(*reinterpret_cast<const uint64_t*>(a + 128 + c0 + c + e), sa2);
-            acc[(c + e) / 2] = ffma2(p, w, acc[(c + e) / 2]);
-          }
-        }
+        acc.add(lanes + b * BN, a + q * 32, a + 128 + (COL ? c0 : c0 / 128), lane);
         fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -312,33 +415,52 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
       }
       if (!ok) {
         if (lane == 0) fail();
-#pragma unroll
-        for (int c = 0; c < C::PER / 2; ++c) acc[c] = f2_pack(NAN, NAN);
+        acc.fill(NAN);
       }
-      const int row = i * 128 + r, col = j * BN + c0;
+      const int row = i * 128 + q * 32, col = j * BN + c0;
       if (BN <= 128 && g.splits > 1) {
-        // the MMAs have read all stages: the ring holds the partial tile, [column][129]
-        float* part = reinterpret_cast<float*>(sm);
-#pragma unroll
-        for (int c = 0; c < C::PER; ++c) {
-          float lo, hi;
-          f2_unpack(acc[c / 2], lo, hi);
-          part[c * 129 + r] = c % 2 ? hi : lo;
+        // the MMAs have read all stages: the ring holds the partial tile, the result's
+        // contiguous dim along its rows
+        if (g.out_j == 1) {
+          float* part = reinterpret_cast<float*>(sm) + q * 32 * (BN + 4);
+          acc.each(lane, [&](int r, int c, float lo, float hi) {
+            *reinterpret_cast<float2*>(part + r * (BN + 4) + c) = make_float2(lo, hi);
+          });
+        } else {
+          float* part = reinterpret_cast<float*>(sm) + q * 32;
+          acc.each(lane, [&](int r, int c, float lo, float hi) {
+            part[c * 132 + r] = lo;
+            part[c * 132 + 132 + r] = hi;
+          });
         }
       } else if (g.out_j == 1) {
         T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + col;
-        if (row < g.m) {
+        const int n = g.n - col;
+        if (!COL && g.wide) {
+          if (row + lane < g.m) {
 #pragma unroll
-          for (int c = 0; c < C::PER; c += 16) store_row<T>(out + c, acc + c / 2, g.n - col - c, g.wide);
+            for (int c = 0; c < C::PER; c += 16)
+              store_row<T>(out + lane * g.out_i + c, acc.v + c / 2, n - c);
+          }
+        } else {
+          acc.each(lane, [&](int r, int c, float lo, float hi) {
+            if (row + r >= g.m) return;
+            T* p = out + r * g.out_i + c;
+            if (g.pairs && c + 1 < n) {
+              *reinterpret_cast<Pair<T>*>(p) = Pair<T>(lo, hi);
+            } else {
+              if (c < n) p[0] = from_f32<T>(lo);
+              if (c + 1 < n) p[1] = from_f32<T>(hi);
+            }
+          });
         }
       } else {
-        T* out = static_cast<T*>(g.out) + row;
-#pragma unroll
-        for (int c = 0; c < C::PER; ++c) {
-          float lo, hi;
-          f2_unpack(acc[c / 2], lo, hi);
-          if (row < g.m && col + c < g.n) out[(int64_t)(col + c) * g.out_j] = from_f32<T>(c % 2 ? hi : lo);
-        }
+        T* out = static_cast<T*>(g.out) + row + (int64_t)col * g.out_j;
+        acc.each(lane, [&](int r, int c, float lo, float hi) {
+          if (row + r >= g.m) return;
+          if (col + c < g.n) out[c * g.out_j + r] = from_f32<T>(lo);
+          if (col + c + 1 < g.n) out[(c + 1) * g.out_j + r] = from_f32<T>(hi);
+        });
       }
     }
   }
@@ -348,21 +470,37 @@ __global__ void __launch_bounds__(GCfg<BN>::THREADS, GCfg<BN>::CTAS)
       __syncthreads();
       cluster_sync_all();
       int i, j;
-      tile_at(first, ti, tj, i, j);
+      tile_at<C::GROUP>(first, ti, tj, i, j);
       const uint32_t part = saddr(sm);
       bool bad = false;
       for (int p = 0; p < g.splits; ++p) bad |= ld_cluster(saddr(&s_fail), p) != 0;
-      const int e0 = (int)((int64_t)128 * BN * rank / g.splits);
-      const int e1 = (int)((int64_t)128 * BN * (rank + 1) / g.splits);
+      // four neighbours of the result's contiguous dim at a time, all ranks' under way at
+      // once (one by one, a sum of 7 ranks at 128 x 5120 x 5120 took 60 us)
+      const bool rows = g.out_j == 1;
+      const int wide = rows ? BN : 128, pitch = wide + 4, quads = 128 * BN / 4;
+      const int e0 = quads * rank / g.splits, e1 = quads * (rank + 1) / g.splits;
       for (int e = e0 + threadIdx.x; e < e1; e += C::THREADS) {
-        const int r = g.out_j == 1 ? e / BN : e & 127, c = g.out_j == 1 ? e % BN : e >> 7;
-        const int row = i * 128 + r, col = j * BN + c;
+        const int x = e * 4 / wide, y = e * 4 - x * wide;    // y: along the contiguous dim
+        const int row = i * 128 + (rows ? x : y), col = j * BN + (rows ? y : x);
         if (row >= g.m || col >= g.n) continue;
-        float v = 0.f;
-        for (int p = 0; p < g.splits; ++p)
-          v += __uint_as_float(ld_cluster(part + (c * 129 + r) * 4, p));
-        if (bad) v = NAN;
-        static_cast<T*>(g.out)[(int64_t)row * g.out_i + (int64_t)col * g.out_j] = from_f32<T>(v);
+        uint4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < g.splits) v[p] = ld_cluster4(part + (x * pitch + y) * 4, p);
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < g.splits) {
+            f[0] += __uint_as_float(v[p].x);
+            f[1] += __uint_as_float(v[p].y);
+            f[2] += __uint_as_float(v[p].z);
+            f[3] += __uint_as_float(v[p].w);
+          }
+        T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + (int64_t)col * g.out_j;
+        const int left = rows ? g.n - col : g.m - row;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u < left) out[u] = from_f32<T>(bad ? NAN : f[u]);
       }
       cluster_sync_all();
     }
@@ -392,9 +530,9 @@ cudaError_t allow(int bytes) {
 
 template <int BN, bool COL, typename T>
 cudaError_t launch(const Gemm8& g, cudaStream_t st) {
-  using C = GCfg<BN>;
+  using C = GCfg<BN, COL>;
   CUtensorMap ta, tb;
-  const int box_b = g.b_mn ? 128 : BN < 128 ? BN : 128;
+  const int box_b = g.b_mn || BN > 128 ? 128 : BN;
   if (!make_codes_map(&ta, g.a, g.a_mn ? g.m : g.k, g.a_mn ? g.k : g.m, g.a_pitch, 128) ||
       !make_codes_map(&tb, g.b, g.b_mn ? g.n : g.k, g.b_mn ? g.k : g.n, g.b_pitch, box_b))
     return cudaErrorInvalidValue;
@@ -403,19 +541,20 @@ cudaError_t launch(const Gemm8& g, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + BN - 1) / BN);
   const int64_t most = kSMs * C::CTAS;
+  const int share = g.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * g.splits : tiles < most ? tiles : most));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  if (g.splits > 1) {
+  if (share > 1) {
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = g.splits;
+    at[0].val.clusterDim.x = share;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
+  cfg.gridDim = dim3((unsigned)((g.splits > 1 || tiles < most ? tiles : most) * share));
   return cudaLaunchKernelEx(&cfg, k, ta, tb, g, wait_limit_ns());
 }
 
@@ -437,6 +576,7 @@ cudaError_t run(const Gemm8& in, cudaStream_t st) {
   Gemm8 g = in;
   const int nkb = (g.k + 127) / 128;
   g.wide = g.out_j == 1 && aligned_to(g.out, 32) && g.out_i * (int64_t)sizeof(T) % 32 == 0;
+  g.pairs = g.out_j == 1 && aligned_to(g.out, 2 * sizeof(T)) && g.out_i % 2 == 0;
   // few rows: they become the columns of narrow tiles, and clusters share the summed dim
   const bool few = g.m <= 64 && !g.a_mn;
   const int64_t big = (int64_t)((g.m + 127) / 128) * ((g.n + 255) / 256);
