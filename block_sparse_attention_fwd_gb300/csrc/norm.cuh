@@ -138,8 +138,8 @@ __device__ __forceinline__ bool lane_behind(const Rows<LPR>& R) {
   return LPR ? R.t < LPR - 1 : (threadIdx.x & 31) < 31;
 }
 
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v, float (*buf)[32], int& slot) {
+template <int LPR, int N>
+__device__ __forceinline__ float row_sum(float v, float (*buf)[N], int& slot) {
   if constexpr (LPR != 0) return lanes_sum(v, LPR);
   v = block_sum(v, buf, slot);
   slot ^= 1;
@@ -208,6 +208,20 @@ inline unsigned grid(int64_t rows, int here, int most) {
   return (unsigned)(blocks < most ? blocks : most);
 }
 
+// Blocks of the forward's ring kernel.  One block for each that is resident runs them all
+// in step: the reads of all blocks and then their writes come in bursts.  Eight
+// times as many, as far as a block keeps about six rows, take turns out of step and
+// work on neighbouring rows: 5120 columns 84 -> 99% of the copy rate without and
+// 90 -> 101% with a residual, 128 columns 83 -> 96%; blocks of fewer rows lose it
+// again to filling their rings (4096 rows of 4096: 87 -> 70% at eight times).
+inline int fwd_blocks(int64_t rows, const Plan& p, int regs, size_t smem) {
+  const int once = resident(p.threads, regs, smem);
+  int64_t times = rows / ((int64_t)once * p.here * 6);
+  if (times > 8) times = 8;
+  if (times < 1) times = 1;
+  return (int)(once * times);
+}
+
 // The ring kernels for rows that start anywhere (norm_fwd_odd.cu: 16-bit types;
 // norm_bwd_odd.cu: those, and fp32 that a block holds, without 8 bits);
 // cudaErrorNotSupported for others and where a row is too wide.
@@ -215,6 +229,12 @@ cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st);
 cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 // The layer norm's.
 cudaError_t layer_fwd_odd(int dtype, const NormFwd& a, cudaStream_t st);
+// The layer norm's forward, two rows at a time (layer_norm_pairs.cu), where it takes the
+// rows: whole aligned chunks, held by a block with two chunks a thread at most, and no
+// scale a row.
+cudaError_t layer_fwd_pairs(int dtype, const NormFwd& a, cudaStream_t st);
+// Its backward on such rows (layer_norm_bwd_rows.cu).
+cudaError_t layer_bwd_rows(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 cudaError_t layer_bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 
 // Calls f(lanes a row, chunks a thread) as compile-time constants.

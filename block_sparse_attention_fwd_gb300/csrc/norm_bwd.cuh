@@ -482,8 +482,11 @@ __global__ void __launch_bounds__(1024) norm_gw_kernel(const float* __restrict__
 
 template <typename T, int FMT, bool LN>
 cudaError_t bwd(int dtype, const NormBwd& a, bool vec, int* blocks, cudaStream_t st) {
-  cudaError_t e =
-      vec  ? bwd_ring<T, FMT, false, LN>(a, blocks, st)
+  cudaError_t e = cudaErrorNotSupported;
+  if constexpr (LN)
+    if (vec) e = layer_bwd_rows(dtype, a, blocks, st);
+  if (e != cudaErrorNotSupported) return e;
+  e = vec  ? bwd_ring<T, FMT, false, LN>(a, blocks, st)
       : LN ? layer_bwd_odd(dtype, a, blocks, st)
            : bwd_odd(dtype, a, blocks, st);
   if (e != cudaErrorNotSupported) return e;
@@ -508,6 +511,10 @@ template <bool LN>
 int bwd_parts_of(int64_t rows, int64_t cols) {
   // of either way to lay out the rows
   int most = 0;
+  if (LN) {                                              // layer_bwd_rows
+    const Plan p = plan(cols, 512, 96);
+    if (!p.lpr) most = (int)grid(rows, 1, resident(p.threads, p.nv == 1 ? 72 : 96, 0));
+  }
   for (bool odd : {false, true}) {
     const Plan p = plan(cols, 512, 96, odd);
     const int blocks =

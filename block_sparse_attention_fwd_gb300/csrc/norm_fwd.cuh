@@ -9,6 +9,14 @@ using namespace norm;
 
 namespace {
 
+// Threads of a block that holds a row, at most.  The layer norm, which keeps the bias too,
+// needs more than the 64 registers that 1024 threads leave each.
+constexpr int fwd_threads(bool layer) { return layer ? 512 : 1024; }
+// Registers a thread (the launch counts on them).
+constexpr int fwd_regs(bool layer, bool norm, int nv) {
+  return !layer ? (norm ? 64 : 48) : nv == 1 ? 64 : nv == 2 ? 88 : 128;
+}
+
 // The same for rows whose chunks are whole and aligned: a block takes rows
 // gridDim.x apart, and x and r of the next S - 1 of them are on their way to
 // shared memory meanwhile, each thread's chunks into places of its own.  Loading
@@ -17,17 +25,17 @@ namespace {
 // (6.8 TB/s), with the residual to e4m3 in 175 us (6.7 TB/s; issue slots are 74%
 // busy there).  FMT8: 0 without the 8-bit output, else its format.  NORM = false
 // only saves x in 8 bits: the same walk without the norm.  LN: the layer norm, whose
-// squares are summed of the centred row, which is a second reduction.
+// squares are summed of centred elements.
 // ODD: rows of a 16-bit type that start anywhere.  Their aligned vectors go to
 // the ring, and a chunk is shifted out of its own and the next thread's vector:
 // one barrier more, and some 40 instructions a chunk and tensor (2561 columns: 23%
 // of the copy rate element by element, 50% so, 63% with a residual).
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd a) {
+__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
   static_assert(NORM || !LN);
-  __shared__ float buf[2][32];
+  __shared__ float buf[2][LN ? 64 : 32];
   extern __shared__ __align__(16) uint8_t ring[];
   const Rows<LPR> R;
   const int cols = (int)a.cols;
@@ -83,6 +91,12 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
       const int col = (R.t + k * R.step) * 8;
       float f[8];
       load_weight8<T, !ODD>(a.w, a.w_f32, col, cols - col, f);
+      if constexpr (LN) {
+        // y is 0 behind the row, where it has no part in a group's largest value
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i >= cols - col) f[i] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[k][i] = f2_pack(f[2 * i], f[2 * i + 1]);
       if constexpr (LN) {
@@ -90,6 +104,26 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[k][i] = f2_pack(f[2 * i], f[2 * i + 1]);
       }
+    }
+  }
+  // LN: one over the elements of a row that the thread's warp holds, and those of the
+  // warp whose number is the thread's lane
+  float inv_part = inv_cols, inv_lane = 0.f, n_lane = 0.f;
+  if constexpr (LN && LPR == 0) {
+    auto held = [&](int warp) {
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int left = cols - (warp * 32 + k * R.step) * 8;
+        n += left < 0 ? 0 : left < 256 ? left : 256;
+      }
+      return n;
+    };
+    const int mine_n = held(threadIdx.x >> 5), lane_n = held(threadIdx.x & 31);
+    inv_part = mine_n ? 1.f / (float)mine_n : 0.f;
+    if ((threadIdx.x & 31) < (blockDim.x >> 5)) {
+      n_lane = (float)lane_n;
+      inv_lane = lane_n ? 1.f / n_lane : 0.f;
     }
   }
   int slot = 0, now = 0, fill = S - 1;
@@ -155,41 +189,62 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
     if constexpr (NORM) {
       float s0, s1;
       f2_unpack(ss, s0, s1);
-      float sum = row_sum<LPR>(s0 + s1, buf, slot);
-      if constexpr (LN) {
-        const float mean = sum * inv_cols;
-        if (R.t == 0 && in && a.mean) a.mean[row] = mean;
-        const uint64_t mm = f2_pack(-mean, -mean);
+      float sum = s0 + s1, mean = 0.f;
+      if constexpr (!LN) {
+        sum = row_sum<LPR>(sum, buf, slot);
+      } else {
+        // the squares around the mean of the elements that the warp's lanes (LPR of them)
+        // hold; over the block the parts' means are put right, so one barrier does
+        constexpr int W = LPR ? LPR : 32;
+        sum = lanes_sum(sum, W);
+        mean = sum * inv_part;
         ss = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           const int valid = in ? cols - (R.t + k * R.step) * 8 : 0;
-          if (valid <= 0) continue;                  // h stays 0 there
+          const float off = valid > 0 ? -mean : 0.f;     // h is 0 where there is no chunk
+          const uint64_t mm = f2_pack(off, off);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[k][i] = fadd2(h[k][i], mm);
-          if constexpr (ODD) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4; ++i) {
+            uint64_t d = fadd2(h[k][i], mm);
+            if constexpr (ODD) {
               float lo, hi;
-              f2_unpack(h[k][i], lo, hi);
-              h[k][i] = f2_pack(2 * i < valid ? lo : 0.f, 2 * i + 1 < valid ? hi : 0.f);
+              f2_unpack(d, lo, hi);
+              d = f2_pack(2 * i < valid ? lo : 0.f, 2 * i + 1 < valid ? hi : 0.f);
             }
+            ss = ffma2(d, d, ss);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ss = ffma2(h[k][i], h[k][i], ss);
         }
         f2_unpack(ss, s0, s1);
-        sum = row_sum<LPR>(s0 + s1, buf, slot);
+        float squares = lanes_sum(s0 + s1, W);
+        if constexpr (LPR == 0) {
+          const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+          if (lane == 0) {
+            buf[slot][warp] = sum;
+            buf[slot][32 + warp] = squares;
+          }
+          __syncthreads();
+          const float part = lane < warps ? buf[slot][lane] : 0.f;
+          squares = lane < warps ? buf[slot][32 + lane] : 0.f;
+          mean = lanes_sum(part, 32) * inv_cols;
+          const float off = part * inv_lane - mean;      // of the mean of warp `lane`
+          squares = lanes_sum(fmaf(off * off, n_lane, squares), 32);
+          slot ^= 1;
+        }
+        sum = squares;
+        if (R.t == 0 && in && a.mean) a.mean[row] = mean;
       }
       const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
       if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
       const uint64_t rr = f2_pack(rstd, rstd);
+      const float base = -mean * rstd;                   // rounded like the mean itself
+      const uint64_t bb = f2_pack(base, base);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const bool has = in && (R.t + k * R.step) * 8 < cols;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          h[k][i] = LN ? ffma2(fmul2(h[k][i], rr), w[k][i], b[LN ? k : 0][i])
+          h[k][i] = LN ? ffma2(ffma2(h[k][i], rr, bb), w[k][i], b[LN ? k : 0][i])
                        : fmul2(fmul2(h[k][i], rr), w[k][i]);
         if (a.y) write(a.y, k, h[k], has);
       }
@@ -236,29 +291,15 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_ring_kernel(NormFwd
   }
 }
 
-// Blocks of the ring kernel.  One block for each that is resident runs them all
-// in step: the reads of all blocks and then their writes come in bursts.  Eight
-// times as many, as far as a block keeps about six rows, take turns out of step and
-// work on neighbouring rows: 5120 columns 84 -> 99% of the copy rate without and
-// 90 -> 101% with a residual, 128 columns 83 -> 96%; blocks of fewer rows lose it
-// again to filling their rings (4096 rows of 4096: 87 -> 70% at eight times).
-int fwd_blocks(int64_t rows, const Plan& p, int regs, size_t smem) {
-  const int once = resident(p.threads, regs, smem);
-  int64_t times = rows / ((int64_t)once * p.here * 6);
-  if (times > 8) times = 8;
-  if (times < 1) times = 1;
-  return (int)(once * times);
-}
-
 // Launches the ring kernel on rows that it takes, else cudaErrorNotSupported.
 template <typename T, int FMT8, bool NORM, bool ODD, bool LN>
 cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
-  const Plan p = plan(a.cols, 1024, 64, ODD);
+  const Plan p = plan(a.cols, fwd_threads(LN), 64, ODD);
   cudaError_t e = cudaErrorNotSupported;
-  if (p.threads > 1024) return e;
+  if (p.threads > fwd_threads(LN)) return e;
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    if constexpr (N <= 2) {
+    if constexpr (N <= 2 || (LN && L == 0)) {
       const size_t stage = (size_t)N * p.threads * (NORM ? 2 : 1) * sizeof(Chunk<T>);
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
@@ -266,7 +307,7 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
         const size_t smem = S * stage;
         e = allow_smem<k>();
         if (e != cudaSuccess) return;
-        k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, LN ? 80 : NORM ? 64 : 48, smem)), p.threads, smem,
+        k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, fwd_regs(LN, NORM, N), smem)), p.threads, smem,
             st>>>(a);
         e = cudaGetLastError();
       };
@@ -274,7 +315,7 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
       if (L != 0 || N == 1 || MOST * stage <= kMaxSmem / 2)
         ring(Int<MOST>());
       else if (2 * stage <= kMaxSmem)
-        ring(Int<L == 0 && N == 2 ? 2 : MOST>());
+        ring(Int<L == 0 && N >= 2 ? 2 : MOST>());
     }
   });
   return e;
@@ -285,7 +326,7 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
 // columns.  OUT8: with the 8-bit output, whose
 // groups are neighbours, so those rows keep to chunks.
 template <typename T, int LPR, int NV, bool VEC, bool OUT8, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_kernel(NormFwd a) {
   __shared__ float buf[2][32];
   constexpr bool SPREAD = !VEC && !OUT8;
   const Rows<LPR> R;
@@ -393,16 +434,21 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) norm_fwd_kernel(NormFwd a) {
 
 template <typename T, int FMT8, bool LN>
 cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
-  cudaError_t e = vec  ? fwd_ring<T, FMT8, true, false, LN>(a, st)
+  cudaError_t e = cudaErrorNotSupported;
+  if constexpr (LN)
+    if (vec) e = layer_fwd_pairs(dtype, a, st);
+  if (e != cudaErrorNotSupported) return e;
+  e = vec  ? fwd_ring<T, FMT8, true, false, LN>(a, st)
                   : LN ? layer_fwd_odd(dtype, a, st)
                        : fwd_odd(dtype, true, a, st);
   if (e != cudaErrorNotSupported) return e;
-  const Plan p = plan(a.cols, 1024, 64);
+  const Plan p = plan(a.cols, fwd_threads(LN), 64);
   const unsigned g = grid(a.rows, p.here, kSMs * 32);
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    if constexpr (N <= 2 && (sizeof(T) == 4 || (L == 0 && N == 2))) {
-      constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == 2;     // too wide for the ring
+    constexpr int MOST = LN ? 4 : 2;                  // chunks a thread of the widest rows
+    if constexpr (N <= (L ? 2 : MOST) && (sizeof(T) == 4 || (L == 0 && N == MOST))) {
+      constexpr bool WIDE = sizeof(T) == 4 && L == 0 && N == MOST;  // too wide for the ring
       if (vec && WIDE)
         norm_fwd_kernel<T, L, N, WIDE, FMT8 != 0, LN><<<g, p.threads, 0, st>>>(a);
       else

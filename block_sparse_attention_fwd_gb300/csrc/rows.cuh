@@ -303,14 +303,16 @@ __device__ __forceinline__ float lanes_sum(float v, int width) {
 // slots of `buf`, which the caller alternates, so that one barrier a reduction
 // is enough: a slot is written again only after the barrier of the reduction
 // in between.  Every thread gets the result, formed in the same order.
-__device__ __forceinline__ float block_sum(float v, float (*buf)[32], int slot) {
+template <int N>
+__device__ __forceinline__ float block_sum(float v, float (*buf)[N], int slot) {
   v = lanes_sum(v, 32);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) buf[slot][warp] = v;
   __syncthreads();
   return lanes_sum(lane < warps ? buf[slot][lane] : 0.f, 32);
 }
-__device__ __forceinline__ float block_amax(float v, float (*buf)[32], int slot) {
+template <int N>
+__device__ __forceinline__ float block_amax(float v, float (*buf)[N], int slot) {
   v = lanes_amax(v, 32);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) buf[slot][warp] = v;
