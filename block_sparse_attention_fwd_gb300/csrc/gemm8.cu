@@ -32,18 +32,24 @@ namespace {
 using namespace tc;
 
 constexpr int kSMs = 152;
+constexpr int kMostSplits = 4;     // CTAs that share a tile's sum
 
 template <int BN, bool COL>
 struct GCfg {
-  static constexpr int NB = BN <= 64 ? 4 : 2;           // accumulators in TMEM
+  static constexpr int NB = BN == 256 ? 2 : 4;          // accumulators in TMEM
   static constexpr int COLS = NB * BN < 32 ? 32 : NB * BN;
-  static constexpr int EPI = BN != 256 ? 4 : COL ? 8 : 16; // accumulating warps
-  static constexpr int THREADS = 128 + EPI * 32;
-  static constexpr int CTAS = BN == 256 ? 1 : 2;        // on an SM
+  static constexpr int ISSUERS = BN == 256 ? 2 : 4;
+  static constexpr int PRE = 2 + ISSUERS;               // warps in front of the accumulating ones
+#ifndef CEPI
+#define CEPI 8
+#endif
+  static constexpr int EPI = BN == 256 ? (COL ? CEPI : 16) : BN >= 64 ? 8 : 4;
+  static constexpr int THREADS = (PRE + EPI) * 32;
+  static constexpr int CTAS = BN >= 64 ? 1 : 2;         // on an SM
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
-  static constexpr int GROUP = 16;           // see tile_at
+  static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : 5;
+  static constexpr int GROUP = 16;                      // see tile_at
   static constexpr int NSC = 8;                         // stages of scales
   static constexpr int SC_FLOATS = 128 + BN;
   static constexpr int SMEM = NS * STAGE + NSC * SC_FLOATS * 4 + 1024;
@@ -262,6 +268,17 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   const int kb0 = (int)((int64_t)nkb * rank / share);
   const int kb1 = (int)((int64_t)nkb * (rank + 1) / share);
 
+  // a stage of the summed dim's block kb of tile (i, j)
+  auto load = [&](int s, int i, int j, int kb) {
+    uint8_t* a = sm + s * C::STAGE;
+    mbar_expect_tx(&bars.full[s], C::STAGE);
+    const int row = i * 128, col = j * BN;
+    tma_load_2d(a, &tm_a, &bars.full[s], g.a_mn ? row : kb * 128, g.a_mn ? kb * 128 : row);
+#pragma unroll
+    for (int h = 0; h < (BN + 127) / 128; ++h)
+      tma_load_2d(a + C::A_BYTES + h * 16384, &tm_b, &bars.full[s],
+                  g.b_mn ? col + h * 128 : kb * 128, g.b_mn ? kb * 128 : col + h * 128);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&bars.full[s], 1);
@@ -278,6 +295,12 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
     s_fail = 0;
     s_loads = 0;
     fence_mbar_init();
+    // the first stages are on their way while the rest of the CTA gets ready
+    prefetch_tmap(&tm_a);
+    prefetch_tmap(&tm_b);
+    int i, j;
+    tile_at<C::GROUP>(first, ti, tj, i, j);
+    for (int s = 0; s < C::NS && first < tiles && kb0 + s < kb1; ++s) load(s, i, j, kb0 + s);
   }
   if (warp == 1) tmem_alloc(&s_tmem, C::COLS);
   fence_before_sync();
@@ -291,39 +314,31 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   auto fail = [&]() { atomicOr(&s_fail, 1); };
 
   // The accumulating warps need registers, the others few; the shares stay within the
-  // launch's 640 x 96, 384 x 168 or 256 x 128.  (A share that makes the compiler spill a
+  // launch's 640 x 96 or 384 x 168.  (A share that makes the compiler spill a
   // few registers costs a third of the rate: the spills land in the loop over the blocks.)
-  if (warp < 4) {
-  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if constexpr (BN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+  if (warp < C::PRE) {
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tmap(&tm_a);
-      prefetch_tmap(&tm_b);
       int it = 0;
       bool ok = true;
+      s_loads = min(C::NS, first < tiles ? kb1 - kb0 : 0);
       for (int t = first; ok && t < tiles; t += step) {
         int i, j;
         tile_at<C::GROUP>(t, ti, tj, i, j);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          if (t == first && kb - kb0 < C::NS) continue;  // on their way
           const int s = it % C::NS;
-          ok = (it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS));
+          ok = it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS);
           if (!ok) break;
-          uint8_t* a = sm + s * C::STAGE;
-          mbar_expect_tx(&bars.full[s], C::STAGE);
-          const int row = i * 128, col = j * BN;
-          tma_load_2d(a, &tm_a, &bars.full[s], g.a_mn ? row : kb * 128, g.a_mn ? kb * 128 : row);
-#pragma unroll
-          for (int h = 0; h < (BN + 127) / 128; ++h)
-            tma_load_2d(a + C::A_BYTES + h * 16384, &tm_b, &bars.full[s],
-                        g.b_mn ? col + h * 128 : kb * 128, g.b_mn ? kb * 128 : col + h * 128);
+          load(s, i, j, kb);
           s_loads = it + 1;
         }
       }
       if (!ok) fail();
     }
-  } else if (warp <= 2) {
-    // Two issuers take turns: a look at a barrier behind MMAs returns only when those have
+  } else if (warp <= C::ISSUERS) {
+    // The issuers take turns: a look at a barrier behind MMAs returns only when those have
     // been taken up, some 100 clocks in which one issuer alone would leave the tensor core
     // idle (with two looks a block, 930 clocks a block of 512).
     const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
       const uint32_t id = idesc_e4m3(128, BN, g.a_mn, g.b_mn);
       const uint32_t step_a = g.a_mn ? 4096 : 32, step_b = g.b_mn ? 4096 : 32;
       int it = warp - 1;
-      for (; it < total; it += 2) {
+      for (; it < total; it += C::ISSUERS) {
         const int s = it % C::NS, b = it % C::NB;
         if (!((it < C::NB || wait(&bars.t_empty[b], it - C::NB, C::NB)) &&
               wait(&bars.full[s], it, C::NS)))
@@ -348,7 +363,8 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
       if (it < total) {
         fail();
         // nothing may be in flight when the CTA ends: its MMAs, and then the copies
-        if (it >= 2) mbar_wait_poll(&bars.t_full[(it - 2) % C::NB], ((it - 2) / C::NB) & 1);
+        const int last = it - C::ISSUERS;
+        if (last >= 0) mbar_wait_poll(&bars.t_full[last % C::NB], (last / C::NB) & 1);
       }
     }
   } else {
@@ -386,10 +402,9 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
-  if constexpr (BN == 256 && !COL) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-  if constexpr (BN == 256 && COL) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-  if constexpr (BN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int q = warp & 3, c0 = ((warp - 4) >> 2) * C::PER;
+    if constexpr (BN == 256 && C::EPI == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int q = warp & 3, c0 = ((warp - C::PRE) >> 2) * C::PER;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + c0;
     int it = 0;
     bool ok = true;
@@ -477,30 +492,43 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
       // four neighbours of the result's contiguous dim at a time, all ranks' under way at
       // once (one by one, a sum of 7 ranks at 128 x 5120 x 5120 took 60 us)
       const bool rows = g.out_j == 1;
-      const int wide = rows ? BN : 128, pitch = wide + 4, quads = 128 * BN / 4;
+      const int wide = rows ? BN : 128, pitch = wide + 4, quads = 128 * BN / 4;   // x: along the other
       const int e0 = quads * rank / g.splits, e1 = quads * (rank + 1) / g.splits;
-      for (int e = e0 + threadIdx.x; e < e1; e += C::THREADS) {
-        const int x = e * 4 / wide, y = e * 4 - x * wide;    // y: along the contiguous dim
-        const int row = i * 128 + (rows ? x : y), col = j * BN + (rows ? y : x);
-        if (row >= g.m || col >= g.n) continue;
-        uint4 v[8];
+      for (int e = e0 + threadIdx.x; e < e1; e += 2 * C::THREADS) {
+        uint4 v[2][kMostSplits];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-          if (p < g.splits) v[p] = ld_cluster4(part + (x * pitch + y) * 4, p);
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < 2; ++u) {
+          const int eu = e + u * C::THREADS, x = eu * 4 / wide, y = eu * 4 - x * wide;
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-          if (p < g.splits) {
-            f[0] += __uint_as_float(v[p].x);
-            f[1] += __uint_as_float(v[p].y);
-            f[2] += __uint_as_float(v[p].z);
-            f[3] += __uint_as_float(v[p].w);
+          for (int p = 0; p < kMostSplits; ++p)
+            if (p < g.splits && eu < e1) v[u][p] = ld_cluster4(part + (x * pitch + y) * 4, p);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int eu = e + u * C::THREADS, x = eu * 4 / wide, y = eu * 4 - x * wide;
+          const int row = i * 128 + (rows ? x : y), col = j * BN + (rows ? y : x);
+          if (eu >= e1 || row >= g.m || col >= g.n) continue;
+          float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = 0; p < kMostSplits; ++p)
+            if (p < g.splits) {
+              f[0] += __uint_as_float(v[u][p].x);
+              f[1] += __uint_as_float(v[u][p].y);
+              f[2] += __uint_as_float(v[u][p].z);
+              f[3] += __uint_as_float(v[u][p].w);
+            }
+          T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + (int64_t)col * g.out_j;
+          const int left = rows ? g.n - col : g.m - row;
+          if (g.quads && left >= 4) {
+            if (bad) f[0] = f[1] = f[2] = f[3] = NAN;
+            reinterpret_cast<Pair<T>*>(out)[0] = Pair<T>(f[0], f[1]);
+            reinterpret_cast<Pair<T>*>(out)[1] = Pair<T>(f[2], f[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < left) out[k] = from_f32<T>(bad ? NAN : f[k]);
           }
-        T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + (int64_t)col * g.out_j;
-        const int left = rows ? g.n - col : g.m - row;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u < left) out[u] = from_f32<T>(bad ? NAN : f[u]);
+        }
       }
       cluster_sync_all();
     }
@@ -531,6 +559,8 @@ cudaError_t allow(int bytes) {
 template <int BN, bool COL, typename T>
 cudaError_t launch(const Gemm8& g, cudaStream_t st) {
   using C = GCfg<BN, COL>;
+  // rows of B that lie across the summed dim come 128 columns at a time
+  if (BN < 128 && g.b_mn) return cudaErrorInvalidValue;
   CUtensorMap ta, tb;
   const int box_b = g.b_mn || BN > 128 ? 128 : BN;
   if (!make_codes_map(&ta, g.a, g.a_mn ? g.m : g.k, g.a_mn ? g.k : g.m, g.a_pitch, 128) ||
@@ -571,28 +601,51 @@ Gemm8 swapped(const Gemm8& g) {
   return s;
 }
 
+// Which tile, by an estimate of the time in us.  Measured for a block of 128 of the summed
+// dim: 0.48 us in tiles of 128 x 256, ... (see the constants); a launch takes some 4 us, a sum over a
+// cluster kSum more.
+struct Choice {
+  int bn, splits;
+  float us;
+};
+void consider(Choice& best, const Gemm8& g, int bn, int ctas, float block_us, float tile_us) {
+  const int nkb = (g.k + 127) / 128;
+  const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + bn - 1) / bn);
+  const int64_t at_once = (int64_t)kSMs * ctas;
+  for (int splits = 1; splits <= (bn == 256 ? 1 : kMostSplits); splits *= 2) {
+    if (splits > 1 && (splits > nkb || tiles * splits > at_once)) break;
+    const int64_t rounds = (tiles * splits + at_once - 1) / at_once;
+    const int blocks = (nkb + splits - 1) / splits;
+    const float us = rounds * (blocks * block_us + tile_us) + (splits > 1 ? 1.5f + bn / 64.f : 0.f);
+    if (us < best.us) best = Choice{bn, splits, us};
+  }
+}
+
 template <typename T>
 cudaError_t run(const Gemm8& in, cudaStream_t st) {
   Gemm8 g = in;
-  const int nkb = (g.k + 127) / 128;
-  g.wide = g.out_j == 1 && aligned_to(g.out, 32) && g.out_i * (int64_t)sizeof(T) % 32 == 0;
-  g.pairs = g.out_j == 1 && aligned_to(g.out, 2 * sizeof(T)) && g.out_i % 2 == 0;
-  // few rows: they become the columns of narrow tiles, and clusters share the summed dim
+  // few rows become the columns of narrow tiles
   const bool few = g.m <= 64 && !g.a_mn;
-  const int64_t big = (int64_t)((g.m + 127) / 128) * ((g.n + 255) / 256);
-  g.splits = 1;
-  if (!few && big >= kSMs)
-    return g.sb_shift == 7 ? launch<256, false, T>(g, st) : launch<256, true, T>(g, st);
-  const int bn = !few ? 128 : g.m <= 16 ? 16 : g.m <= 32 ? 32 : 64;
   if (few) g = swapped(g);
-  const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + bn - 1) / bn);
-  int64_t splits = 2 * kSMs / tiles;
-  if (splits > 8) splits = 8;
-  if (splits > nkb / 2) splits = nkb / 2;
-  if (splits > 1) g.splits = (int)splits;
-  if (bn == 128) return g.sb_shift == 7 ? launch<128, false, T>(g, st) : launch<128, true, T>(g, st);
-  if (bn == 64) return launch<64, true, T>(g, st);
-  if (bn == 32) return launch<32, true, T>(g, st);
+  const bool col = g.sb_shift != 7;
+  Choice c{128, 1, 1e30f};
+  if (few) {
+    const int bn = g.n <= 16 ? 16 : g.n <= 32 ? 32 : 64;
+    consider(c, g, bn, bn == 64 ? 1 : 2, 0.2f, 1.f);
+  } else {
+    consider(c, g, 256, 1, col ? 0.65f : 0.48f, 2.f);
+    consider(c, g, 128, 1, col ? 0.4f : 0.3f, 1.5f);
+    if (!g.b_mn) consider(c, g, 64, 1, 0.22f, 1.f);
+  }
+  g.splits = c.splits;
+  const size_t z = sizeof(T);
+  g.wide = g.out_j == 1 && aligned_to(g.out, 32) && g.out_i * z % 32 == 0;
+  g.pairs = g.out_j == 1 && aligned_to(g.out, 2 * z) && g.out_i % 2 == 0;
+  g.quads = aligned_to(g.out, 2 * z) && (g.out_j == 1 ? g.out_i : g.out_j) % 2 == 0;
+  if (c.bn == 256) return col ? launch<256, true, T>(g, st) : launch<256, false, T>(g, st);
+  if (c.bn == 128) return col ? launch<128, true, T>(g, st) : launch<128, false, T>(g, st);
+  if (c.bn == 64) return col ? launch<64, true, T>(g, st) : launch<64, false, T>(g, st);
+  if (c.bn == 32) return launch<32, true, T>(g, st);
   return launch<16, true, T>(g, st);
 }
 

@@ -168,7 +168,7 @@ struct Gemm8 {
   void* out;                      // at [i * out_i + j * out_j], one of them 1
   int64_t out_i, out_j;
   int splits;                     // set by the launch, like:
-  bool wide, pairs;               // stores of 32 bytes, of two elements
+  bool wide, pairs, quads;        // stores of 32 bytes, of two elements, of two at a time
 };
 cudaError_t launch_gemm8(int dtype, const Gemm8& g, cudaStream_t st);
 // 2-D TMA map of codes: `rows` rows of `inner` bytes, `pitch` bytes apart; box of 128
