@@ -92,7 +92,7 @@ __device__ __forceinline__ uint64_t drop2(const Dropout& a, uint32_t w0, uint32_
 template <typename T, bool ADD, bool ALL>
 __global__ void __launch_bounds__(256) dropout_kernel(Dropout a) {
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
-  const int64_t chunks = a.rows * a.cols / 8;
+  const int64_t total = a.rows * a.cols, chunks = total / 8;
   const T* __restrict__ x = static_cast<const T*>(a.x);
   const T* __restrict__ r = static_cast<const T*>(a.r);
   int64_t c0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
@@ -138,17 +138,30 @@ __global__ void __launch_bounds__(256) dropout_kernel(Dropout a) {
       if (c < chunks) store8(static_cast<T*>(a.y) + c * 8, out);
     }
   }
+  // what is left behind the chunks
+  const int64_t at = chunks * 8 + threadIdx.x;
+  if (blockIdx.x == 0 && at < total) {
+    gen.upper((uint32_t)((uint64_t)chunks >> 31));
+    uint32_t w[4];
+    gen.words((uint64_t)(uint32_t)(at / 4) * Philox::kM0, w);
+    const uint32_t word = at % 4 < 2 ? (at % 4 ? w[1] : w[0]) : at % 4 == 2 ? w[2] : w[3];
+    float lo, hi;
+    f2_unpack(drop2<ALL>(a, word, 0, to_f32(x[at]), 0.f, scale, ADD,
+                         f2_pack(ADD ? to_f32(r[at]) : 0.f, 0.f)),
+              lo, hi);
+    static_cast<T*>(a.y)[at] = from_f32<T>(lo);
+  }
 }
 
-// Elements from `from` on, wherever they lie (rows apart, tensors that start anywhere, what
-// is left behind whole chunks): a thread takes the four of a counter, each at its own place.
+// Elements wherever they lie (rows apart, tensors that start anywhere): a thread takes the
+// four of a counter, each at its own place.
 template <typename T, bool ALL>
-__global__ void __launch_bounds__(256) dropout_rows_kernel(Dropout a, int64_t from) {
+__global__ void __launch_bounds__(256) dropout_rows_kernel(Dropout a) {
   const int64_t total = a.rows * a.cols;
   const int64_t step = (int64_t)gridDim.x * 256 * 4;
   Philox gen(a.state);
   const uint64_t scale = f2_pack(a.scale, a.scale);
-  for (int64_t at = from + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < total; at += step) {
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < total; at += step) {
     uint32_t w[4];
     gen.upper((uint32_t)(at >> 34));
     gen.words((uint64_t)(uint32_t)(at / 4) * Philox::kM0, w);
@@ -185,10 +198,8 @@ cudaError_t launch_dropout(int dtype, const Dropout& a, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(z)>;
     const bool dense = a.rows == 1 || (a.x_stride == a.cols && (!a.r || a.r_stride == a.cols));
     const size_t al = chunk_align(dtype);
-    int64_t done = 0;
     if (dense && total >= 8 && aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.y, al)) {
       constexpr int U = sizeof(T) == 2 ? 2 : 1;
-      done = total / 8 * 8;
       const int64_t runs = (total / 8 + 256 * U - 1) / (256 * U), most = 152 * kRuns;
       const unsigned g = (unsigned)(runs < most ? runs : most);
       if (a.all)
@@ -197,12 +208,11 @@ cudaError_t launch_dropout(int dtype, const Dropout& a, cudaStream_t st) {
       else
         a.r ? dropout_kernel<T, true, false><<<g, 256, 0, st>>>(a)
             : dropout_kernel<T, false, false><<<g, 256, 0, st>>>(a);
-    }
-    if (done < total) {
-      const int64_t blocks = (total - done + 1023) / 1024;
+    } else {
+      const int64_t blocks = (total + 1023) / 1024;
       const unsigned g = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
-      a.all ? dropout_rows_kernel<T, true><<<g, 256, 0, st>>>(a, done)
-            : dropout_rows_kernel<T, false><<<g, 256, 0, st>>>(a, done);
+      a.all ? dropout_rows_kernel<T, true><<<g, 256, 0, st>>>(a)
+            : dropout_rows_kernel<T, false><<<g, 256, 0, st>>>(a);
     }
     return cudaGetLastError();
   });

@@ -40,10 +40,7 @@ struct GCfg {
   static constexpr int COLS = NB * BN < 32 ? 32 : NB * BN;
   static constexpr int ISSUERS = BN == 256 ? 2 : 4;
   static constexpr int PRE = 2 + ISSUERS;               // warps in front of the accumulating ones
-#ifndef CEPI
-#define CEPI 8
-#endif
-  static constexpr int EPI = BN == 256 ? (COL ? CEPI : 16) : BN >= 64 ? 8 : 4;
+  static constexpr int EPI = BN == 256 ? (COL ? 8 : 16) : BN >= 64 ? 8 : 4;
   static constexpr int THREADS = (PRE + EPI) * 32;
   static constexpr int CTAS = BN >= 64 ? 1 : 2;         // on an SM
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
@@ -183,6 +180,8 @@ struct Acc {
 #pragma unroll
         for (int k = 0; k < CH / 8; ++k)
           cols[k] = *reinterpret_cast<const uint64_t*>(sb + c + k * 8 + (lane & 3) * 2);
+        // (both halves of the lanes at once spill at 224 registers, and 16 warps of half the
+        // columns wait as long for half the work: 648, 733 and 723 us at 8192^3)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x[CH / 2];
@@ -317,7 +316,8 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   // launch's 640 x 96 or 384 x 168.  (A share that makes the compiler spill a
   // few registers costs a third of the rate: the spills land in the loop over the blocks.)
   if (warp < C::PRE) {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (BN == 256 && C::EPI == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     if (lane == 0) {
       int it = 0;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   }
   } else {
     if constexpr (BN == 256 && C::EPI == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, c0 = ((warp - C::PRE) >> 2) * C::PER;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + c0;
     int it = 0;
@@ -437,12 +437,12 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
         // the MMAs have read all stages: the ring holds the partial tile, the result's
         // contiguous dim along its rows
         if (g.out_j == 1) {
-          float* part = reinterpret_cast<float*>(sm) + q * 32 * (BN + 4);
+          float* part = reinterpret_cast<float*>(sm) + q * 32 * (BN + 4) + c0;
           acc.each(lane, [&](int r, int c, float lo, float hi) {
             *reinterpret_cast<float2*>(part + r * (BN + 4) + c) = make_float2(lo, hi);
           });
         } else {
-          float* part = reinterpret_cast<float*>(sm) + q * 32;
+          float* part = reinterpret_cast<float*>(sm) + q * 32 + c0 * 132;
           acc.each(lane, [&](int r, int c, float lo, float hi) {
             part[c * 132 + r] = lo;
             part[c * 132 + 132 + r] = hi;

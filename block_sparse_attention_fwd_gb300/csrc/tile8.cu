@@ -5,9 +5,12 @@
 //   128 x 128 elements           a weight's, which both kinds of product read
 // in the format of rows.cuh.  And the loading of the last two.
 //
-// A block takes a tile of 128 x 128: a thread holds a chunk of 8 columns of 8 rows, 16
-// apart, in registers, so a row lies in 16 neighbouring lanes and a column in 16 threads
-// of 8 warps.  Bound by HBM: x once in, a byte an element and kind out.
+// A block takes a tile of 128 x 128: a thread has a chunk of 8 columns of 8 rows, 16
+// apart, so a row lies in 16 neighbouring lanes and a column in 16 threads of 8 warps.
+// The tile waits in shared memory for its second use (in registers, where the compiler
+// kept it as 64 fp32 numbers a thread, two blocks fit an SM: 16384 x 4096 bf16 to rows
+// and columns in 74 us).  Bound by HBM: x once in, a byte an element and kind out.
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -28,57 +31,80 @@ __device__ __forceinline__ void put_codes(uint8_t* p, const Codes& c, int valid)
 
 template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(256) tile_save_kernel(TileSave a) {
+  constexpr int CB = (int)sizeof(Chunk<T>);
+  extern __shared__ __align__(16) uint8_t tile[];        // a thread's chunks in its own places
   __shared__ float part[8][128];
   __shared__ __align__(16) float col_scale[128];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t tiles_x = (a.cols + 127) / 128;
   const int64_t bx = blockIdx.x % tiles_x, by = blockIdx.x / tiles_x;
-  const int64_t row0 = by * 128, col0 = bx * 128, col = col0 + tx * 8;
+  const int64_t row0 = by * 128 + ty, col0 = bx * 128, col = col0 + tx * 8;
   const int valid = (int)min(max(a.cols - col, (int64_t)0), (int64_t)8);
-  Chunk<T> c[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t row = row0 + ty + 16 * k;
-    c[k] = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.x_stride + col,
-                         row < a.rows ? valid : 0);
-  }
-  if (a.row_codes) {
+  const int here = (int)min(max((a.rows - row0 + 15) / 16, (int64_t)0), (int64_t)8);  // rows
+  uint8_t* const mine = tile + threadIdx.x * 16;
+  {
+    const T* x = static_cast<const T*>(a.x) + row0 * a.x_stride + col;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int64_t row = row0 + ty + 16 * k;
-      float f[8];
+      uint8_t* p = mine + k * 256 * CB;
+      if (VEC && k < here && valid) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = to_f32(c[k].e[i]);
-      const float scale = scale_of(lanes_amax(amax8(f), 16), kFmtE4m3);
-      if (row < a.rows) {
-        put_codes<WIDE>(a.row_codes + row * a.row_stride + col, encode8<kFmtE4m3>(f, scale), valid);
-        if (tx == 0) a.row_scales[row * tiles_x + bx] = scale;
+        for (int v = 0; v < CB / 16; ++v)
+          copy_chunk<CB>(p + v * 256 * 16, x + v * (16 / (int)sizeof(T)));
+      } else {
+        const Chunk<T> c = load8<T, false>(x, !VEC && k < here ? valid : 0);
+#pragma unroll
+        for (int v = 0; v < CB / 16; ++v)
+          *reinterpret_cast<uint4*>(p + v * 256 * 16) = reinterpret_cast<const uint4*>(&c)[v];
       }
+      x += 16 * a.x_stride;
+    }
+    copy_commit();
+    copy_wait<0>();
+  }
+  auto chunk = [&](int k, float (&f)[8]) {
+    Chunk<T> c;
+#pragma unroll
+    for (int v = 0; v < CB / 16; ++v)
+      reinterpret_cast<uint4*>(&c)[v] =
+          *reinterpret_cast<const uint4*>(mine + k * 256 * CB + v * 256 * 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f32(c.e[i]);
+  };
+  float top[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const bool rows = a.row_codes != nullptr, down = a.col_codes || a.block_codes;
+  uint8_t* to = a.row_codes + row0 * a.row_stride + col;
+#pragma unroll 2
+  for (int k = 0; k < 8; ++k) {
+    float f[8];
+    chunk(k, f);
+    if (rows) {
+      const float scale = scale_of(lanes_amax(amax8(f), 16), kFmtE4m3);
+      if (k < here) {
+        put_codes<WIDE>(to, encode8<kFmtE4m3>(f, scale), valid);
+        if (tx == 0) a.row_scales[(row0 + 16 * k) * tiles_x + bx] = scale;
+      }
+      to += 16 * a.row_stride;
+    }
+    if (down) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = amax2(top[i], f[i]);
     }
   }
-  if (!a.col_codes && !a.block_codes) return;
-  float top[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top[i] = to_f32(c[0].e[i]);
-#pragma unroll
-    for (int k = 1; k < 8; ++k) top[i] = amax2(top[i], to_f32(c[k].e[i]));
-  }
+  if (!down) return;
   if (a.block_codes) {
     const float m = lanes_amax(amax8(top), 32);
     if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = m;
     __syncthreads();
     const float scale = scale_of(lanes_amax(part[0][threadIdx.x & 7], 8), kFmtE4m3);
     if (threadIdx.x == 0) a.block_scales[by * tiles_x + bx] = scale;
-#pragma unroll
+    to = a.block_codes + row0 * a.block_stride + col;
+#pragma unroll 4
     for (int k = 0; k < 8; ++k) {
-      const int64_t row = row0 + ty + 16 * k;
       float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = to_f32(c[k].e[i]);
-      if (row < a.rows)
-        put_codes<WIDE>(a.block_codes + row * a.block_stride + col, encode8<kFmtE4m3>(f, scale),
-                        valid);
+      chunk(k, f);
+      if (k < here) put_codes<WIDE>(to, encode8<kFmtE4m3>(f, scale), valid);
+      to += 16 * a.block_stride;
     }
     return;
   }
@@ -98,23 +124,25 @@ __global__ void __launch_bounds__(256) tile_save_kernel(TileSave a) {
   }
   __syncthreads();
   float inv[8];
-  uint32_t keep[2] = {0u, 0u};                       // codes 0 under a scale that is NaN
+  uint32_t keep[2] = {0u, 0u};                           // codes 0 under a scale that is NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float scale = col_scale[tx * 8 + i];
     inv[i] = __frcp_rn(scale);
     if (!isnan(scale)) keep[i / 4] |= 0xffu << (8 * (i % 4));
   }
-#pragma unroll
+  to = a.col_codes + row0 * a.col_stride + col;
+#pragma unroll 4
   for (int k = 0; k < 8; ++k) {
-    const int64_t row = row0 + ty + 16 * k;
     float f[8];
+    chunk(k, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(to_f32(c[k].e[i]), inv[i]);
+    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], inv[i]);
     Codes codes = encode8<kFmtE4m3>(f, 1.f);
     codes.w[0] &= keep[0];
     codes.w[1] &= keep[1];
-    if (row < a.rows) put_codes<WIDE>(a.col_codes + row * a.col_stride + col, codes, valid);
+    if (k < here) put_codes<WIDE>(to, codes, valid);
+    to += 16 * a.col_stride;
   }
 }
 
@@ -159,6 +187,19 @@ __global__ void __launch_bounds__(256) repitch_kernel(const uint8_t* __restrict_
   }
 }
 
+// Raises a kernel's limit of dynamic shared memory, once a device.
+template <auto* KERNEL>
+cudaError_t allow(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_repitch(const uint8_t* from, int64_t from_pitch, uint8_t* to, int64_t pitch,
@@ -180,13 +221,17 @@ cudaError_t launch_tile_save(int dtype, const TileSave& a, cudaStream_t st) {
                       aligned_to(a.row_codes, 8) && aligned_to(a.col_codes, 8) &&
                       aligned_to(a.block_codes, 8);
     const unsigned g = (unsigned)tiles;
-    if (vec && wide)
-      tile_save_kernel<T, true, true><<<g, 256, 0, st>>>(a);
-    else if (wide)
-      tile_save_kernel<T, false, true><<<g, 256, 0, st>>>(a);
-    else
-      tile_save_kernel<T, false, false><<<g, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    constexpr int smem = 128 * 128 * (int)sizeof(T);
+    auto go = [&](auto v, auto w) {
+      constexpr auto* k = tile_save_kernel<T, decltype(v)::value, decltype(w)::value>;
+      const cudaError_t e = allow<k>(smem);
+      if (e != cudaSuccess) return e;
+      k<<<g, 256, smem, st>>>(a);
+      return cudaGetLastError();
+    };
+    if (vec && wide) return go(std::true_type(), std::true_type());
+    return wide ? go(std::false_type(), std::true_type())
+                : go(std::false_type(), std::false_type());
   });
 }
 

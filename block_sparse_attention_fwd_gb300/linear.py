@@ -229,8 +229,8 @@ def _layer_fwd(x, weight, bias, eps, residual, want_y, y8):
         h = _like(x)
         r_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
     y = _like(x) if want_y else None
-    stats = torch.empty((2, *shape[:-1]), dtype=torch.float32, device=device)
-    mean, rstd = stats.unbind(0)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
     s8 = None if y8 is None else y8.struct()
     _launch("bl_layer_norm_fwd", device, _LAYER_NORM_ARGS.pack(
         rows, cols, stride, r_stride, x.data_ptr(), r_ptr,
