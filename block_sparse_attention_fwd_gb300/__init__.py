@@ -8,7 +8,8 @@ library is loaded on first use and a missing library raises.
 from . import _lib  # noqa: F401
 from ._lib import (BLError, alloc_lists, attn_bwd, attn_fwd, bwd_check_status,  # noqa: F401
                    bwd_workspace_bytes, make_shape, mask_from_stats, tile_stats_elems, tiles)
-from .api import BLAttention, BLRMSNorm, Rotary  # noqa: F401
+from .api import (BLAttention, BLDropout, BLLayerNorm, BLLinear8, BLRMSNorm,  # noqa: F401
+                  Rotary)
 from .linear import (Cols8, Weight8, act_save_both, dropout, dropout_next,  # noqa: F401
                      layer_norm_bwd, layer_norm_fwd, layer_norm_fwd_8bit, matmul8, matmul8_gw,
                      matmul8_gx, weight_save)

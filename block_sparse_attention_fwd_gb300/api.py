@@ -18,8 +18,9 @@ the sliding windows of the "Introducing BackLite" post's Nanochat runs
 same chain on a packed variable-length batch ([total, heads, head_dim]
 tensors, host offsets cu_seqlens), each sequence attending only to itself.
 
-Around it: ``BLRMSNorm`` (root-mean-square norm with the residual's addition,
-also as the attention's q/k norm), ``Rotary`` (positions on several axes, such
+Around it: ``BLRMSNorm`` and ``BLLayerNorm`` (norms with the residual's addition,
+also as the attention's q/k norm), ``BLLinear8`` (linear layers whose products
+run on 8-bit codes), ``BLDropout`` (dropout whose mask is never stored), ``Rotary`` (positions on several axes, such
 as time, height and width), and activations kept in 8 bits until the backward
 (``checkpoint="int8"`` or ``"e4m3"`` of the attention and the norm).
 
@@ -34,7 +35,7 @@ import os
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _lib, ops
+from . import _lib, linear, ops
 
 
 def default_tiles(n: int, d: int):
@@ -264,6 +265,179 @@ class BLRMSNorm(torch.nn.Module):
         return _RMSNormFn.apply(x, self.weight, residual, self.eps, checkpoint, self.group)
 
 
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps, checkpoint, group):
+        ctx.set_materialize_grads(False)
+        y, h, mean, rstd = linear.layer_norm_fwd(x, weight, bias, eps, residual)
+        ctx.in8 = (group, x.dtype) if checkpoint is not None else None
+        if ctx.in8:
+            h8 = ops.act_save(h, checkpoint, group)
+            ctx.save_for_backward(h8.codes, h8.scales, mean, rstd, weight)
+        else:
+            ctx.save_for_backward(h, mean, rstd, weight)
+        ctx.added = residual is not None
+        ctx.bias_type = None if bias is None else bias.dtype
+        return (y, h) if ctx.added else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_y, g_h=None):
+        *h, mean, rstd, weight = ctx.saved_tensors
+        _, need_w, need_b, *_ = ctx.needs_input_grad
+        if g_y is None:                    # only the stream behind the addition was used
+            cols = g_h.shape[-1]
+            g_w = torch.zeros_like(weight) if need_w else None
+            g_b = g_h.new_zeros(cols, dtype=ctx.bias_type) if need_b else None
+            return g_h, g_w, g_b, g_h, None, None, None
+        h = ops.Act8(*h, *ctx.in8) if ctx.in8 else h[0].contiguous()
+        g_x, g_w, g_b = linear.layer_norm_bwd(g_y.contiguous(), h, mean, rstd, weight,
+                                              None if g_h is None else g_h.contiguous(),
+                                              need_g_w=need_w, need_g_b=need_b)
+        if g_b is not None:
+            g_b = g_b.to(ctx.bias_type)    # fp32 where there is no weight
+        return g_x, g_w, g_b, g_x if ctx.added else None, None, None, None
+
+
+class BLLayerNorm(torch.nn.Module):
+    """Layer norm over the last dim of ``cols`` elements, with a weight and a ``bias``
+    unless these are off (``affine=False`` turns both off).
+
+    ``norm(x)`` gives y; ``norm(x, residual)`` adds first and gives (y, h) with
+    h = x + residual, the stream that goes on.  ``checkpoint`` ("int8" or
+    "e4m3") keeps h in 8 bits until the backward, one scale for every ``group``
+    elements, and the backward reads the codes as they are."""
+
+    def __init__(self, cols: int, eps: float = 1e-5, affine: bool = True, bias: bool = True,
+                 checkpoint: str | None = None, group: int = 128, device=None, dtype=None):
+        super().__init__()
+        if not 1 <= cols <= _lib.NORM_MAX_COLS:
+            raise ValueError(f"1 to {_lib.NORM_MAX_COLS} elements, got {cols}")
+        _check_checkpoint(checkpoint)
+        if group not in (0, 32, 64, 128):
+            raise ValueError(f"group must be 0, 32, 64 or 128, got {group}")
+        self.cols, self.eps, self.checkpoint, self.group = int(cols), float(eps), checkpoint, group
+        self.weight = self.bias = None
+        if affine:
+            self.weight = torch.nn.Parameter(torch.ones(cols, device=device, dtype=dtype))
+            if bias:
+                self.bias = torch.nn.Parameter(torch.zeros(cols, device=device, dtype=dtype))
+
+    def forward(self, x, residual=None):
+        if x.shape[-1] != self.cols:
+            raise ValueError(f"rows of {x.shape[-1]} elements, the norm has {self.cols}")
+        x, residual = (t if t is None or ops.row_stride(t) is not None else t.contiguous()
+                       for t in (x, residual))
+        wants = _wants_backward(x, self.weight, self.bias, residual)
+        return _LayerNormFn.apply(x, self.weight, self.bias, residual, self.eps,
+                                  self.checkpoint if wants else None, self.group)
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, used):
+        ctx.save_for_backward(used)
+        ctx.p, ctx.added = p, residual is not None
+        return linear.dropout(x, p, used, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_y):
+        used, = ctx.saved_tensors
+        g_x = linear.dropout(g_y.contiguous(), ctx.p, used) if ctx.needs_input_grad[0] else None
+        return g_x, g_y if ctx.added else None, None, None
+
+
+class BLDropout(torch.nn.Module):
+    """Dropout whose mask is a function of (seed, offset) and the element's place and is
+    formed again in the backward.  ``drop(x)`` or ``drop(x, residual)``, which adds the
+    residual behind it.  Every call in training takes the next offset of ``state``, an
+    int64 buffer (seed, offset) on the device: a captured graph draws anew with every
+    replay, and a saved state brings the same masks back.  ``seed`` None draws one.
+    Out of training, and with p = 0, nothing is dropped."""
+
+    def __init__(self, p: float = 0.1, seed: int | None = None, device=None):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must lie in [0, 1], got {p}")
+        if device is None:
+            device = "cuda" if torch.cuda.is_available() else "cpu"
+        if seed is None:
+            seed = int(torch.randint(2 ** 63 - 1, ()))
+        self.p = float(p)
+        self.register_buffer("state", torch.tensor([seed, 0], dtype=torch.int64, device=device))
+
+    def forward(self, x, residual=None):
+        if not self.training or self.p == 0.0:
+            return x if residual is None else x + residual
+        x, residual = (t if t is None or ops.row_stride(t) is not None else t.contiguous()
+                       for t in (x, residual))
+        return _DropoutFn.apply(x, residual, self.p, linear.dropout_next(self.state))
+
+
+class _Linear8Fn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, w8, wants):
+        need_x, need_w = wants and ctx.needs_input_grad[0], wants and ctx.needs_input_grad[1]
+        if w8 is None:
+            w8 = linear.weight_save(weight)
+        x8, x_cols = linear.act_save_both(x, cols=need_w)
+        if need_x or need_w:
+            ctx.save_for_backward(*((w8.codes, w8.scales) if need_x else (None, None)),
+                                  *((x_cols.codes, x_cols.scales) if need_w else (None, None)))
+            ctx.types = x.dtype, weight.dtype
+        return linear.matmul8(x8, w8, x.dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_y):
+        w_codes, w_scales, x_codes, x_scales = ctx.saved_tensors
+        need_x, need_w, *_ = ctx.needs_input_grad
+        x_type, w_type = ctx.types
+        if ops.row_stride(g_y) is None:
+            g_y = g_y.contiguous()
+        g8, g_cols = linear.act_save_both(g_y, rows=need_x, cols=need_w)
+        g_x = g_w = None
+        if need_x:
+            g_x = linear.matmul8_gx(g8, linear.Weight8(w_codes, w_scales, w_type), x_type)
+        if need_w:
+            g_w = linear.matmul8_gw(g_cols, linear.Cols8(x_codes, x_scales, x_type), w_type)
+        return g_x, g_w, None, None
+
+
+class BLLinear8(torch.nn.Module):
+    """y = x w^T with a weight [out, in] kept in its own type and products on e4m3 codes:
+    x and g_y with a scale for every 128 elements of a row (of a column of 128 tokens for
+    the weight's gradient), w with one for every 128 x 128.  What waits for the backward
+    are codes: a byte an element of x and of w.
+
+    ``linear(x)``; x may also be an Act8 in e4m3 with groups of 128, such as a norm's
+    8-bit output, where no backward is wanted.  ``w8``, the ``weight_save`` of the weight,
+    spares a call its saving; it has to be that of the weight as it is."""
+
+    def __init__(self, in_features: int, out_features: int, device=None, dtype=None):
+        super().__init__()
+        if in_features < 1 or out_features < 1:
+            raise ValueError(f"at least one feature, got {in_features} and {out_features}")
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.weight = torch.nn.Parameter(
+            torch.empty(out_features, in_features, device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
+
+    def forward(self, x, w8=None):
+        if w8 is not None and (not isinstance(w8, linear.Weight8) or
+                               w8.codes.shape != self.weight.shape):
+            raise ValueError(f"w8 must be the Weight8 of a weight {tuple(self.weight.shape)}")
+        if isinstance(x, ops.Act8):
+            if _wants_backward(self.weight):
+                raise ValueError("codes carry no gradient: call with x, or without gradients")
+            return linear.matmul8(x, linear.weight_save(self.weight) if w8 is None else w8)
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"rows of {x.shape[-1]} elements, the layer takes {self.in_features}")
+        x = x if ops.row_stride(x) is not None else x.contiguous()
+        return _Linear8Fn.apply(x, self.weight, w8, _wants_backward(x, self.weight))
+
+
 def _wants_backward(*tensors):
     """Whether a backward can follow.  (Within an autograd function the grad mode is off.)"""
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
@@ -279,8 +453,8 @@ def _check_checkpoint(checkpoint, out=False, in_forward=False):
 class BLAttention(torch.nn.Module):
     """Attention whose backward skips the lightest tiles (negl_prob of the mass).
 
-    ``q_norm`` and ``k_norm`` (``BLRMSNorm`` of head_dim or of heads * head_dim
-    elements) and then ``rotary`` (``Rotary``; the call takes ``positions``) are
+    ``q_norm`` and ``k_norm`` (``BLRMSNorm`` or ``BLLayerNorm`` of head_dim or of
+    heads * head_dim elements) and then ``rotary`` (``Rotary``; the call takes ``positions``) are
     applied to the query and the key first.
 
     ``checkpoint`` ("int8" or "e4m3") keeps the q, k and v that the backward reads
@@ -295,7 +469,8 @@ class BLAttention(torch.nn.Module):
 
     def __init__(self, negl_prob: float = 0.05, block_q: int | None = None,
                  block_k: int | None = None, causal: bool = False, window: int = 0,
-                 q_norm: BLRMSNorm | None = None, k_norm: BLRMSNorm | None = None,
+                 q_norm: BLRMSNorm | BLLayerNorm | None = None,
+                 k_norm: BLRMSNorm | BLLayerNorm | None = None,
                  rotary: Rotary | None = None, checkpoint: str | None = None,
                  checkpoint_out: bool = False, checkpoint_in_forward: bool = False):
         super().__init__()

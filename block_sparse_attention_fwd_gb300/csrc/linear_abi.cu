@@ -225,14 +225,14 @@ bl_status bl_layer_norm_bwd(const bl_layer_norm_bwd_args* p, void* stream) {
 bl_status bl_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t x_stride,
                      const void* residual, int64_t residual_stride, double p, const int64_t* state,
                      void* y, void* stream) {
-  if (!rows_ok(rows, cols) || !dtype_ok(dtype)) return BL_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 1 || !dtype_ok(dtype)) return BL_ERR_INVALID_ARG;
   if (!(p >= 0. && p <= 1.)) return BL_ERR_INVALID_ARG;
+  if (rows > ((int64_t)1 << 42) / cols) return BL_ERR_UNSUPPORTED;
   if (x_stride < cols || (residual && residual_stride < cols)) return BL_ERR_INVALID_ARG;
   if (rows && (!x || !y || !state)) return BL_ERR_INVALID_ARG;
   if (!elem_ok(x, dtype) || !elem_ok(residual, dtype) || !elem_ok(y, dtype) ||
       !bl::aligned_to(state, 8))
     return BL_ERR_INVALID_ARG;
-  if (rows > ((int64_t)1 << 42) / cols) return BL_ERR_UNSUPPORTED;
   bl::Dropout a{};
   a.rows = rows; a.cols = cols; a.x_stride = x_stride; a.r_stride = residual ? residual_stride : 0;
   a.x = x; a.r = residual; a.y = y; a.state = state;
