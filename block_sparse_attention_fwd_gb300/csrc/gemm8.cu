@@ -7,12 +7,12 @@
 // nothing is rounded to fewer than 32 bits before the result.
 //
 // A CTA has a tile of 128 x BN.  Warp roles:
-//   warp 0      TMA producer: codes of A and B, 128 of the summed dim a stage.
-//   warps 1, 2  MMA issuers (one thread each, turn by turn), warp 1 the TMEM's owner: a
-//               block's product into one of NB accumulators.
-//   warp 3      scales of the tile's rows and columns into a ring of shared memory.
-//   warps 4-    accumulate: a thread has a row of up to 128 columns of the tile in
-//               registers, reads the block's product from TMEM and adds it, scaled.
+//   warp 0        TMA producer: codes of A and B, 128 of the summed dim a stage.
+//   ISSUERS more  MMA issuers (one thread each, turn by turn), warp 1 the TMEM's owner: a
+//                 block's product into one of NB accumulators.
+//   one more      scales of the tile's rows and columns into a ring of shared memory.
+//   EPI more      accumulate: 32 rows of BN or BN / 2 columns of the tile in registers, to
+//                 which a warp adds the block's product from TMEM, scaled.
 // Either operand may have the summed dim contiguous (K-major) or the other one
 // (MN-major): the tiles in shared memory are alike, 128 rows of 128 bytes, and only
 // the descriptors differ, so no operand is ever transposed in memory.
@@ -39,8 +39,8 @@ struct GCfg {
   static constexpr int NB = BN == 256 ? 2 : 4;          // accumulators in TMEM
   static constexpr int COLS = NB * BN < 32 ? 32 : NB * BN;
   static constexpr int ISSUERS = BN == 256 ? 2 : 4;
-  static constexpr int PRE = 2 + ISSUERS;               // warps in front of the accumulating ones
-  static constexpr int EPI = BN == 256 ? (COL ? 8 : 16) : BN >= 64 ? 8 : 4;
+  static constexpr int PRE = 2 + ISSUERS;               // warps in front of the accumulating
+  static constexpr int EPI = BN >= 64 ? 8 : 4;          // accumulating warps
   static constexpr int THREADS = (PRE + EPI) * 32;
   static constexpr int CTAS = BN >= 64 ? 1 : 2;         // on an SM
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
@@ -168,37 +168,41 @@ struct Acc {
       }
     } else {
       constexpr int CH = PER < 32 ? 16 : 32;             // columns at a time
-      uint64_t rows[4];
+      constexpr int N = PER / CH * 2;                    // of 16 lanes
+      float rows[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float s = sa[(lane >> 2) + 8 * u];
-        rows[u] = f2_pack(s, s);
-      }
+      for (int u = 0; u < 4; ++u) rows[u] = sa[(lane >> 2) + 8 * u];
+      // the next part is on its way while this one is added
+      uint32_t x[2][CH / 2];
+      auto load = [&](int n) {
+        const uint32_t at = taddr + ((uint32_t)(16 * (n & 1)) << 16) + n / 2 * CH;
+        if constexpr (CH == 32)
+          tmem_ld_16x32(at, x[n & 1]);
+        else
+          tmem_ld_16x16(at, x[n & 1]);
+      };
+      load(0);
+      uint64_t cols[CH / 8];
 #pragma unroll
-      for (int c = 0; c < PER; c += CH) {
-        uint64_t cols[CH / 8];
-#pragma unroll
-        for (int k = 0; k < CH / 8; ++k)
-          cols[k] = *reinterpret_cast<const uint64_t*>(sb + c + k * 8 + (lane & 3) * 2);
-        // (both halves of the lanes at once spill at 224 registers, and 16 warps of half the
-        // columns wait as long for half the work: 648, 733 and 723 us at 8192^3)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[CH / 2];
-          if constexpr (CH == 32)
-            tmem_ld_16x32(taddr + ((uint32_t)(16 * h) << 16) + c, x);
-          else
-            tmem_ld_16x16(taddr + ((uint32_t)(16 * h) << 16) + c, x);
-          tmem_ld_wait();
+      for (int n = 0; n < N; ++n) {
+        const int c = n / 2 * CH, h = n & 1;
+        if (h == 0) {
 #pragma unroll
           for (int k = 0; k < CH / 8; ++k)
+            cols[k] = *reinterpret_cast<const uint64_t*>(sb + c + k * 8 + (lane & 3) * 2);
+        }
+        tmem_ld_wait();
+        if (n + 1 < N) load(n + 1);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint64_t& to = v[(c / 8 + k) * 4 + 2 * h + u];
-              to = ffma2(f2_pack(__uint_as_float(x[4 * k + 2 * u]),
-                                 __uint_as_float(x[4 * k + 2 * u + 1])),
-                         fmul2(cols[k], rows[2 * h + u]), to);
-            }
+        for (int u = 0; u < 2; ++u) {
+          const uint64_t row = f2_pack(rows[2 * h + u], rows[2 * h + u]);
+#pragma unroll
+          for (int k = 0; k < CH / 8; ++k) {
+            uint64_t& to = v[(c / 8 + k) * 4 + 2 * h + u];
+            to = ffma2(f2_pack(__uint_as_float(x[h][4 * k + 2 * u]),
+                               __uint_as_float(x[h][4 * k + 2 * u + 1])),
+                       fmul2(cols[k], row), to);
+          }
         }
       }
     }
@@ -312,98 +316,127 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   auto failed = [&]() { return *(volatile int*)&s_fail != 0; };
   auto fail = [&]() { atomicOr(&s_fail, 1); };
 
-  // The accumulating warps need registers, the others few; the shares stay within the
-  // launch's 640 x 96 or 384 x 168.  (A share that makes the compiler spill a
-  // few registers costs a third of the rate: the spills land in the loop over the blocks.)
+  // The accumulating warps need registers, the others few; the shares are the launch's 384
+  // x 168.  (Either share too small spills a few in its loop over the blocks, which costs a
+  // third of the rate: 634 and 763 us of g_w at 8192^3 with 56 and 224.)
   if (warp < C::PRE) {
-    if constexpr (BN == 256 && C::EPI == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 0) {
-    if (lane == 0) {
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      if (lane == 0) {
+        int it = 0;
+        bool ok = true;
+        s_loads = min(C::NS, first < tiles ? kb1 - kb0 : 0);
+        for (int t = first; ok && t < tiles; t += step) {
+          int i, j;
+          tile_at<C::GROUP>(t, ti, tj, i, j);
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            if (t == first && kb - kb0 < C::NS) continue;  // on their way
+            const int s = it % C::NS;
+            ok = it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS);
+            if (!ok) break;
+            load(s, i, j, kb);
+            s_loads = it + 1;
+          }
+        }
+        if (!ok) fail();
+      }
+    } else if (warp <= C::ISSUERS) {
+      // The issuers take turns: a look at a barrier behind MMAs returns only when those have
+      // been taken up, some 100 clocks in which one issuer alone would leave the tensor core
+      // idle (with two looks a block, 930 clocks a block of 512).
+      const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
+      if (lane == 0) {
+        const uint32_t id = idesc_e4m3(128, BN, g.a_mn, g.b_mn);
+        const uint32_t step_a = g.a_mn ? 4096 : 32, step_b = g.b_mn ? 4096 : 32;
+        int it = warp - 1;
+        for (; it < total; it += C::ISSUERS) {
+          const int s = it % C::NS, b = it % C::NB;
+          if (!((it < C::NB || wait(&bars.t_empty[b], it - C::NB, C::NB)) &&
+                wait(&bars.full[s], it, C::NS)))
+            break;
+          fence_after_sync();
+          const uint32_t a = saddr(sm + s * C::STAGE);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8(tmem + b * BN, sdesc_sw128(a + kk * step_a, 16384, 1024),
+                   sdesc_sw128(a + C::A_BYTES + kk * step_b, 16384, 1024), id, kk > 0);
+          mma_commit(&bars.empty[s]);
+          mma_commit(&bars.t_full[b]);
+        }
+        if (it < total) {
+          fail();
+          // nothing may be in flight when the CTA ends: its MMAs, and then the copies
+          const int last = it - C::ISSUERS;
+          if (last >= 0) mbar_wait_poll(&bars.t_full[last % C::NB], (last / C::NB) & 1);
+        }
+      }
+    } else {
+      // Scales that lie side by side come 16 bytes a lane, others by pointers that walk with
+      // the blocks.
+      const bool a_run = g.sa_i == 1 && g.sa_shift == 0;
+      const bool a_wide = a_run && aligned_to(g.sa, 16) && g.sa_b % 4 == 0;
+      const bool b_wide = aligned_to(g.sb, 16) && g.sb_b % 4 == 0;
+      auto run = [&](float* to, const float* from, int left, int count, bool wide) {
+        if (wide) {
+          for (int e = lane * 4; e < count; e += 128)
+            copy_async<16>(to + e, from + (e < left ? e : 0), min(max(left - e, 0) * 4, 16));
+        } else {
+          for (int e = lane; e < count; e += 32)
+            copy_async<4>(to + e, from + (e < left ? e : 0), e < left ? 4 : 0);
+        }
+      };
       int it = 0;
       bool ok = true;
-      s_loads = min(C::NS, first < tiles ? kb1 - kb0 : 0);
       for (int t = first; ok && t < tiles; t += step) {
         int i, j;
         tile_at<C::GROUP>(t, ti, tj, i, j);
+        const float* pa[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = a_run ? i * 128 : min(i * 128 + lane + 32 * u, g.m - 1);
+          pa[u] = g.sa + (int64_t)(row >> g.sa_shift) * g.sa_i + kb0 * g.sa_b;
+        }
+        // few columns: one a lane, or two; many: side by side; !COL: one for 128
+        constexpr int PB = BN <= 64 ? (BN + 31) / 32 : 1;
+        const float* pb[PB];
+#pragma unroll
+        for (int u = 0; u < PB; ++u) {
+          const int col = j * BN + (!COL ? lane * 128 : BN <= 64 ? lane + 32 * u : 0);
+          pb[u] = g.sb + (int64_t)(min(col, g.n - 1) >> g.sb_shift) * g.sb_i + kb0 * g.sb_b;
+        }
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          if (t == first && kb - kb0 < C::NS) continue;  // on their way
-          const int s = it % C::NS;
-          ok = it < C::NS || wait(&bars.empty[s], it - C::NS, C::NS);
+          const int s = it % C::NSC;
+          ok = __all_sync(0xffffffffu,
+                          it < C::NSC || wait(&bars.s_empty[s], it - C::NSC, C::NSC));
           if (!ok) break;
-          load(s, i, j, kb);
-          s_loads = it + 1;
-        }
-      }
-      if (!ok) fail();
-    }
-  } else if (warp <= C::ISSUERS) {
-    // The issuers take turns: a look at a barrier behind MMAs returns only when those have
-    // been taken up, some 100 clocks in which one issuer alone would leave the tensor core
-    // idle (with two looks a block, 930 clocks a block of 512).
-    const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
-    if (lane == 0) {
-      const uint32_t id = idesc_e4m3(128, BN, g.a_mn, g.b_mn);
-      const uint32_t step_a = g.a_mn ? 4096 : 32, step_b = g.b_mn ? 4096 : 32;
-      int it = warp - 1;
-      for (; it < total; it += C::ISSUERS) {
-        const int s = it % C::NS, b = it % C::NB;
-        if (!((it < C::NB || wait(&bars.t_empty[b], it - C::NB, C::NB)) &&
-              wait(&bars.full[s], it, C::NS)))
-          break;
-        fence_after_sync();
-        const uint32_t a = saddr(sm + s * C::STAGE);
+          float* a = sc + s * C::SC_FLOATS;
+          if (a_run) {
+            run(a, pa[0], g.m - i * 128, 128, a_wide);
+          } else {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f8(tmem + b * BN, sdesc_sw128(a + kk * step_a, 16384, 1024),
-                       sdesc_sw128(a + C::A_BYTES + kk * step_b, 16384, 1024), id, kk > 0);
-        mma_commit(&bars.empty[s]);
-        mma_commit(&bars.t_full[b]);
-      }
-      if (it < total) {
-        fail();
-        // nothing may be in flight when the CTA ends: its MMAs, and then the copies
-        const int last = it - C::ISSUERS;
-        if (last >= 0) mbar_wait_poll(&bars.t_full[last % C::NB], (last / C::NB) & 1);
-      }
-    }
-  } else {
-    const int t0 = lane;
-    int it = 0;
-    bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      int i, j;
-      tile_at<C::GROUP>(t, ti, tj, i, j);
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % C::NSC;
-        ok = __all_sync(0xffffffffu,
-                        it < C::NSC || wait(&bars.s_empty[s], it - C::NSC, C::NSC));
-        if (!ok) break;
-        float* a = sc + s * C::SC_FLOATS;
-#pragma unroll
-        for (int e = t0; e < 128; e += 32) {
-          const int row = min(i * 128 + e, g.m - 1);
-          copy_async<4>(a + e, g.sa + (int64_t)(row >> g.sa_shift) * g.sa_i + kb * g.sa_b);
-        }
-        if constexpr (COL) {
-#pragma unroll 2
-          for (int e = t0; e < BN; e += 32) {
-            const int col = min(j * BN + e, g.n - 1);
-            copy_async<4>(a + 128 + e, g.sb + (int64_t)(col >> g.sb_shift) * g.sb_i + kb * g.sb_b);
+            for (int u = 0; u < 4; ++u) copy_async<4>(a + lane + 32 * u, pa[u]);
           }
-        } else if (t0 < (BN + 127) / 128) {
-          const int col = min(j * BN + t0 * 128, g.n - 1);
-          copy_async<4>(a + 128 + t0, g.sb + (int64_t)(col >> g.sb_shift) * g.sb_i + kb * g.sb_b);
+          if constexpr (!COL) {
+            if (lane < (BN + 127) / 128) copy_async<4>(a + 128 + lane, pb[0]);
+          } else if constexpr (BN <= 64) {
+#pragma unroll
+            for (int u = 0; u < PB; ++u)
+              if (lane + 32 * u < BN) copy_async<4>(a + 128 + lane + 32 * u, pb[u]);
+          } else {
+            run(a + 128, pb[0], g.n - j * BN, BN, b_wide);
+          }
+          copies_arrive(&bars.s_full[s]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) pa[u] += g.sa_b;
+#pragma unroll
+          for (int u = 0; u < PB; ++u) pb[u] += g.sb_b;
         }
-        copies_arrive(&bars.s_full[s]);
       }
+      if (!ok && lane == 0) fail();
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (!ok && lane == 0) fail();
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  }
   } else {
-    if constexpr (BN == 256 && C::EPI == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if constexpr (BN == 256 && C::EPI == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int q = warp & 3, c0 = ((warp - C::PRE) >> 2) * C::PER;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + c0;
     int it = 0;
@@ -492,7 +525,7 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
       // four neighbours of the result's contiguous dim at a time, all ranks' under way at
       // once (one by one, a sum of 7 ranks at 128 x 5120 x 5120 took 60 us)
       const bool rows = g.out_j == 1;
-      const int wide = rows ? BN : 128, pitch = wide + 4, quads = 128 * BN / 4;   // x: along the other
+      const int wide = rows ? BN : 128, pitch = wide + 4, quads = 128 * BN / 4;
       const int e0 = quads * rank / g.splits, e1 = quads * (rank + 1) / g.splits;
       for (int e = e0 + threadIdx.x; e < e1; e += 2 * C::THREADS) {
         uint4 v[2][kMostSplits];
@@ -561,6 +594,8 @@ cudaError_t launch(const Gemm8& g, cudaStream_t st) {
   using C = GCfg<BN, COL>;
   // rows of B that lie across the summed dim come 128 columns at a time
   if (BN < 128 && g.b_mn) return cudaErrorInvalidValue;
+  // many columns with a scale each lie side by side
+  if (COL && BN >= 128 && g.sb_i != 1) return cudaErrorInvalidValue;
   CUtensorMap ta, tb;
   const int box_b = g.b_mn || BN > 128 ? 128 : BN;
   if (!make_codes_map(&ta, g.a, g.a_mn ? g.m : g.k, g.a_mn ? g.k : g.m, g.a_pitch, 128) ||
@@ -601,9 +636,12 @@ Gemm8 swapped(const Gemm8& g) {
   return s;
 }
 
-// Which tile, by an estimate of the time in us.  Measured for a block of 128 of the summed
-// dim: 0.48 us in tiles of 128 x 256, ... (see the constants); a launch takes some 4 us, a sum over a
-// cluster kSum more.
+// Which tile, by an estimate of the time.  A block of 128 of the summed dim takes 0.46 us in
+// a tile of 128 x 256 (0.64 with a scale a column), 0.33 (0.45) in one of 128 x 128, 0.3 in
+// one of 128 x 64, 0.25 in a narrow one, whose products are too short to fill the time
+// between one wait and the next; a tile's end takes 1 to 1.5, a sum over a cluster 1.5 and
+// more with the columns.  Measured: 512 x 5120 x 5120 in 23, 33 and 41 us in tiles of 256, 128
+// and 64 columns, 128 x 5120 x 5120 in 23, 18.5 and 17 us, 14.8 with two CTAs a tile.
 struct Choice {
   int bn, splits;
   float us;
@@ -631,11 +669,11 @@ cudaError_t run(const Gemm8& in, cudaStream_t st) {
   Choice c{128, 1, 1e30f};
   if (few) {
     const int bn = g.n <= 16 ? 16 : g.n <= 32 ? 32 : 64;
-    consider(c, g, bn, bn == 64 ? 1 : 2, 0.2f, 1.f);
+    consider(c, g, bn, bn == 64 ? 1 : 2, bn == 64 ? 0.3f : 0.25f, 1.f);
   } else {
-    consider(c, g, 256, 1, col ? 0.65f : 0.48f, 2.f);
-    consider(c, g, 128, 1, col ? 0.4f : 0.3f, 1.5f);
-    if (!g.b_mn) consider(c, g, 64, 1, 0.22f, 1.f);
+    consider(c, g, 256, 1, col ? 0.64f : 0.46f, 1.5f);
+    consider(c, g, 128, 1, col ? 0.45f : 0.33f, 1.f);
+    if (!g.b_mn) consider(c, g, 64, 1, 0.3f, 1.f);
   }
   g.splits = c.splits;
   const size_t z = sizeof(T);

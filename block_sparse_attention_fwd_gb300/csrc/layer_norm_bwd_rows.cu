@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(512) __maxnreg__(NV == 1 ? 72 : 96)
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = ffma2(u[i], rr, bb);
     } else {
-      const uint2 raw = *reinterpret_cast<const uint2*>(ring + place + h_plane + k * nt * 8 + t * 8);
+      const uint2 raw =
+          *reinterpret_cast<const uint2*>(ring + place + h_plane + k * nt * 8 + t * 8);
       float f[8];
       decode8<FMT>(Codes{{raw.x, raw.y}}, f);
       const uint64_t rr = f2_pack(scale * rstd, scale * rstd);

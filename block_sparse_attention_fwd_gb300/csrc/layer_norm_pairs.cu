@@ -23,7 +23,8 @@ constexpr int pair_regs(int nv) { return nv == 1 ? 64 : 96; }
 // together likewise, around the first warp's.
 // FULL: every thread has all of its chunks.
 template <typename T, int NV, int RB, int FMT8, bool RES, bool FULL>
-__global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV)) layer_norm_pair_kernel(NormFwd a) {
+__global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV))
+    layer_norm_pair_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>), TENSORS = RES ? 2 : 1;
   __shared__ float2 buf[2][RB][16];
   extern __shared__ __align__(16) uint8_t ring[];

@@ -200,7 +200,8 @@ bl_status bl_layer_norm_bwd(const bl_layer_norm_bwd_args* p, void* stream) {
       !elem_ok(p->g_x, p->dtype) || !bl::aligned_to(p->mean, 4) || !bl::aligned_to(p->rstd, 4))
     return BL_ERR_INVALID_ARG;
   if ((p->weight && !elem_ok(p->weight, p->weight_dtype)) ||
-      (p->g_w && !elem_ok(p->g_w, p->weight_dtype)) || (p->g_b && !elem_ok(p->g_b, p->weight_dtype)))
+      (p->g_w && !elem_ok(p->g_w, p->weight_dtype)) ||
+      (p->g_b && !elem_ok(p->g_b, p->weight_dtype)))
     return BL_ERR_INVALID_ARG;
   if (cols > BL_NORM_MAX_COLS) return BL_ERR_UNSUPPORTED;
   const bool sums = p->g_w || p->g_b;

@@ -505,7 +505,7 @@ __device__ __forceinline__ void load_bias8(const void* b, bool f32, int64_t col,
   }
 }
 
-inline bool aligned_to(const void* p, size_t a) {
+inline __host__ __device__ bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
