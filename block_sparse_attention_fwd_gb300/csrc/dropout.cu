@@ -78,7 +78,8 @@ __device__ __forceinline__ void two(const Chunk<__nv_bfloat16>& c, int i, float&
   hi = __uint_as_float(w & 0xffff0000u);
 }
 
-// Two elements: what is dropped is 0 before its product, so infinities go too.  ALL: p = 1.
+// Two elements: what is dropped is 0 before its product, so infinities go too.  ALL: all
+// are, p = 1 or within 2^-33 of it.
 template <bool ALL>
 __device__ __forceinline__ uint64_t drop2(const Dropout& a, uint32_t w0, uint32_t w1, float x0,
                                           float x1, uint64_t scale, bool add, uint64_t r) {

@@ -186,7 +186,7 @@ struct Dropout {
   void* y;
   const int64_t* state;
   uint32_t threshold;             // words below are dropped
-  bool all;                       // p = 1
+  bool all;                       // all are
   float scale;
 };
 cudaError_t launch_dropout(int dtype, const Dropout& a, cudaStream_t st);

@@ -238,8 +238,8 @@ bl_status bl_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64
   a.rows = rows; a.cols = cols; a.x_stride = x_stride; a.r_stride = residual ? residual_stride : 0;
   a.x = x; a.r = residual; a.y = y; a.state = state;
   const double words = nearbyint(p * 4294967296.);
-  a.all = p == 1.;
-  a.threshold = words >= 4294967295. ? 0xffffffffu : (uint32_t)words;
+  a.all = words >= 4294967296.;                         // no word is as large
+  a.threshold = a.all ? 0xffffffffu : (uint32_t)words;
   a.scale = p < 1. ? (float)(1. / (1. - p)) : 0.f;
   return cuda_status(bl::launch_dropout(dtype, a, (cudaStream_t)stream));
 }

@@ -38,9 +38,9 @@ __device__ __forceinline__ void write_partial(const NormBwd& a, float* partial, 
 
 // Registers a thread of the backward may take (the launch counts on them).
 // SPREAD, with an address an element, takes more, and so does the layer norm, with
-// the sums of g_b.
+// the sums of g_b (262144 x 128 bf16: 59 us with 88, two blocks an SM, 46 with 64).
 constexpr int bwd_regs(int lpr, int nv, bool spread = false, bool layer = false) {
-  return layer    ? (nv >= 2 || spread ? 128 : 88)
+  return layer    ? (nv >= 2 || spread ? 128 : lpr ? 64 : 88)
          : nv >= 3  ? 128
          : spread ? (nv == 1 ? 104 : 128)
          : nv == 2 ? 96

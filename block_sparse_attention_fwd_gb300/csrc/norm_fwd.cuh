@@ -14,7 +14,7 @@ namespace {
 constexpr int fwd_threads(bool layer) { return layer ? 512 : 1024; }
 // Registers a thread (the launch counts on them).
 constexpr int fwd_regs(bool layer, bool norm, int nv) {
-  return !layer ? (norm ? 64 : 48) : nv == 1 ? 64 : nv == 2 ? 88 : 128;
+  return !layer ? (norm ? 64 : 48) : nv == 1 ? 64 : nv == 2 ? 80 : 128;
 }
 
 // The same for rows whose chunks are whole and aligned: a block takes rows
@@ -31,7 +31,8 @@ constexpr int fwd_regs(bool layer, bool norm, int nv) {
 // one barrier more, and some 40 instructions a chunk and tensor (2561 columns: 23%
 // of the copy rate element by element, 50% so, 63% with a residual).
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_ring_kernel(NormFwd a) {
+__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
+    __maxnreg__(LN && ODD && NV == 2 ? 80 : 128) norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
   static_assert(NORM || !LN);
@@ -204,15 +205,20 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_ring_ker
           const int valid = in ? cols - (R.t + k * R.step) * 8 : 0;
           const float off = valid > 0 ? -mean : 0.f;     // h is 0 where there is no chunk
           const uint64_t mm = f2_pack(off, off);
+          if (!ODD || valid >= 8 || valid <= 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint64_t d = fadd2(h[k][i], mm);
-            if constexpr (ODD) {
-              float lo, hi;
-              f2_unpack(d, lo, hi);
-              d = f2_pack(2 * i < valid ? lo : 0.f, 2 * i + 1 < valid ? hi : 0.f);
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t d = fadd2(h[k][i], mm);
+              ss = ffma2(d, d, ss);
             }
-            ss = ffma2(d, d, ss);
+          } else {                                       // the row's end: the warp that has it
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float lo, hi;
+              f2_unpack(fadd2(h[k][i], mm), lo, hi);
+              const uint64_t d = f2_pack(2 * i < valid ? lo : 0.f, 2 * i + 1 < valid ? hi : 0.f);
+              ss = ffma2(d, d, ss);
+            }
           }
         }
         f2_unpack(ss, s0, s1);

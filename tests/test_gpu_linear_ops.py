@@ -543,6 +543,9 @@ def test_dropout_at_the_ends_and_of_what_is_not_finite(bl):
     x, r, st = _randn(5, 33, seed=1), _randn(5, 33, seed=2), _state(1, 2)
     assert torch.equal(bl.dropout(x, 0.0, st), x) and torch.equal(bl.dropout(x, 0.0, st, r), x + r)
     assert (bl.dropout(x, 1.0, st) == 0).all() and torch.equal(bl.dropout(x, 1.0, st, r), r)
+    # round(p 2^32) = 2^32, which no word reaches
+    big = torch.ones(2 ** 24, device="cuda")
+    assert (bl.dropout(big, 1 - 2.0 ** -34, st) == 0).all()
     keep = torch.from_numpy(OL.kept(165, 0.5, 1, 2)).view(5, 33).cuda()
     for v in (float("inf"), float("-inf"), float("nan")):
         y = bl.dropout(torch.full_like(x, v), 0.5, st)
