@@ -32,7 +32,8 @@ constexpr int fwd_regs(bool layer, bool norm, int nv) {
 // of the copy rate element by element, 50% so, 63% with a residual).
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
 __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
-    __maxnreg__(LN && ODD && NV == 2 ? 80 : 128) norm_fwd_ring_kernel(NormFwd a) {
+    __maxnreg__(LN && ODD && NV == 2 ? 80 : LPR ? 255 : 65536 / fwd_threads(LN))
+    norm_fwd_ring_kernel(NormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
   static_assert(NORM || !LN);
