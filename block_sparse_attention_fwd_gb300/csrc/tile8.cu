@@ -9,7 +9,8 @@
 // apart, so a row lies in 16 neighbouring lanes and a column in 16 threads of 8 warps.
 // The tile waits in shared memory for its second use (in registers, where the compiler
 // kept it as 64 fp32 numbers a thread, two blocks fit an SM: 16384 x 4096 bf16 to rows
-// and columns in 74 us).  Bound by HBM: x once in, a byte an element and kind out.
+// and columns in 74 us, 53 so: 75% of the copy rate, the issue slots 75% busy; rows or
+// columns alone 89 and 84%, a weight's blocks 83%).
 #include <atomic>
 #include <type_traits>
 
