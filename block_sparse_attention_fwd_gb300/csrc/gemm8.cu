@@ -20,7 +20,7 @@
 //
 // 8192^3 in 413 us, 2.66 PFLOP/s (1.4 times the measured bf16 rate of the tensor cores), in
 // bursts; run for seconds the GPU's power is the bound (2.3 PFLOP/s at 1390 W and 1810 MHz,
-// the tensor cores 57% busy).  With a scale a column, g_w, 608 us: two packed fp32
+// the tensor cores 57% busy).  With a scale a column, g_w, 600 us: two packed fp32
 // instructions for two elements of a product instead of one.  Few rows: 8 x 16384 x 16384 in
 // 45 us, the weight at 5.9 TB/s; a call of 8 x 5120 x 5120 takes 10.8, of which 4 are the
 // launch and the sum over the cluster.
@@ -210,6 +210,57 @@ struct Acc {
                                __uint_as_float(x[h][4 * k + 2 * u + 1])),
                        fmul2(cols[k], row), to);
           }
+        }
+      }
+    }
+  }
+  // COL: rows of the warp's part to `out`, whose rows are `pitch` apart and 32-byte aligned;
+  // `rows` and `cols` of them exist.  Four lanes that share a row put their pairs of four
+  // groups of 8 columns together, so that each writes one group (pair by pair, half sectors
+  // and four times the stores: g_w of 1024 tokens x 4096 x 4096 in 37 us, 32 so, of 8 x 5120 x
+  // 5120 32 and 16.5).
+  template <typename T>
+  __device__ __forceinline__ void store_groups(T* out, int64_t pitch, int rows, int cols,
+                                               int lane) const {
+    const bool odd = lane & 1, high = lane & 2;
+    auto swap = [&](auto& lo, auto& hi, bool up, int with) {  // up keeps hi, else lo
+      const auto got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, with);
+      lo = up ? got : lo;
+      hi = up ? hi : got;
+    };
+    auto gather = [&](auto (&p)[4]) {
+      swap(p[0], p[1], odd, 1);
+      swap(p[2], p[3], odd, 1);
+      swap(p[0], p[2], high, 2);
+      swap(p[1], p[3], high, 2);
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (lane >> 2) + 8 * u;
+#pragma unroll
+      for (int c = 0; c < PER; c += 32) {
+        const int col = c + (lane & 3) * 8;
+        const bool in = r < rows && col < cols;
+        T* const to = out + r * pitch + col;
+        if constexpr (sizeof(T) == 4) {
+          float x[4], y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f2_unpack(v[(c / 8 + k) * 4 + u], x[k], y[k]);
+          gather(x);
+          gather(y);
+          const float f[8] = {x[0], y[0], x[1], y[1], x[2], y[2], x[3], y[3]};
+          store8<T, true>(to, f, in ? 8 : 0);
+        } else {
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            f2_unpack(v[(c / 8 + k) * 4 + u], lo, hi);
+            const Pair<T> pair(lo, hi);
+            p[k] = *reinterpret_cast<const uint32_t*>(&pair);
+          }
+          gather(p);
+          if (in) store_words(to, p);
         }
       }
     }
@@ -491,13 +542,19 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
       } else if (g.out_j == 1) {
         T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + col;
         const int n = g.n - col;
-        if (!COL && g.wide) {
-          if (row + lane < g.m) {
+        bool whole = false;
+        if constexpr (!COL) {
+          whole = g.wide;
+          if (whole && row + lane < g.m) {
 #pragma unroll
             for (int c = 0; c < C::PER; c += 16)
               store_row<T>(out + lane * g.out_i + c, acc.v + c / 2, n - c);
           }
-        } else {
+        } else if constexpr (BN >= 128) {   // (narrower ones have their columns along out_j)
+          whole = g.wide;
+          if (whole) acc.store_groups(out, g.out_i, g.m - row, n, lane);
+        }
+        if (!whole) {
           acc.each(lane, [&](int r, int c, float lo, float hi) {
             if (row + r >= g.m) return;
             T* p = out + r * g.out_i + c;

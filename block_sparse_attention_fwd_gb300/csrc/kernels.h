@@ -175,9 +175,13 @@ cudaError_t launch_gemm8(int dtype, const Gemm8& g, cudaStream_t st);
 // bytes x `box` rows, 128-byte swizzle, out-of-range reads 0.
 bool make_codes_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t pitch,
                     int box);
-// `rows` rows of `cols` codes to rows `pitch` bytes apart.
-cudaError_t launch_repitch(const uint8_t* from, int64_t from_pitch, uint8_t* to, int64_t pitch,
-                           int64_t rows, int64_t cols, cudaStream_t st);
+// `rows` rows of `cols` codes to rows `pitch` bytes apart; of two tensors, either without rows.
+struct Repitch {
+  const uint8_t* from;
+  uint8_t* to;
+  int64_t from_pitch, pitch, rows, cols;
+};
+cudaError_t launch_repitch(const Repitch& a, const Repitch& b, cudaStream_t st);
 
 // Dropout (dropout.cu).  state: seed and offset, on the device.
 struct Dropout {

@@ -121,16 +121,21 @@ bl_status bl_matmul8(const bl_matmul8_args* p, void* stream) {
   if (need && (!p->workspace || !bl::aligned16(p->workspace) || p->workspace_bytes < need))
     return BL_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
-  for (Operand* o : {&a, &b}) {
-    if (o->packed()) continue;
-    const int64_t pitch = (o->cols + 15) / 16 * 16;
-    const size_t bytes = o->copy_bytes();
-    const cudaError_t e = bl::launch_repitch(static_cast<const uint8_t*>(o->codes), o->stride, ws,
-                                             pitch, o->rows, o->cols, st);
-    if (e != cudaSuccess) return BL_ERR_CUDA;
-    o->codes = ws;
-    o->stride = pitch;
+  bl::Repitch copies[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    Operand& o = i ? b : a;
+    if (o.packed()) continue;
+    const int64_t pitch = (o.cols + 15) / 16 * 16;
+    const size_t bytes = o.copy_bytes();
+    copies[i] = bl::Repitch{static_cast<const uint8_t*>(o.codes), ws, o.stride, pitch, o.rows,
+                            o.cols};
+    o.codes = ws;
+    o.stride = pitch;
     ws += bytes;
+  }
+  if (need) {
+    const cudaError_t e = bl::launch_repitch(copies[0], copies[1], st);
+    if (e != cudaSuccess) return BL_ERR_CUDA;
   }
   bl::Gemm8 g{};
   g.m = (int)m; g.n = (int)n; g.k = (int)k;

@@ -168,23 +168,28 @@ __global__ void __launch_bounds__(256) tile_load_kernel(TileLoad a) {
 }
 
 // Rows of codes that start anywhere to rows `pitch` bytes apart (16-byte aligned), 16 bytes
-// a thread out of the aligned words that cover them.
-__global__ void __launch_bounds__(256) repitch_kernel(const uint8_t* __restrict__ from,
-                                                      int64_t from_pitch, uint8_t* __restrict__ to,
-                                                      int64_t pitch, int64_t rows, int64_t cols) {
-  const int64_t per_row = (cols + 15) / 16, total = rows * per_row;
+// a thread out of the aligned words that cover them; two tensors in one launch, of which
+// either may have no rows.
+__global__ void __launch_bounds__(256) repitch_kernel(Repitch a, Repitch b) {
+  const int64_t row_a = (a.cols + 15) / 16, row_b = (b.cols + 15) / 16;
+  const int64_t in_a = a.rows * row_a, total = in_a + b.rows * row_b;
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += step) {
-    const int64_t row = x / per_row, col = (x - row * per_row) * 16;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(from + row * from_pitch + col);
-    const uintptr_t end = reinterpret_cast<uintptr_t>(from + row * from_pitch + cols);
+    const bool first = x < in_a;
+    const Repitch& t = first ? a : b;
+    const int64_t per_row = first ? row_a : row_b, y = first ? x : x - in_a;
+    const int64_t row = y / per_row, col = (y - row * per_row) * 16;
+    const uint8_t* const begin = t.from + row * t.from_pitch;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(begin + col);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(begin + t.cols);
     const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
     uint32_t w[5], out[4];
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = reinterpret_cast<uintptr_t>(p + i) < end ? __ldg(p + i) : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (int)(at & 3) * 8);
-    *reinterpret_cast<uint4*>(to + row * pitch + col) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(t.to + row * t.pitch + col) =
+        make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -203,11 +208,10 @@ cudaError_t allow(int bytes) {
 
 }  // namespace
 
-cudaError_t launch_repitch(const uint8_t* from, int64_t from_pitch, uint8_t* to, int64_t pitch,
-                           int64_t rows, int64_t cols, cudaStream_t st) {
-  const int64_t blocks = (rows * ((cols + 15) / 16) + 255) / 256;
-  repitch_kernel<<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, st>>>(
-      from, from_pitch, to, pitch, rows, cols);
+cudaError_t launch_repitch(const Repitch& a, const Repitch& b, cudaStream_t st) {
+  const int64_t pieces = a.rows * ((a.cols + 15) / 16) + b.rows * ((b.cols + 15) / 16);
+  const int64_t blocks = (pieces + 255) / 256;
+  repitch_kernel<<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, st>>>(a, b);
   return cudaGetLastError();
 }
 
