@@ -208,6 +208,22 @@ def test_products_of_rows_that_start_anywhere(bl, M, N, K, form):
     _check_product(_run(bl, form, a, b, torch.float32), values, "fp32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(130, 4100, 4112), (100, 1000, 1008), (3, 200, 272), (260, 4200, 4104)])
+def test_weight_gradients_of_few_tokens(bl, M, N, K, dtype):
+    """More tiles than SMs, a block or two of tokens each; rows of whole 32 bytes that end inside a
+    tile, and (4104 elements of 16 bits) rows that are not; what lies behind the result stays."""
+    a, b, values = _product(bl, "g_w", M, N, K, dtype, seed=11)
+    _check_product(_run(bl, "g_w", a, b), values, dtype)
+    from block_sparse_attention_fwd_gb300 import linear
+    t = TYPES[dtype]
+    flat = torch.full((N * K + 512,), 9.0, dtype=t, device="cuda")
+    linear._launch("bl_matmul8", flat.device, linear._MATMUL8_ARGS.pack(
+        M, N, K, a.codes.data_ptr(), a.scales.data_ptr(), a.stride, b.codes.data_ptr(), b.scales.data_ptr(),
+        b.stride, flat.data_ptr(), 0, 0, 2, ["bf16", "fp16", "fp32"].index(dtype)))
+    assert torch.equal(flat[:N * K].view(N, K), _run(bl, "g_w", a, b)) and (flat[N * K:] == 9).all()
+
+
 def test_products_keep_the_batch_dims_and_repeat(bl):
     a, b, values = _product(bl, "y", 60, 200, 256, "bf16")
     x8 = bl.Act8(a.codes.view(3, 4, 5, 256), a.scales.view(3, 4, 5, 2), 128, torch.bfloat16)
