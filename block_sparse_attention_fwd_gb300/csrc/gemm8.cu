@@ -18,9 +18,9 @@
 // the descriptors differ, so no operand is ever transposed in memory.
 // Every mbarrier wait is bounded (tc.cuh); a tile that was given up is written as NaN.
 //
-// 8192^3 in 413 us, 2.66 PFLOP/s (1.4 times the measured bf16 rate of the tensor cores), in
+// 8192^3 in 409 us, 2.69 PFLOP/s (1.4 times the measured bf16 rate of the tensor cores), in
 // bursts; run for seconds the GPU's power is the bound (2.3 PFLOP/s at 1390 W and 1810 MHz,
-// the tensor cores 57% busy).  With a scale a column, g_w, 600 us: two packed fp32
+// the tensor cores 57% busy).  With a scale a column, g_w, 590 us: two packed fp32
 // instructions for two elements of a product instead of one.  Few rows: 8 x 16384 x 16384 in
 // 45 us, the weight at 5.9 TB/s; a call of 8 x 5120 x 5120 takes 10.8, of which 4 are the
 // launch and the sum over the cluster.
@@ -150,7 +150,8 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&x)[8]) 
 // for all columns a thread has a row; with a scale a column too, four rows (r / 4 and 8, 16,
 // 24 on) of every fourth pair, so that it needs a quarter of the columns' scales: the
 // shared memory that a thread would read them from is what feeds the MMAs (8192^3: 1250
-// TFLOP/s with a row a thread).
+// TFLOP/s with a row a thread).  Its loads of 16 lanes take longer than those of 32: with them
+// y and g_x of 8192^3 take 510 us.
 template <int PER, bool COL>
 struct Acc {
   uint64_t v[PER / 2];
@@ -214,54 +215,96 @@ struct Acc {
       }
     }
   }
-  // COL: rows of the warp's part to `out`, whose rows are `pitch` apart and 32-byte aligned;
-  // `rows` and `cols` of them exist.  Four lanes that share a row put their pairs of four
-  // groups of 8 columns together, so that each writes one group (pair by pair, half sectors
-  // and four times the stores: g_w of 1024 tokens x 4096 x 4096 in 37 us, 32 so, of 8 x 5120 x
-  // 5120 32 and 16.5).
+  // Rows of the warp's part to `out`, whose rows are `pitch` apart and 32-byte aligned; `rows`
+  // and `cols` of them exist.  Four neighbouring lanes exchange what they hold of 32 columns,
+  // so that they write four groups of 8 columns of a row side by side.  (As the lanes have
+  // them: with a scale a column pairs, half sectors and four times the stores, g_w of 1024
+  // tokens x 4096 x 4096 in 37 us, 32 so, of 8 x 5120 x 5120 32 and 16.5; else a sector of each
+  // of 32 rows a store, 32779 x 2880 x 48 to fp32 in 94 us, 68 so.)
   template <typename T>
-  __device__ __forceinline__ void store_groups(T* out, int64_t pitch, int rows, int cols,
-                                               int lane) const {
+  __device__ __forceinline__ void store(T* out, int64_t pitch, int rows, int cols,
+                                        int lane) const {
     const bool odd = lane & 1, high = lane & 2;
-    auto swap = [&](auto& lo, auto& hi, bool up, int with) {  // up keeps hi, else lo
+    auto swap = [](auto& lo, auto& hi, bool up, int with) {  // up keeps hi, else lo
       const auto got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, with);
       lo = up ? got : lo;
       hi = up ? hi : got;
     };
-    auto gather = [&](auto (&p)[4]) {
-      swap(p[0], p[1], odd, 1);
-      swap(p[2], p[3], odd, 1);
-      swap(p[0], p[2], high, 2);
-      swap(p[1], p[3], high, 2);
+    // p[k] of the four lanes' lane l to p[l] of lane k
+    auto exchange = [&](auto& p0, auto& p1, auto& p2, auto& p3) {
+      swap(p0, p1, odd, 1);
+      swap(p2, p3, odd, 1);
+      swap(p0, p2, high, 2);
+      swap(p1, p3, high, 2);
     };
+    auto halves = [](uint64_t x) {                       // a pair in 16 bits each
+      float lo, hi;
+      f2_unpack(x, lo, hi);
+      const Pair<T> p(lo, hi);
+      return *reinterpret_cast<const uint32_t*>(&p);
+    };
+    if constexpr (COL) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (lane >> 2) + 8 * u;
+      for (int u = 0; u < 4; ++u) {
+        const int r = (lane >> 2) + 8 * u;
+#pragma unroll
+        for (int c = 0; c < PER; c += 32) {
+          const int col = c + (lane & 3) * 8;
+          const bool in = r < rows && col < cols;
+          T* const to = out + r * pitch + col;
+          if constexpr (sizeof(T) == 4) {
+            float x[4], y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f2_unpack(v[(c / 8 + k) * 4 + u], x[k], y[k]);
+            exchange(x[0], x[1], x[2], x[3]);
+            exchange(y[0], y[1], y[2], y[3]);
+            const float f[8] = {x[0], y[0], x[1], y[1], x[2], y[2], x[3], y[3]};
+            store8<T, true>(to, f, in ? 8 : 0);
+          } else {
+            uint32_t p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = halves(v[(c / 8 + k) * 4 + u]);
+            exchange(p[0], p[1], p[2], p[3]);
+            if (in) store_words(to, p);
+          }
+        }
+      }
+    } else if constexpr (sizeof(T) == 4 && PER < 128) {
+      // (exchanging costs registers that these tiles' few have not: 128 x 5120 x 5120 in 16.3 us
+      // instead of 14.4)
+      if (lane < rows) {
+#pragma unroll
+        for (int c = 0; c < PER; c += 8) {
+          const uint64_t f[4] = {v[c / 2], v[c / 2 + 1], v[c / 2 + 2], v[c / 2 + 3]};
+          if (c < cols) store8(out + lane * pitch + c, f);
+        }
+      }
+    } else {
+      constexpr int W = 2 * (int)sizeof(T);              // words of 8 elements
+      T* const mine = out + (lane & ~3) * pitch + (lane & 3) * 8;
 #pragma unroll
       for (int c = 0; c < PER; c += 32) {
-        const int col = c + (lane & 3) * 8;
-        const bool in = r < rows && col < cols;
-        T* const to = out + r * pitch + col;
-        if constexpr (sizeof(T) == 4) {
-          float x[4], y[4];
+        uint32_t w[4][W];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f2_unpack(v[(c / 8 + k) * 4 + u], x[k], y[k]);
-          gather(x);
-          gather(y);
-          const float f[8] = {x[0], y[0], x[1], y[1], x[2], y[2], x[3], y[3]};
-          store8<T, true>(to, f, in ? 8 : 0);
-        } else {
-          uint32_t p[4];
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            f2_unpack(v[(c / 8 + k) * 4 + u], lo, hi);
-            const Pair<T> pair(lo, hi);
-            p[k] = *reinterpret_cast<const uint32_t*>(&pair);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t x = v[c / 2 + k * 4 + i];
+            if constexpr (sizeof(T) == 4) {
+              float lo, hi;
+              f2_unpack(x, lo, hi);
+              w[k][2 * i] = __float_as_uint(lo);
+              w[k][2 * i + 1] = __float_as_uint(hi);
+            } else {
+              w[k][i] = halves(x);
+            }
           }
-          gather(p);
-          if (in) store_words(to, p);
-        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) exchange(w[0][i], w[1][i], w[2][i], w[3][i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((lane & ~3) + k < rows && c + (lane & 3) * 8 < cols)
+            store_words(mine + k * pitch + c, w[k]);
       }
     }
   }
@@ -288,23 +331,6 @@ __device__ __forceinline__ void tile_at(int t, int ti, int tj, int& i, int& j) {
   const int h = min(GROUP, ti - g * GROUP);
   j = r / h;
   i = g * GROUP + (r - j * h);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_row(T* p, const uint64_t* acc, int n) {
-  if (n >= 16) {
-    float f[2][8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f2_unpack(acc[c], f[c / 4][2 * (c % 4)], f[c / 4][2 * (c % 4) + 1]);
-    store16<T, true>(p, f);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float lo, hi;
-      f2_unpack(acc[c / 2], lo, hi);
-      if (c < n) p[c] = from_f32<T>(c % 2 ? hi : lo);
-    }
-  }
 }
 
 // COL: every column has a scale of its own; else every 128 share one.
@@ -543,16 +569,9 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
         T* out = static_cast<T*>(g.out) + (int64_t)row * g.out_i + col;
         const int n = g.n - col;
         bool whole = false;
-        if constexpr (!COL) {
+        if constexpr (C::PER >= 32) {
           whole = g.wide;
-          if (whole && row + lane < g.m) {
-#pragma unroll
-            for (int c = 0; c < C::PER; c += 16)
-              store_row<T>(out + lane * g.out_i + c, acc.v + c / 2, n - c);
-          }
-        } else if constexpr (BN >= 128) {   // (narrower ones have their columns along out_j)
-          whole = g.wide;
-          if (whole) acc.store_groups(out, g.out_i, g.m - row, n, lane);
+          if (whole) acc.store(out, g.out_i, g.m - row, n, lane);
         }
         if (!whole) {
           acc.each(lane, [&](int r, int c, float lo, float hi) {
