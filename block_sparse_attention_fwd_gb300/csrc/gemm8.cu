@@ -447,12 +447,12 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
           mma_commit(&bars.empty[s]);
           mma_commit(&bars.t_full[b]);
         }
-        if (it < total) {
-          fail();
-          // nothing may be in flight when the CTA ends: its MMAs, and then the copies
-          const int last = it - C::ISSUERS;
-          if (last >= 0) mbar_wait_poll(&bars.t_full[last % C::NB], (last / C::NB) & 1);
-        }
+        if (it < total) fail();
+        // Nothing may be in flight when the CTA ends: the MMAs, and then the copies.  An issuer
+        // that has issued all of its blocks waits too: the warps that give up may be the
+        // accumulating ones, with its last products still under way.
+        const int last = it - C::ISSUERS;
+        if (last >= 0) mbar_wait_poll(&bars.t_full[last % C::NB], (last / C::NB) & 1);
       }
     } else {
       // Scales that lie side by side come 16 bytes a lane, others by pointers that walk with
