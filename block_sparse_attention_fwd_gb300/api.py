@@ -354,7 +354,14 @@ class BLDropout(torch.nn.Module):
     residual behind it.  Every call in training takes the next offset of ``state``, an
     int64 buffer (seed, offset) on the device: a captured graph draws anew with every
     replay, and a saved state brings the same masks back.  ``seed`` None draws one.
-    Out of training, and with p = 0, nothing is dropped."""
+    Out of training, and with p = 0, nothing is dropped.
+
+    ``used`` is a call's state drawn in advance, ``used = dropout_next(drop.state)``; the
+    call then leaves ``state`` as it is.  A forward that the backward runs again
+    (``torch.utils.checkpoint`` and its like) needs it, drawn outside of what is run again
+    and passed in, so that both runs drop the same places:
+    ``checkpoint(lambda x, used: drop(x, used=used), x, dropout_next(drop.state))``.
+    Within a backward a call without it is refused, as its mask would be another one."""
 
     def __init__(self, p: float = 0.1, seed: int | None = None, device=None):
         super().__init__()
@@ -367,12 +374,20 @@ class BLDropout(torch.nn.Module):
         self.p = float(p)
         self.register_buffer("state", torch.tensor([seed, 0], dtype=torch.int64, device=device))
 
-    def forward(self, x, residual=None):
+    def forward(self, x, residual=None, used=None):
         if not self.training or self.p == 0.0:
             return x if residual is None else x + residual
+        if used is None:
+            if torch._C._current_graph_task_id() != -1:
+                raise RuntimeError(
+                    "a forward that a backward runs again needs the state of its first run: "
+                    "draw used = dropout_next(drop.state) outside and call drop(x, used=used)")
+            used = linear.dropout_next(self.state)
+        elif used.data_ptr() == self.state.data_ptr():
+            raise ValueError("used is the state that goes on: pass dropout_next(drop.state)")
         x, residual = (t if t is None or ops.row_stride(t) is not None else t.contiguous()
                        for t in (x, residual))
-        return _DropoutFn.apply(x, residual, self.p, linear.dropout_next(self.state))
+        return _DropoutFn.apply(x, residual, self.p, used)
 
 
 class _Linear8Fn(torch.autograd.Function):

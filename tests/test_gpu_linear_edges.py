@@ -1,10 +1,11 @@
 """The linear layers around the attention where they may go wrong: waits that run out in
-products of few blocks.  Inputs, tolerances and the oracle are those of
-test_gpu_linear_ops.py."""
+products of few blocks, dropout in forwards that the backward runs again.  Inputs,
+tolerances and the oracle are those of test_gpu_linear_ops.py."""
 import pytest
 import torch
 
-from tests.test_gpu_linear_ops import _product, _run, bl, built  # noqa: F401
+from oracle import linear as OL
+from tests.test_gpu_linear_ops import _product, _randn, _run, bl, built  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,71 @@ def test_product_of_few_blocks_whose_waits_run_out(bl, form, M, N, K):  # noqa: 
         for got in left:
             assert (torch.isnan(got) | (got == want)).all()
         assert torch.equal(_run(bl, form, a, b), want)
+
+
+# --- dropout ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_dropout_in_a_forward_that_is_run_again(bl, reentrant):  # noqa: F811
+    """Under either kind of recomputation, with the call's state passed in, gradients are those of
+    the same layers without it; without the state the backward is refused."""
+    from torch.utils.checkpoint import checkpoint
+    lin = bl.BLLinear8(256, 192, device="cuda", dtype=torch.bfloat16)
+    drop = bl.BLDropout(0.4, seed=11, device="cuda")
+    out = bl.BLLinear8(192, 256, device="cuda", dtype=torch.bfloat16)
+    x = _randn(50, 256, dtype=torch.bfloat16, seed=1).requires_grad_()
+    g = _randn(50, 256, dtype=torch.bfloat16, seed=2)
+    leaves = [x, lin.weight, out.weight]
+
+    def layers(x, used=None):
+        return out(drop(lin(x), used=used))
+
+    def gradients(y):
+        for t in leaves:
+            t.grad = None
+        y.backward(g)
+        return [t.grad for t in leaves]
+
+    for call in range(2):
+        used = bl.dropout_next(drop.state)
+        y = checkpoint(layers, x, used, use_reentrant=reentrant)
+        got = gradients(y)
+        drop.state[1] -= 1
+        plain = layers(x)
+        want = gradients(plain)
+        assert drop.state.tolist() == [11, call + 1]
+        assert torch.equal(y, plain)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    y = checkpoint(layers, x, use_reentrant=reentrant)
+    with pytest.raises(RuntimeError, match="dropout_next"):
+        y.backward(g)
+
+
+def test_dropout_run_again_replays_from_a_graph(bl):  # noqa: F811
+    """A captured step with a recomputed forward: every replay draws anew, once, and its gradient
+    has the mask of its output."""
+    from torch.utils.checkpoint import checkpoint
+    drop = bl.BLDropout(0.5, seed=4, device="cuda")
+    x, g = _randn(33, 40, seed=1).requires_grad_(), _randn(33, 40, seed=2)
+
+    def step():
+        used = bl.dropout_next(drop.state)
+        y = checkpoint(lambda x, used: drop(x, used=used) * 3, x, used, use_reentrant=False,
+                       preserve_rng_state=False)
+        return y.detach(), torch.autograd.grad(y, x, g)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, gx = step()
+    for call in range(1, 4):
+        graph.replay()
+        torch.cuda.synchronize()
+        keep = torch.from_numpy(OL.kept(x.numel(), 0.5, 4, call)).view(x.shape).cuda()
+        assert torch.equal(y != 0, keep) and torch.equal(gx != 0, keep)
+        assert drop.state.tolist() == [4, call + 1]
