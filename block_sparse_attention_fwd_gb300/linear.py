@@ -337,4 +337,6 @@ def dropout_next(state):
     _state(state)
     used = torch.empty_like(state)
     _launch("bl_dropout_next", state.device, state.data_ptr(), used.data_ptr())
+    if not state.is_inference():           # what autograd holds of it is stale now
+        torch.autograd.graph.increment_version(state)
     return used

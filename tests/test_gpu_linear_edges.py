@@ -101,3 +101,19 @@ def test_dropout_run_again_replays_from_a_graph(bl):  # noqa: F811
         keep = torch.from_numpy(OL.kept(x.numel(), 0.5, 4, call)).view(x.shape).cuda()
         assert torch.equal(y != 0, keep) and torch.equal(gx != 0, keep)
         assert drop.state.tolist() == [4, call + 1]
+
+
+def test_a_state_that_went_on_is_not_read_by_a_backward(bl):  # noqa: F811
+    """A call given a tensor that dropout_next then moves on: its backward would form another mask,
+    and is refused as after any change in place."""
+    drop = bl.BLDropout(0.5, seed=4, device="cuda")
+    x = _randn(8, 40, seed=1).requires_grad_()
+    mine = torch.tensor([4, 7], device="cuda")
+    y = drop(x, used=mine)
+    bl.dropout_next(mine)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    drop(x, used=mine).sum().backward()
+    with torch.inference_mode():
+        state = torch.tensor([4, 7], device="cuda")
+        assert bl.dropout_next(state).tolist() == [4, 7] and state.tolist() == [4, 8]
