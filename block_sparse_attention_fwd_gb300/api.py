@@ -352,9 +352,15 @@ class BLDropout(torch.nn.Module):
     """Dropout whose mask is a function of (seed, offset) and the element's place and is
     formed again in the backward.  ``drop(x)`` or ``drop(x, residual)``, which adds the
     residual behind it.  Every call in training takes the next offset of ``state``, an
-    int64 buffer (seed, offset) on the device: a captured graph draws anew with every
+    int64 tensor (seed, offset) on the device: a captured graph draws anew with every
     replay, and a saved state brings the same masks back.  ``seed`` None draws one.
     Out of training, and with p = 0, nothing is dropped.
+
+    ``state`` moves with the module and is in its ``state_dict``, but it is none of its
+    buffers: data-parallel wrappers send rank 0's buffers to all ranks with every forward,
+    which would have all ranks drop the same places.  Ranks drop different ones where their
+    seeds differ, and so do layers: a copy (``copy.deepcopy``) has the state of what it was
+    copied from, and needs a seed of its own (``drop.state[0] = seed``) to drop others.
 
     ``used`` is a call's state drawn in advance, ``used = dropout_next(drop.state)``; the
     call then leaves ``state`` as it is.  A forward that the backward runs again
@@ -372,7 +378,33 @@ class BLDropout(torch.nn.Module):
         if seed is None:
             seed = int(torch.randint(2 ** 63 - 1, ()))
         self.p = float(p)
-        self.register_buffer("state", torch.tensor([seed, 0], dtype=torch.int64, device=device))
+        self.state = torch.tensor([seed, 0], dtype=torch.int64, device=device)
+
+    def _apply(self, fn, *args, **kwargs):
+        super()._apply(fn, *args, **kwargs)
+        self.state = fn(self.state)
+        return self
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        destination[prefix + "state"] = self.state if keep_vars else self.state.detach()
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
+                              unexpected_keys, error_msgs):
+        name, unexpected = prefix + "state", []
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys,
+                                      unexpected, error_msgs)
+        unexpected_keys += [k for k in unexpected if k != name]
+        state = state_dict.get(name)
+        if state is None:
+            if strict:
+                missing_keys.append(name)
+        elif state.dtype != torch.int64 or state.shape != (2,):
+            error_msgs.append(f"{name} must be two int64, got {state.dtype} {tuple(state.shape)}")
+        elif local_metadata.get("assign_to_params_buffers", False):
+            self.state = state.detach()
+        else:
+            self.state.copy_(state)
 
     def forward(self, x, residual=None, used=None):
         if not self.training or self.p == 0.0:
