@@ -65,22 +65,22 @@ __global__ void __launch_bounds__(512) __maxnreg__(NV == 1 ? 72 : 96)
           *reinterpret_cast<const uint4*>(ring + at + t * 16 + v * nt * 16);
     return c;
   };
-  // (h - mean) rstd, base = -mean rstd
-  auto load_u = [&](int place, int k, float scale, float rstd, float base, uint64_t (&u)[4]) {
-    const uint64_t bb = f2_pack(base, base);
+  // (h - mean) rstd
+  auto load_u = [&](int place, int k, float scale, float rstd, float mean, uint64_t (&u)[4]) {
+    const uint64_t rr = f2_pack(rstd, rstd), mm = f2_pack(-mean, -mean);
     if constexpr (FMT == 0) {
-      const uint64_t rr = f2_pack(rstd, rstd);
       unpack2(chunk(place + h_plane + k * nt * CB), u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = ffma2(u[i], rr, bb);
+      for (int i = 0; i < 4; ++i) u[i] = fmul2(fadd2(u[i], mm), rr);
     } else {
       const uint2 raw =
           *reinterpret_cast<const uint2*>(ring + place + h_plane + k * nt * 8 + t * 8);
       float f[8];
       decode8<FMT>(Codes{{raw.x, raw.y}}, f);
-      const uint64_t rr = f2_pack(scale * rstd, scale * rstd);
+      const uint64_t ss = f2_pack(scale, scale);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = ffma2(f2_pack(f[2 * i], f[2 * i + 1]), rr, bb);
+      for (int i = 0; i < 4; ++i)
+        u[i] = fmul2(ffma2(f2_pack(f[2 * i], f[2 * i + 1]), ss, mm), rr);
     }
   };
   int64_t left = a.rows - first;                        // rows from this one on
@@ -115,14 +115,13 @@ __global__ void __launch_bounds__(512) __maxnreg__(NV == 1 ? 72 : 96)
       scales += gridDim.x * a.groups;
     }
     copy_wait<S - 1>();
-    const float base = -mean * rstd;
     uint64_t wg[NV][4], dot = 0, all = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!has[k]) continue;
       uint64_t g[4], u[4];
       unpack2(chunk(place + k * nt * CB), g);
-      load_u(place, k, FMT ? scale[k] : 0.f, rstd, base, u);
+      load_u(place, k, FMT ? scale[k] : 0.f, rstd, mean, u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[k][i] = ffma2(g[i], u[i], acc[k][i]);
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(512) __maxnreg__(NV == 1 ? 72 : 96)
     for (int k = 0; k < NV; ++k) {
       if (!has[k]) continue;
       uint64_t g[4];
-      load_u(place, k, FMT ? scale[k] : 0.f, rstd, base, g);
+      load_u(place, k, FMT ? scale[k] : 0.f, rstd, mean, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = fadd2(ffma2(g[i], cc, ff), wg[k][i]);
       if constexpr (GH) {

@@ -201,13 +201,12 @@ __global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV))
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
       }
-      const float base = -mean * rstd;                   // rounded like the mean itself
-      const uint64_t rr = f2_pack(rstd, rstd), bb = f2_pack(base, base);
+      const uint64_t rr = f2_pack(rstd, rstd), mm = f2_pack(-mean, -mean);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          h[rb][k][i] = ffma2(ffma2(h[rb][k][i], rr, bb), w[k][i], b[k][i]);
+          h[rb][k][i] = ffma2(fmul2(fadd2(h[rb][k][i], mm), rr), w[k][i], b[k][i]);
         if ((FMT8 == 0 || a.y) && in && has[k]) store8(py + rb * cols + k * nt * 8, h[rb][k]);
         if constexpr (FMT8 != 0) {
           float f[8];

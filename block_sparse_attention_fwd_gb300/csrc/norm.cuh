@@ -166,6 +166,13 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float (*buf)[64], int& slot
   return v;
 }
 
+// sum / n, inv = fl(1 / n), to within a rounding: a row of one number whose sum is exact has
+// that number for its mean, and what is taken from it leaves 0.
+__device__ __forceinline__ float mean_of(float sum, float inv, float n) {
+  const float mean = sum * inv;
+  return fmaf(fmaf(-mean, n, sum), inv, mean);
+}
+
 // Lanes a row (0: the block), chunks a thread and threads of a launch over rows
 // of `cols` columns.  Up to warp_chunks chunks a warp holds whole rows and needs
 // no barrier; beyond, a block of as few threads as hold the row with two chunks

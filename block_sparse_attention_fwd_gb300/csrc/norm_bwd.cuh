@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) norm_bwd_kernel(NormBwd a) {
       const float s = valid > 0 ? a.scales[row * a.groups + (col >> a.shift)] : 0.f;
       decode8(a.fmt, c, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = (LN ? u[i] * s - mean : u[i] * s) * rstd;
+      for (int i = 0; i < 8; ++i) u[i] = (LN ? fmaf(u[i], s, -mean) : u[i] * s) * rstd;
     }
   };
   for (int64_t row0 = (int64_t)blockIdx.x * R.here; row0 < a.rows;

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
         // hold; over the block the parts' means are put right, so one barrier does
         constexpr int W = LPR ? LPR : 32;
         sum = lanes_sum(sum, W);
-        mean = sum * inv_part;
+        mean = LPR ? mean_of(sum, inv_part, (float)cols) : sum * inv_part;
         ss = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
           __syncthreads();
           const float part = lane < warps ? buf[slot][lane] : 0.f;
           squares = lane < warps ? buf[slot][32 + lane] : 0.f;
-          mean = lanes_sum(part, 32) * inv_cols;
+          mean = mean_of(lanes_sum(part, 32), inv_cols, (float)cols);
           const float off = part * inv_lane - mean;      // of the mean of warp `lane`
           squares = lanes_sum(fmaf(off * off, n_lane, squares), 32);
           slot ^= 1;
@@ -243,15 +243,13 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
       }
       const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
       if (R.t == 0 && in && a.rstd) a.rstd[row] = rstd;
-      const uint64_t rr = f2_pack(rstd, rstd);
-      const float base = -mean * rstd;                   // rounded like the mean itself
-      const uint64_t bb = f2_pack(base, base);
+      const uint64_t rr = f2_pack(rstd, rstd), mm = f2_pack(-mean, -mean);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const bool has = in && (R.t + k * R.step) * 8 < cols;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          h[k][i] = LN ? ffma2(ffma2(h[k][i], rr, bb), w[k][i], b[LN ? k : 0][i])
+          h[k][i] = LN ? ffma2(fmul2(fadd2(h[k][i], mm), rr), w[k][i], b[LN ? k : 0][i])
                        : fmul2(fmul2(h[k][i], rr), w[k][i]);
         if (a.y) write(a.y, k, h[k], has);
       }
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_kernel(N
     }
     float ss = row_sum<LPR>(s0 + s1, buf, slot);
     if constexpr (LN) {
-      const float mean = ss * inv_cols;
+      const float mean = mean_of(ss, inv_cols, (float)cols);
       if (R.t == 0 && in && a.mean) a.mean[row] = mean;
       s0 = s1 = 0.f;
 #pragma unroll

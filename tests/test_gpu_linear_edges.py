@@ -1,11 +1,13 @@
 """The linear layers around the attention where they may go wrong: waits that run out in
-products of few blocks, dropout in forwards that the backward runs again.  Inputs,
-tolerances and the oracle are those of test_gpu_linear_ops.py."""
+products of few blocks, norms of rows far from zero, dropout in forwards that the backward
+runs again.  Inputs, tolerances and the oracle are those of test_gpu_linear_ops.py where
+nothing else is said."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import linear as OL
-from tests.test_gpu_linear_ops import _product, _randn, _run, bl, built  # noqa: F401
+from tests.test_gpu_linear_ops import TYPES, F, _close, _f64, _product, _randn, _run, bl, built  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +35,86 @@ def test_product_of_few_blocks_whose_waits_run_out(bl, form, M, N, K):  # noqa: 
         for got in left:
             assert (torch.isnan(got) | (got == want)).all()
         assert torch.equal(_run(bl, form, a, b), want)
+
+
+# --- layer norm ------------------------------------------------------------------
+
+FAR = [1, 24, 128, 200, 520, 1000, 1001, 1024, 2561, 4096, 5120, 8192, 8200, 12288, 16383]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cols", FAR)
+def test_layer_norm_of_one_number(bl, cols, dtype):  # noqa: F811
+    """Rows of one number c whose sum is exact in fp32 (at most 11 bits times 2^14): the mean is c,
+    y the bias, and g_w 0; whatever the width, the alignment and the output."""
+    t = TYPES[dtype]
+    c = torch.tensor([1000.0, -0.75, 3.0, 0.0, 40.0], dtype=t, device="cuda")
+    wide = torch.zeros(5, cols + 16, dtype=t, device="cuda")
+    w, b = 1 + 0.3 * _randn(cols, seed=1), 0.3 * _randn(cols, seed=2)
+    for off in (0, 1, 8):
+        x = wide[:, off:off + cols]
+        x.copy_(c[:, None].expand(5, cols))
+        for weight, bias in ((w, b), (None, None), (w.to(t), b.to(t))):
+            y, _, mean, rstd = bl.layer_norm_fwd(x, weight, bias)
+            want = torch.zeros_like(y) if bias is None else bias.to(t).expand(5, cols)
+            assert torch.equal(y, want) and torch.equal(mean, c.float())
+            assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-3)
+            for group in (128, 0):
+                y8 = bl.layer_norm_fwd_8bit(x, weight, bias, group=group)[0]
+                # the codes of the bias, the same in every row
+                assert (y8.codes.view(torch.uint8) == y8.codes.view(torch.uint8)[:1]).all()
+                assert bias is not None or (y8.codes.float() == 0).all()
+    g = _randn(5, cols, dtype=t, seed=3)
+    for weight in (None, w):
+        _, gw, _ = bl.layer_norm_bwd(g, x.contiguous(), mean, rstd, weight)
+        assert (gw == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cols", FAR)
+def test_layer_norm_takes_the_mean_away_first(bl, cols, dtype):  # noqa: F811
+    """y from the mean and rstd that are returned: one rounding each of h - mean, of its product
+    with rstd and of the last multiply-add, whatever the mean is."""
+    t = TYPES[dtype]
+    wide = torch.zeros(6, cols + 16, dtype=t, device="cuda")
+    w, b = 1 + 0.3 * _randn(cols, seed=1), 0.3 * _randn(cols, seed=2)
+    for off in (0, 3):
+        x = wide[:, off:off + cols]
+        x.copy_(1000 + 4 * _randn(6, cols, seed=cols))
+        for weight, bias in ((w, b), (None, None)):
+            y, _, mean, rstd = bl.layer_norm_fwd(x, weight, bias)
+            u = (_f64(x) - _f64(mean)[:, None]) * _f64(rstd)[:, None]
+            wv, bv = (1.0, 0.0) if weight is None else (_f64(weight), _f64(bias))
+            _close(y, u * wv + bv, 4 * F * (np.abs(u * wv) + np.abs(bv)), t)
+
+
+@pytest.mark.parametrize("saved", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cols", FAR)
+def test_layer_norm_backward_of_rows_far_from_zero(bl, cols, dtype, saved):  # noqa: F811
+    """Of the mean and rstd that it is given: u carries 3 F of itself (h - mean and the product,
+    or the multiply-add of a code), whatever the mean is."""
+    t = TYPES[dtype]
+    rows = 40
+    x = (1000 + 4 * _randn(rows, cols, seed=cols)).to(t)
+    _, _, mean, rstd = bl.layer_norm_fwd(x, None, None)
+    h = x if saved is None else bl.act_save(x, saved, 128)
+    hv = _f64(x)
+    if saved is not None:                                # code times scale, unrounded
+        hv = _f64(h.codes.float()) * np.repeat(_f64(h.scales), 128, 1)[:, :cols]
+    g, w = _randn(rows, cols, dtype=t, seed=8), 1 + 0.3 * _randn(cols, seed=9)
+    gx, gw, gb = bl.layer_norm_bwd(g, h, mean, rstd, w)
+    rx, rw, rb = OL.layer_norm_backward(g, hv, mean, rstd, w)
+    s = _f64(rstd)[:, None]
+    u = np.abs((hv - _f64(mean)[:, None]) * s)
+    du = 3 * F * u
+    gv = np.abs(_f64(g))
+    wg = gv * _f64(w)
+    c, dc = (wg * u).mean(1, keepdims=True), (wg * du).mean(1, keepdims=True)
+    terms = s * (wg + wg.mean(1, keepdims=True) + u * c)
+    _close(gx, rx, 64 * F * terms + s * (du * c + u * dc + du * dc), t)
+    _close(gw, rw, (rows + 64) * F * (gv * u).sum(0) + (gv * du).sum(0), torch.float32)
+    _close(gb, rb, (rows + 64) * F * gv.sum(0), torch.float32)
 
 
 # --- dropout ---------------------------------------------------------------------
