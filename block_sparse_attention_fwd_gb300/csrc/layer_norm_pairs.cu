@@ -19,9 +19,12 @@ constexpr int pair_regs(int nv) { return nv == 1 ? 64 : 96; }
 // time, 102 so, 97% of the copy rate; with the residual 196, 101%; to e4m3 181, 96%).  A
 // row's mean and squares come from one round of shuffles: each warp sums
 // distances from the mean of its first lane's elements, and the squares around its own mean
-// follow by sum d^2 - (sum d)^2 / n, which takes away at most a few times what is left, as
-// the pivot is the mean of 8 elements or more out of 512 at most; the warps' means are put
-// together likewise, around the first warp's.
+// follow by sum d^2 - (sum d)^2 / n.  With a pivot p that is the mean of k of the n elements,
+// whose mean is m, (sum d)^2 / n = n (p - m)^2, and what is left, at least k n / (n - k)
+// (p - m)^2, is at most n / k - 1 = 31 times smaller (the k of one value, the others of
+// another).  The warps' means are put together likewise, around the first warp's, which holds
+// as many elements as any other of 16: at most 15 times.  So the squares, summed to within
+// 64 2^-24 of themselves, give the variance within 64 (32 + 16) 2^-24 at worst, 2e-4.
 // FULL: every thread has all of its chunks.
 template <typename T, int NV, int RB, int FMT8, bool RES, bool FULL>
 __global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV))

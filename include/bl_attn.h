@@ -497,7 +497,8 @@ bl_status bl_matmul8(const bl_matmul8_args* args, void* stream);
  * rstd = 1 / sqrt(mean((h - m)^2) + eps), y = (h - m) rstd weight + bias, row by
  * row.  Arguments as bl_rms_norm_fwd's; weight and bias [cols] have the same type,
  * either may be NULL (ones, zeros); mean and rstd [rows] fp32 for the backward may
- * be NULL.  The squares are summed of the centred row. */
+ * be NULL.  The squares are summed of distances from a mean of some of the row's
+ * elements and put right, so a row far from zero loses nothing by it. */
 typedef struct {
   int64_t rows, cols, x_stride, residual_stride;
   const void* x;

@@ -117,6 +117,33 @@ def test_layer_norm_backward_of_rows_far_from_zero(bl, cols, dtype, saved):  # n
     _close(gb, rb, (rows + 64) * F * gv.sum(0), torch.float32)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [768, 1024, 2048, 4096, 5120, 8192])
+def test_layer_norm_of_rows_that_begin_with_outliers(bl, cols, dtype):  # noqa: F811
+    """Rows whose first 8 elements, whose first lane's 16 and whose first warp's elements stand
+    apart from the rest: the pivots of the sums of squares are as far off as they can be.  Of a
+    sum within 64 F of itself, 31 parts in 32 go where a warp's elements are put right and 15 in
+    16 over the warps: the variance within 64 (32 + 16) F, rstd within half of that; 1600 F with
+    what the mean adds."""
+    t = TYPES[dtype]
+    threads = (cols // 8 + (0 if cols <= 1024 else 1)) // (1 if cols <= 1024 else 2)
+    threads = -(-threads // 32) * 32
+    where = torch.zeros(5, cols, dtype=torch.bool, device="cuda")
+    where[0, :8] = where[1, :8] = where[2, :256] = where[3, -8:] = True
+    if cols > 1024:                                      # a lane's second chunk
+        where[1, threads * 8:threads * 8 + 8] = where[2, threads * 8:threads * 8 + 256] = True
+    for apart, spread in ((1.0, 1e-3), (-300.0, 1.0), (1.0, 0.0)):
+        x = (spread * _randn(5, cols, seed=cols) + apart * where).to(t)
+        y, _, mean, rstd = bl.layer_norm_fwd(x, None, None, 0.0 if spread else 1e-5)
+        ry, _, rm, rs = OL.layer_norm(x, None, None, 0.0 if spread else 1e-5)
+        xv = _f64(x)
+        _close(mean, rm, 64 * F * np.abs(xv).mean(1), torch.float32)
+        rows = slice(0, 5) if spread else slice(0, 4)    # the last row without a spread is zeros
+        _close(rstd[rows], rs[rows], 1600 * F * rs[rows], torch.float32)
+        off = (64 * F * np.abs(xv).mean(1, keepdims=True) + 2 * F * np.abs(xv)) * rs[:, None]
+        _close(y, ry, off + 1600 * F * np.abs(ry), t)
+
+
 # --- dropout ---------------------------------------------------------------------
 
 @pytest.mark.parametrize("reentrant", [False, True])
