@@ -469,8 +469,9 @@ bl_status bl_tile8_load(int64_t rows, int64_t cols, int dtype, const void* codes
  * the blocks' sums, times the product of their two scales, in fp32 in the blocks'
  * order (in a few parts of it, each in order, where few tiles share a sum); the
  * result is rounded once, to out_dtype.  The product of two scales is an fp32
- * number: below 2^-126 it loses bits, beyond 2^128 it is infinite.  A block
- * whose scale is NaN makes what it reaches NaN.  tokens = 0 gives g_w = 0.
+ * number: below 2^-126 it loses bits, beyond 2^128 it is infinite, and the block's
+ * part too, or NaN where its codes' products sum to 0.  A block whose scale is NaN
+ * makes what it reaches NaN.  tokens = 0 gives g_w = 0.
  * Where a code tensor's rows are not 16-byte aligned, the call copies it to the
  * workspace first (bl_matmul8_workspace_bytes, which reads everything but `out`
  * and the workspace; 16-byte aligned).  When a device-side wait gives up

@@ -37,6 +37,27 @@ def test_product_of_few_blocks_whose_waits_run_out(bl, form, M, N, K):  # noqa: 
         assert torch.equal(_run(bl, form, a, b), want)
 
 
+@pytest.mark.parametrize("M", [5, 300])
+def test_products_of_scales_beyond_fp32(bl, M):  # noqa: F811
+    """Scales whose product is beyond 2^128: infinite where the block's codes have a sum, NaN where
+    they have none; other blocks, and products of as large a scale with a small one, are right."""
+    N, K = 256, 256
+    codes = torch.ones(M, K, device="cuda")
+    codes[1] = 0
+    codes = codes.to(torch.float8_e4m3fn)
+    ones = torch.ones(N, K, device="cuda").to(torch.float8_e4m3fn)
+    sa = torch.full((M, 2), 2.0 ** 70, device="cuda")
+    sa[3] = 1.0
+    sb = torch.full((2, 2), 2.0 ** -70, device="cuda")
+    sb[1] = 2.0 ** 70
+    y = bl.matmul8(bl.Act8(codes, sa, 128, torch.float32), bl.Weight8(ones, sb, torch.float32))
+    assert torch.isnan(y[1, 128:]).all() and (y[1, :128] == 0).all()
+    assert (y[3, :128] == 256 * 2.0 ** -70).all() and (y[3, 128:] == 256 * 2.0 ** 70).all()
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    rest[1] = rest[3] = False
+    assert (y[rest, :128] == 256).all() and (y[rest, 128:] == float("inf")).all()
+
+
 # --- layer norm ------------------------------------------------------------------
 
 FAR = [1, 24, 128, 200, 520, 1000, 1001, 1024, 2561, 4096, 5120, 8192, 8200, 12288, 16383]
