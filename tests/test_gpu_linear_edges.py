@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from oracle import linear as OL
-from tests.test_gpu_linear_ops import TYPES, F, _close, _f64, _product, _randn, _run, bl, built  # noqa: F401
+from tests.test_gpu_linear_ops import (TYPES, F, _close, _f64, _norm_inputs, _product, _randn, _run,  # noqa: F401
+                                       bl, built)
 
 pytestmark = pytest.mark.gpu
 
@@ -163,6 +164,42 @@ def test_layer_norm_of_rows_that_begin_with_outliers(bl, cols, dtype):  # noqa: 
         _close(rstd[rows], rs[rows], 1600 * F * rs[rows], torch.float32)
         off = (64 * F * np.abs(xv).mean(1, keepdims=True) + 2 * F * np.abs(xv)) * rs[:, None]
         _close(y, ry, off + 1600 * F * np.abs(ry), t)
+
+
+FORMS = [("fp16", "fp16", None, 0), ("fp16", "fp32", None, 0), ("bf16", "bf16", None, 0),
+         ("bf16", "bf16", "int8", 32), ("bf16", "fp32", "e4m3", 64), ("bf16", "bf16", "int8", 0),
+         ("fp16", "fp16", "e4m3", 32), ("fp16", "fp32", "int8", 64), ("fp16", "fp16", "e4m3", 0),
+         ("fp32", "fp32", "int8", 32), ("fp32", "fp32", "e4m3", 0), ("fp16", "fp32", "int8", 128)]
+
+
+@pytest.mark.parametrize("dtype,wtype,saved,group", FORMS)
+@pytest.mark.parametrize("rows,cols", [(3, 7), (33, 128), (40, 264), (9, 520), (5, 1001), (300, 1024), (5, 2561),
+                                       (1200, 4096), (4, 5120), (3, 8200), (2, 16384)])
+def test_layer_norm_backward_of_other_forms(bl, rows, cols, dtype, wtype, saved, group):  # noqa: F811
+    """fp16, weights of 16 bits, and 8 bits with groups of 32 and 64 and with a scale a row."""
+    t, wt = TYPES[dtype], TYPES[wtype]
+    x, _, w, _ = _norm_inputs(rows, cols, t, wt, seed=cols + 3)
+    _, _, mean, rstd = bl.layer_norm_fwd(x, None, None)
+    h, hv = x, _f64(x)
+    if saved is not None:
+        h = bl.act_save(x, saved, group)
+        hv = _f64(h.codes.float()) * np.repeat(_f64(h.scales).reshape(rows, -1), group or cols, 1)[:, :cols]
+    g, gh = _randn(rows, cols, dtype=t, seed=8), _randn(rows, cols, dtype=t, seed=9)
+    for g_h in (gh, None):
+        gx, gw, gb = bl.layer_norm_bwd(g, h, mean, rstd, w, g_h=g_h)
+        rx, rw, rb = OL.layer_norm_backward(g, hv, mean, rstd, w, g_h)
+        s = _f64(rstd)[:, None]
+        u = np.abs((hv - _f64(mean)[:, None]) * s)
+        du = 3 * F * u
+        gv = np.abs(_f64(g))
+        wg = gv * np.abs(_f64(w))
+        c, dc = (wg * u).mean(1, keepdims=True), (wg * du).mean(1, keepdims=True)
+        terms = s * (wg + wg.mean(1, keepdims=True) + u * c)
+        slack = 64 * F * terms + s * (du * c + u * dc + du * dc)
+        _close(gx, rx, slack if g_h is None else slack + F * np.abs(_f64(g_h)), t)
+        assert gw.dtype == wt and gb.dtype == wt
+        _close(gw, rw, (rows + 64) * F * (gv * u).sum(0) + (gv * du).sum(0), wt)
+        _close(gb, rb, (rows + 64) * F * gv.sum(0), wt)
 
 
 # --- dropout ---------------------------------------------------------------------
