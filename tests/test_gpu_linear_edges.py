@@ -8,7 +8,7 @@ import torch
 
 from oracle import linear as OL
 from tests.test_gpu_linear_ops import (TYPES, F, _close, _f64, _norm_inputs, _product, _randn, _run,  # noqa: F401
-                                       bl, built)
+                                       _state, bl, built)
 
 pytestmark = pytest.mark.gpu
 
@@ -284,3 +284,21 @@ def test_a_state_that_went_on_is_not_read_by_a_backward(bl):  # noqa: F811
     with torch.inference_mode():
         state = torch.tensor([4, 7], device="cuda")
         assert bl.dropout_next(state).tolist() == [4, 7] and state.tolist() == [4, 8]
+
+
+def test_dropout_past_the_counter_s_upper_word(bl):  # noqa: F811
+    """Elements on either side of 2^34, where the counter of four elements passes 32 bits: in place
+    on a dense tensor, and element by element on one that starts at an odd place."""
+    from block_sparse_attention_fwd_gb300 import linear
+    n, st = 2 ** 34 + 43, _state(3, 4)
+    buf = torch.empty(n + 1, dtype=torch.bfloat16, device="cuda")
+    places = (0, 2 ** 32 - 20, 2 ** 33 - 20, 2 ** 34 - 60, 2 ** 34 - 20, n - 48)
+    for off in (0, 1):
+        buf.fill_(1.0)
+        x = buf[off:off + n]
+        linear._launch("bl_dropout", x.device, 1, n, 0, x.data_ptr(), n, None, n, 0.5, st.data_ptr(),
+                       x.data_ptr())
+        for at in places:
+            keep = OL.kept(48, 0.5, 3, 4, first=at)
+            assert (_f64(x[at:at + 48])[:n - at] == np.where(keep, 2.0, 0.0)[:n - at]).all(), (off, at)
+        assert float(buf[n - off * n]) == 1.0            # the neighbour stays
