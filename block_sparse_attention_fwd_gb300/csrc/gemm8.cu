@@ -24,7 +24,6 @@
 // instructions for two elements of a product instead of one.  Few rows: 8 x 16384 x 16384 in
 // 45 us, the weight at 5.9 TB/s; a call of 8 x 5120 x 5120 takes 10.8, of which 4 are the
 // launch and the sum over the cluster.
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -660,18 +659,6 @@ __global__ void __launch_bounds__(GCfg<BN, COL>::THREADS, GCfg<BN, COL>::CTAS)
   if (warp == 1) tmem_free(tmem, C::COLS);
 }
 
-template <auto* KERNEL>
-cudaError_t allow(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-  return e;
-}
-
 template <int BN, bool COL, typename T>
 cudaError_t launch(const Gemm8& g, cudaStream_t st) {
   using C = GCfg<BN, COL>;
@@ -685,7 +672,7 @@ cudaError_t launch(const Gemm8& g, cudaStream_t st) {
       !make_codes_map(&tb, g.b, g.b_mn ? g.n : g.k, g.b_mn ? g.k : g.n, g.b_pitch, box_b))
     return cudaErrorInvalidValue;
   constexpr auto* k = gemm8_kernel<BN, COL, T>;
-  cudaError_t e = allow<k>(C::SMEM);
+  cudaError_t e = allow_smem<k>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + BN - 1) / BN);
   const int64_t most = kSMs * C::CTAS;

@@ -189,7 +189,7 @@ cudaError_t rows_of(const NormBwd& a, int* blocks, cudaStream_t st) {
     const size_t smem = (size_t)3 * N * p.threads * ((GH ? 2 : 1) * sizeof(Chunk<T>) +
                                                      (FMT ? 8 : sizeof(Chunk<T>)));
     if (smem > kMaxSmem) return;
-    e = allow_smem<k>();
+    e = allow_smem<k>((int)kMaxSmem);
     if (e != cudaSuccess) return;
     *blocks = (int)grid(a.rows, 1, resident(p.threads, N == 1 ? 72 : 96, smem));
     k<<<*blocks, p.threads, smem, st>>>(a);

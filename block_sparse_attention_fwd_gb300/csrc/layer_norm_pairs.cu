@@ -245,7 +245,7 @@ cudaError_t pairs_of(const NormFwd& a, cudaStream_t st) {
     constexpr int RB = FMT8 && N == 2 ? 1 : 2;
     constexpr auto* k = layer_norm_pair_kernel<T, N, RB, FMT8, RES, decltype(full)::value != 0>;
     const size_t smem = 2 * RB * (RES ? 2 : 1) * row;
-    e = allow_smem<k>();
+    e = allow_smem<k>((int)kMaxSmem);
     if (e != cudaSuccess) return;
     const int64_t pairs = (a.rows + RB - 1) / RB;
     k<<<grid(pairs, 1, fwd_blocks(pairs, p, pair_regs(N), smem)), p.threads, smem, st>>>(a);

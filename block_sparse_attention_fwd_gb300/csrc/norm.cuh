@@ -21,7 +21,6 @@
 // share: how rows are laid over threads, and how launches are sized.
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -256,20 +255,6 @@ void with_plan(const Plan& p, F&& f) {
   else if (p.nv == 1) f(Int<0>(), Int<1>());
   else if (p.nv == 2) f(Int<0>(), Int<2>());
   else f(Int<0>(), Int<4>());
-}
-
-// Raises a kernel's limit of dynamic shared memory, once a device.
-template <auto* KERNEL>
-cudaError_t allow_smem() {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kMaxSmem);
-  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-  return e;
 }
 
 }  // namespace norm

@@ -341,7 +341,7 @@ cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
         }
         *blocks = (int)grid(a.rows, p.here,
                             resident(p.threads, bwd_regs(L, N, ODD && CB != 16, LN), smem));
-        e = allow_smem<k>();
+        e = allow_smem<k>((int)kMaxSmem);
         if (e != cudaSuccess) return;
         k<<<*blocks, p.threads, smem, st>>>(a);
         e = cudaGetLastError();

@@ -310,7 +310,7 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
         constexpr int S = decltype(stages)::value;
         constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM, ODD, LN>;
         const size_t smem = S * stage;
-        e = allow_smem<k>();
+        e = allow_smem<k>((int)kMaxSmem);
         if (e != cudaSuccess) return;
         k<<<grid(a.rows, p.here, fwd_blocks(a.rows, p, fwd_regs(LN, NORM, N), smem)), p.threads, smem,
             st>>>(a);

@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace bl {
@@ -503,6 +505,19 @@ __device__ __forceinline__ void load_bias8(const void* b, bool f32, int64_t col,
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 0.f;
   }
+}
+
+// Raises a kernel's limit of dynamic shared memory, once a device.
+template <auto* KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return e;
 }
 
 inline __host__ __device__ bool aligned_to(const void* p, size_t a) {

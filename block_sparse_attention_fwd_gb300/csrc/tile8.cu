@@ -11,7 +11,6 @@
 // kept it as 64 fp32 numbers a thread, two blocks fit an SM: 16384 x 4096 bf16 to rows
 // and columns in 74 us, 53 so: 75% of the copy rate, the issue slots 75% busy; rows or
 // columns alone 89 and 84%, a weight's blocks 83%).
-#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -193,19 +192,6 @@ __global__ void __launch_bounds__(256) repitch_kernel(Repitch a, Repitch b) {
   }
 }
 
-// Raises a kernel's limit of dynamic shared memory, once a device.
-template <auto* KERNEL>
-cudaError_t allow(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-  return e;
-}
-
 }  // namespace
 
 cudaError_t launch_repitch(const Repitch& a, const Repitch& b, cudaStream_t st) {
@@ -229,7 +215,7 @@ cudaError_t launch_tile_save(int dtype, const TileSave& a, cudaStream_t st) {
     constexpr int smem = 128 * 128 * (int)sizeof(T);
     auto go = [&](auto v, auto w) {
       constexpr auto* k = tile_save_kernel<T, decltype(v)::value, decltype(w)::value>;
-      const cudaError_t e = allow<k>(smem);
+      const cudaError_t e = allow_smem<k>(smem);
       if (e != cudaSuccess) return e;
       k<<<g, 256, smem, st>>>(a);
       return cudaGetLastError();
