@@ -197,6 +197,11 @@ inline Plan plan(int64_t cols, int max_threads, int warp_chunks, bool odd = fals
   return p;
 }
 
+// The fewest threads of such a block with nv chunks each, two or four.
+constexpr int fewest_threads(int nv, int max_threads) {
+  return ((nv == 4 ? 2 * max_threads : 128) / nv + 32) / 32 * 32;
+}
+
 constexpr int kSMs = 152;
 constexpr size_t kMaxSmem = 220 * 1024;
 

@@ -330,8 +330,11 @@ cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
     constexpr int CB = (int)sizeof(Chunk<T>);
     // fp32 that a warp holds: 4-byte copies cost more than the ring gains (129
     // columns: 72% of the copy rate straight from global memory, 29% so)
-    if constexpr (!(ODD && CB != 16 && L != 0)) {
-      const size_t stage = (size_t)N * p.threads * (2 * CB + (FMT ? 12 : CB));
+    constexpr size_t UNIT = (size_t)N * (2 * CB + (FMT ? 12 : CB));    // a thread's of a stage
+    // layer_bwd_rows takes aligned rows of up to two chunks a thread wherever three stages fit
+    constexpr bool REST = LN && !ODD && L == 0 && N <= 2;
+    if constexpr (!(ODD && CB != 16 && L != 0) && !(REST && (N == 1 || CB == 16 || FMT != 0))) {
+      const size_t stage = p.threads * UNIT;
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
         constexpr auto* k = norm_bwd_ring_kernel<T, L, N, FMT, S, ODD, LN>;
@@ -347,11 +350,12 @@ cudaError_t bwd_ring(const NormBwd& a, int* blocks, cudaStream_t st) {
         e = cudaGetLastError();
       };
       constexpr int MOST = N == 4 ? 2 : 3;               // stages
-      if (MOST * stage <= kMaxSmem) {
-        ring(Int<MOST>());
-        return;
-      }
-      if constexpr (L == 0 && N == 2)
+      if constexpr (!REST)
+        if (MOST * stage <= kMaxSmem) {
+          ring(Int<MOST>());
+          return;
+        }
+      if constexpr (L == 0 && N == 2 && MOST * UNIT * 512 > kMaxSmem)
         if (2 * stage <= kMaxSmem) ring(Int<2>());
     }
   });

@@ -304,8 +304,11 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
   if (p.threads > fwd_threads(LN)) return e;
   with_plan(p, [&](auto lpr, auto nv) {
     constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-    if constexpr (N <= 2 || (LN && L == 0)) {
-      const size_t stage = (size_t)N * p.threads * (NORM ? 2 : 1) * sizeof(Chunk<T>);
+    // layer_fwd_pairs takes aligned rows of one chunk a thread, but for a scale a row
+    constexpr bool PAIRS = LN && !ODD && FMT8 == 0 && L == 0 && N == 1;
+    if constexpr ((N <= 2 || (LN && L == 0)) && !PAIRS) {
+      constexpr size_t UNIT = (size_t)N * (NORM ? 2 : 1) * sizeof(Chunk<T>);  // a thread's of a stage
+      const size_t stage = p.threads * UNIT;
       auto ring = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
         constexpr auto* k = norm_fwd_ring_kernel<T, L, N, FMT8, S, NORM, ODD, LN>;
@@ -316,11 +319,17 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
             st>>>(a);
         e = cudaGetLastError();
       };
-      constexpr int MOST = NORM || ODD ? 3 : 2;
-      if (L != 0 || N == 1 || MOST * stage <= kMaxSmem / 2)
+      constexpr int MOST = NORM || ODD ? 3 : 2, TOP = fwd_threads(LN);
+      if constexpr (L != 0 || N == 1 || MOST * UNIT * TOP <= kMaxSmem / 2) {
         ring(Int<MOST>());
-      else if (2 * stage <= kMaxSmem)
-        ring(Int<L == 0 && N >= 2 ? 2 : MOST>());
+      } else {
+        if constexpr (MOST * UNIT * fewest_threads(N, TOP) <= kMaxSmem / 2)
+          if (MOST * stage <= kMaxSmem / 2) {
+            ring(Int<MOST>());
+            return;
+          }
+        if (2 * stage <= kMaxSmem) ring(Int<2>());
+      }
     }
   });
   return e;
@@ -444,8 +453,8 @@ cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
     if (vec) e = layer_fwd_pairs(dtype, a, st);
   if (e != cudaErrorNotSupported) return e;
   e = vec  ? fwd_ring<T, FMT8, true, false, LN>(a, st)
-                  : LN ? layer_fwd_odd(dtype, a, st)
-                       : fwd_odd(dtype, true, a, st);
+      : LN ? layer_fwd_odd(dtype, a, st)
+           : fwd_odd(dtype, true, a, st);
   if (e != cudaErrorNotSupported) return e;
   const Plan p = plan(a.cols, fwd_threads(LN), 64);
   const unsigned g = grid(a.rows, p.here, kSMs * 32);
@@ -475,8 +484,8 @@ cudaError_t launch_fwd_of(int dtype, const NormFwd& in, cudaStream_t st) {
     const size_t al = chunk_align(dtype);
     const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
                      aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.h, al) &&
-                     aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) && aligned_to(a.b, a.w_f32 ? 32 : 16) &&
-                     aligned_to(a.codes, 8);
+                     aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) &&
+                     aligned_to(a.b, a.w_f32 ? 32 : 16) && aligned_to(a.codes, 8);
     const int fmt = a.codes ? a.fmt : 0;
     return fmt == 0          ? fwd<T, 0, LN>(dtype, a, vec, st)
            : fmt == kFmtInt8 ? fwd<T, kFmtInt8, LN>(dtype, a, vec, st)
