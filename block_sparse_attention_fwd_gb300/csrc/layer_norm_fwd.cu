@@ -3,7 +3,7 @@
 
 namespace bl {
 
-cudaError_t launch_layer_norm_fwd(int dtype, const NormFwd& a, cudaStream_t st) {
+cudaError_t launch_layer_norm_fwd(int dtype, const LayerNormFwd& a, cudaStream_t st) {
   return launch_fwd_of<true>(dtype, a, st);
 }
 

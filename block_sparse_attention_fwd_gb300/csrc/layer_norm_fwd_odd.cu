@@ -5,7 +5,7 @@ namespace bl {
 
 namespace norm {
 
-cudaError_t layer_fwd_odd(int dtype, const NormFwd& a, cudaStream_t st) {
+cudaError_t layer_fwd_odd(int dtype, const LayerNormFwd& a, cudaStream_t st) {
   if (dtype > 1) return cudaErrorNotSupported;       // fp32
   const int fmt = a.codes ? a.fmt : 0;
   auto launch = [&](auto* z) {

@@ -28,7 +28,7 @@ constexpr int pair_regs(int nv) { return nv == 1 ? 64 : 96; }
 // FULL: every thread has all of its chunks.
 template <typename T, int NV, int RB, int FMT8, bool RES, bool FULL>
 __global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV))
-    layer_norm_pair_kernel(NormFwd a) {
+    layer_norm_pair_kernel(LayerNormFwd a) {
   constexpr int CB = (int)sizeof(Chunk<T>), TENSORS = RES ? 2 : 1;
   __shared__ float2 buf[2][RB][16];
   extern __shared__ __align__(16) uint8_t ring[];
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(512) __maxnreg__(pair_regs(NV))
 
 // Launches the kernel of pairs of rows on rows that it takes, else cudaErrorNotSupported.
 template <typename T, int FMT8>
-cudaError_t pairs_of(const NormFwd& a, cudaStream_t st) {
+cudaError_t pairs_of(const LayerNormFwd& a, cudaStream_t st) {
   const Plan p = plan(a.cols, 512, 64);
   cudaError_t e = cudaErrorNotSupported;
   if (p.lpr || p.nv > 2 || p.threads > 512 || (FMT8 && !a.group)) return e;
@@ -266,7 +266,7 @@ cudaError_t pairs_of(const NormFwd& a, cudaStream_t st) {
 
 namespace norm {
 
-cudaError_t layer_fwd_pairs(int dtype, const NormFwd& a, cudaStream_t st) {
+cudaError_t layer_fwd_pairs(int dtype, const LayerNormFwd& a, cudaStream_t st) {
   const int fmt = a.codes ? a.fmt : 0;
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;

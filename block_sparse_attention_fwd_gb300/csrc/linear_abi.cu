@@ -174,7 +174,7 @@ bl_status bl_layer_norm_fwd(const bl_layer_norm_args* p, void* stream) {
       (p->bias && !elem_ok(p->bias, p->weight_dtype)))
     return BL_ERR_INVALID_ARG;
   if (cols > BL_NORM_MAX_COLS) return BL_ERR_UNSUPPORTED;
-  bl::NormFwd a{};
+  bl::LayerNormFwd a{};
   a.rows = rows; a.cols = cols;
   a.x_stride = p->x_stride; a.r_stride = p->residual ? p->residual_stride : 0;
   a.x = p->x; a.r = p->residual; a.w = p->weight; a.b = p->bias;

@@ -239,11 +239,11 @@ inline int fwd_blocks(int64_t rows, const Plan& p, int regs, size_t smem) {
 cudaError_t fwd_odd(int dtype, bool norm, const NormFwd& a, cudaStream_t st);
 cudaError_t bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 // The layer norm's.
-cudaError_t layer_fwd_odd(int dtype, const NormFwd& a, cudaStream_t st);
+cudaError_t layer_fwd_odd(int dtype, const LayerNormFwd& a, cudaStream_t st);
 // The layer norm's forward, two rows at a time (layer_norm_pairs.cu), where it takes the
 // rows: whole aligned chunks, held by a block with two chunks a thread at most, and no
 // scale a row.
-cudaError_t layer_fwd_pairs(int dtype, const NormFwd& a, cudaStream_t st);
+cudaError_t layer_fwd_pairs(int dtype, const LayerNormFwd& a, cudaStream_t st);
 // Its backward on such rows (layer_norm_bwd_rows.cu).
 cudaError_t layer_bwd_rows(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);
 cudaError_t layer_bwd_odd(int dtype, const NormBwd& a, int* blocks, cudaStream_t st);

@@ -12,6 +12,8 @@ namespace {
 // Threads of a block that holds a row, at most.  The layer norm, which keeps the bias too,
 // needs more than the 64 registers that 1024 threads leave each.
 constexpr int fwd_threads(bool layer) { return layer ? 512 : 1024; }
+template <bool LN>
+using FwdArgs = std::conditional_t<LN, LayerNormFwd, NormFwd>;
 // Registers a thread (the launch counts on them).
 constexpr int fwd_regs(bool layer, bool norm, int nv) {
   return !layer ? (norm ? 64 : 48) : nv == 1 ? 64 : nv == 2 ? 80 : 128;
@@ -30,10 +32,13 @@ constexpr int fwd_regs(bool layer, bool norm, int nv) {
 // the ring, and a chunk is shifted out of its own and the next thread's vector:
 // one barrier more, and some 40 instructions a chunk and tensor (2561 columns: 23%
 // of the copy rate element by element, 50% so, 63% with a residual).
+// Registers are bounded by the numbers of threads alone (768 for 80 of them, where a thread has
+// two chunks of rows that start anywhere): under __maxnreg__, even with the same bound, the
+// kernels take more of them and spill (layer norm of 32760 x 2561 bf16 with a residual: 225 us,
+// 199 so).
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
-    __maxnreg__(LN && ODD && NV == 2 ? 80 : LPR ? 255 : 65536 / fwd_threads(LN))
-    norm_fwd_ring_kernel(NormFwd a) {
+__global__ void __launch_bounds__(LPR ? 256 : LN && ODD && NV == 2 ? 768 : fwd_threads(LN))
+    norm_fwd_ring_kernel(FwdArgs<LN> a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
   static_assert(NORM || !LN);
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
 
 // Launches the ring kernel on rows that it takes, else cudaErrorNotSupported.
 template <typename T, int FMT8, bool NORM, bool ODD, bool LN>
-cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
+cudaError_t fwd_ring(const FwdArgs<LN>& a, cudaStream_t st) {
   const Plan p = plan(a.cols, fwd_threads(LN), 64, ODD);
   cudaError_t e = cudaErrorNotSupported;
   if (p.threads > fwd_threads(LN)) return e;
@@ -339,8 +344,10 @@ cudaError_t fwd_ring(const NormFwd& a, cudaStream_t st) {
 // anywhere or is too wide, and 16-bit rows that start anywhere of more than 16376
 // columns.  OUT8: with the 8-bit output, whose
 // groups are neighbours, so those rows keep to chunks.
+// (Arguments that are not marked constant cost registers: fp32 of 2561 columns 155 us, 144 so.)
 template <typename T, int LPR, int NV, bool VEC, bool OUT8, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN))
+    norm_fwd_kernel(const __grid_constant__ FwdArgs<LN> a) {
   __shared__ float buf[2][32];
   constexpr bool SPREAD = !VEC && !OUT8;
   const Rows<LPR> R;
@@ -447,14 +454,14 @@ __global__ void __launch_bounds__(LPR ? 256 : fwd_threads(LN)) norm_fwd_kernel(N
 }
 
 template <typename T, int FMT8, bool LN>
-cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
+cudaError_t fwd(int dtype, const FwdArgs<LN>& a, bool vec, cudaStream_t st) {
   cudaError_t e = cudaErrorNotSupported;
-  if constexpr (LN)
-    if (vec) e = layer_fwd_pairs(dtype, a, st);
-  if (e != cudaErrorNotSupported) return e;
-  e = vec  ? fwd_ring<T, FMT8, true, false, LN>(a, st)
-      : LN ? layer_fwd_odd(dtype, a, st)
-           : fwd_odd(dtype, true, a, st);
+  if constexpr (LN) {
+    e = vec ? layer_fwd_pairs(dtype, a, st) : layer_fwd_odd(dtype, a, st);
+  } else {
+    if (!vec) e = fwd_odd(dtype, true, a, st);
+  }
+  if (vec && e == cudaErrorNotSupported) e = fwd_ring<T, FMT8, true, false, LN>(a, st);
   if (e != cudaErrorNotSupported) return e;
   const Plan p = plan(a.cols, fwd_threads(LN), 64);
   const unsigned g = grid(a.rows, p.here, kSMs * 32);
@@ -475,17 +482,17 @@ cudaError_t fwd(int dtype, const NormFwd& a, bool vec, cudaStream_t st) {
 
 // The forward's launch on rows of any kind.
 template <bool LN>
-cudaError_t launch_fwd_of(int dtype, const NormFwd& in, cudaStream_t st) {
-  NormFwd a = in;
+cudaError_t launch_fwd_of(int dtype, const FwdArgs<LN>& in, cudaStream_t st) {
+  FwdArgs<LN> a = in;
   if (a.rows == 0) return cudaSuccess;
   a.shift = group_shift(a.group);
   return with_type(dtype, [&](auto* z) {
     using T = std::remove_pointer_t<decltype(z)>;
     const size_t al = chunk_align(dtype);
-    const bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
-                     aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.h, al) &&
-                     aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) &&
-                     aligned_to(a.b, a.w_f32 ? 32 : 16) && aligned_to(a.codes, 8);
+    bool vec = a.cols % 8 == 0 && a.x_stride % 8 == 0 && a.r_stride % 8 == 0 &&
+               aligned_to(a.x, al) && aligned_to(a.r, al) && aligned_to(a.h, al) &&
+               aligned_to(a.y, al) && aligned_to(a.w, a.w_f32 ? 32 : 16) && aligned_to(a.codes, 8);
+    if constexpr (LN) vec = vec && aligned_to(a.b, a.w_f32 ? 32 : 16);
     const int fmt = a.codes ? a.fmt : 0;
     return fmt == 0          ? fwd<T, 0, LN>(dtype, a, vec, st)
            : fmt == kFmtInt8 ? fwd<T, kFmtInt8, LN>(dtype, a, vec, st)
