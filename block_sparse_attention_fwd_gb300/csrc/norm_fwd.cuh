@@ -37,7 +37,7 @@ constexpr int fwd_regs(bool layer, bool norm, int nv) {
 // kernels take more of them and spill (layer norm of 32760 x 2561 bf16 with a residual: 225 us,
 // 199 so).
 template <typename T, int LPR, int NV, int FMT8, int S, bool NORM, bool ODD, bool LN>
-__global__ void __launch_bounds__(LPR ? 256 : LN && ODD && NV == 2 ? 768 : fwd_threads(LN))
+__global__ void __launch_bounds__(LN && ODD && NV == 2 ? 768 : LPR ? 256 : fwd_threads(LN))
     norm_fwd_ring_kernel(FwdArgs<LN> a) {
   constexpr int CB = (int)sizeof(Chunk<T>);          // bytes of a chunk
   static_assert(!ODD || CB == 16);
