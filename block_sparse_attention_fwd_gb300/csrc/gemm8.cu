@@ -20,10 +20,11 @@
 //
 // 8192^3 in 409 us, 2.69 PFLOP/s (1.4 times the measured bf16 rate of the tensor cores), in
 // bursts; run for seconds the GPU's power is the bound (2.3 PFLOP/s at 1390 W and 1810 MHz,
-// the tensor cores 57% busy).  With a scale a column, g_w, 590 us: two packed fp32
-// instructions for two elements of a product instead of one.  Few rows: 8 x 16384 x 16384 in
-// 45 us, the weight at 5.9 TB/s; a call of 8 x 5120 x 5120 takes 10.8, of which 4 are the
-// launch and the sum over the cluster.
+// the tensor cores 57% busy).  With a scale a column, g_w, 590 us, of which two packed fp32
+// instructions for two elements of a product instead of one are some 310; no pipe is more than
+// 52% busy (the warps' largest stalls are fixed latencies and reads of TMEM).  Few rows:
+// 8 x 16384 x 16384 in 45 us, the weight at 5.9 TB/s; a call of 8 x 5120 x 5120 takes 11, of
+// which 4 are the launch and the sum over the cluster.
 #include <type_traits>
 
 #include "common.cuh"

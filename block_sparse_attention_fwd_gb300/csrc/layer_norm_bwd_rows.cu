@@ -9,8 +9,8 @@ namespace {
 
 // As norm_bwd_ring_kernel (norm_bwd.cuh), with fewer registers and instructions, which is
 // what bounds the layer norm there: the sums of g_b and the mean take 128 registers, one
-// block of 320 threads an SM (32760 x 5120 bf16 with g_h: 241 us; 196 so, 101% of the copy
-// rate).  Pointers walk with the
+// block of 320 threads an SM (32760 x 5120 bf16 with g_h: 241 us; 193 so, 102% of the copy
+// rate; from int8 247, 70%).  Pointers walk with the
 // rows, FULL (every thread has all of its chunks) needs no predicates, and u is formed
 // again from the ring behind the row's sums instead of being kept.
 template <typename T, int NV, int FMT, bool GH, bool FULL>

@@ -16,7 +16,7 @@ constexpr int pair_regs(int nv) { return nv == 1 ? 64 : 96; }
 // The layer norm of rows that a block holds, whose chunks are whole and aligned: two rows
 // at a time.  One row's sums are a chain of shuffles and a barrier that the few blocks that
 // fit beside weight and bias in registers do not hide (32760 x 5120 bf16: 143 us a row at a
-// time, 102 so, 97% of the copy rate; with the residual 196, 101%; to e4m3 181, 96%).  A
+// time, 102 so, 97% of the copy rate; with the residual 197, 100%; to e4m3 182, 95%).  A
 // row's mean and squares come from one round of shuffles: each warp sums
 // distances from the mean of its first lane's elements, and the squares around its own mean
 // follow by sum d^2 - (sum d)^2 / n.  With a pivot p that is the mean of k of the n elements,

@@ -51,7 +51,7 @@ struct Rows {
 // The 8 elements of a row that a thread has in its unit k.  Chunks: 8 neighbours.
 // SPREAD: R.step apart, so that the lanes of an access have neighbouring elements:
 // for rows that start anywhere, where a chunk would take 8 accesses that each
-// touch a sector a lane.  fp32, 32760 x 2561: forward 45 -> 64% of the copy rate, 83%
+// touch a sector a lane.  fp32, 32760 x 2561: forward 45 -> 68% of the copy rate, 87%
 // with a residual; straight from global memory, as 4-byte copies to the ring wait
 // on their own number (54 and 52%).  Backward 63% on the ring, 33% without.
 template <bool SPREAD, int LPR>

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(256) tile_save_kernel(TileSave a) {
   }
 }
 
+// (16384 x 4096 bf16: columns' groups 70 us, 43% of the copy rate, blocks 66 us.)
 // Values of codes [rows, cols] whose scale lies at scales[(row / 128) * s_row + (col >> shift)
 // * s_col]: columns' groups (shift 0) or blocks (7).
 template <typename T, bool VEC>
