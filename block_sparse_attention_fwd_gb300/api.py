@@ -415,6 +415,8 @@ class BLDropout(torch.nn.Module):
                     "a forward that a backward runs again needs the state of its first run: "
                     "draw used = dropout_next(drop.state) outside and call drop(x, used=used)")
             used = linear.dropout_next(self.state)
+        elif not isinstance(used, torch.Tensor):
+            raise TypeError("used must be a tensor, the state that dropout_next gave")
         elif used.data_ptr() == self.state.data_ptr():
             raise ValueError("used is the state that goes on: pass dropout_next(drop.state)")
         x, residual = (t if t is None or ops.row_stride(t) is not None else t.contiguous()

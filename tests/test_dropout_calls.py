@@ -68,6 +68,8 @@ def test_a_call_may_not_take_the_state_that_goes_on():
     drop = api.BLDropout(0.5, seed=3, device="cpu")
     with pytest.raises(ValueError):
         drop(torch.ones(4), used=drop.state)
+    with pytest.raises(TypeError):
+        drop(torch.ones(4), used=7)
     y = drop(torch.ones(40), used=torch.tensor([3, 7]))
     assert torch.equal(y != 0, torch.from_numpy(OL.kept(40, 0.5, 3, 7))) and drop.state.tolist() == [3, 0]
 
